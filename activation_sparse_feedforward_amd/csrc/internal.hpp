@@ -163,6 +163,54 @@ struct BwdArgs {
   int64_t blk0;          // and the first row block of this launch
 };
 
+// Laid-out weights (few_token.hpp): E matrices of N rows x K inputs.
+struct WeightsArgs {
+  const void* w;     // packing: the matrices
+  void* out;         // unpacking: the matrices
+  uint8_t* codes;
+  uint16_t* scales;  // not used for 16 bits
+  int32_t experts, N, K, bits, group;
+  int32_t tiles, blocks;  // ceil(N / 16), ceil(K / 128)
+};
+
+// y [T x N] = x [T x K] . W^T with 4-bit weights.
+struct LinearArgs {
+  const void* x;
+  void* y;
+  const uint8_t* codes;
+  const uint16_t* scales;
+  int64_t T, ldx, ldy;
+  int32_t N, K, group, tiles, blocks;
+};
+
+// Mixture of experts for at most kMoeBlockTokens tokens at a time (the router
+// takes any number).
+constexpr int kMoeBlockTokens = 64;
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxTopK = 32;
+struct MoeChosen {
+  int32_t expert, first, n, pad;  // its entries in the pair list
+};
+struct MoeArgs {
+  const void* x;
+  void* y;
+  const void* router;  // [E x d]
+  const float* bias;   // [E] or null
+  int32_t* ids;        // [T x k]
+  float* weights;      // [T x k]
+  const uint8_t *gate_codes, *up_codes, *down_codes;
+  const uint16_t *gate_scales, *up_scales, *down_scales;
+  int64_t ldx, ldy;
+  int32_t T, E, k, d, f, bits, group, act, renorm;
+  int32_t tiles_f, blocks_d, tiles_d, blocks_f, most_chosen;
+  // workspace
+  uint16_t* h;         // [planes][T * k][blocks_f * 128] hidden values of each (token, choice) pair
+  int64_t h_plane, h_row;
+  int32_t* n_chosen;   // experts with a token
+  MoeChosen* chosen;   // [most_chosen], ascending experts
+  int32_t* pairs;      // [T * k] (token, choice) pairs by expert
+};
+
 // dtype: 0 = fp32, 1 = bf16.  Each returns hipSuccess or the launch error.
 hipError_t launch_gate_pack(const PackArgs& a, int dtype, hipStream_t s);
 hipError_t launch_fused_updown(const FusedArgs& a, int dtype, hipStream_t s);
@@ -183,6 +231,11 @@ hipError_t launch_splitk_reduce(const float* part, int splits, int64_t M, const 
                                 const int32_t* rows, void* out, int d, int dtype, hipStream_t s);
 hipError_t launch_bwd_sparse(const BwdArgs& a, int dtype, hipStream_t s);
 hipError_t launch_bwd_dense(const BwdArgs& a, int dtype, hipStream_t s);
+hipError_t launch_weights_pack(const WeightsArgs& a, int dtype, bool transposed, hipStream_t s);
+hipError_t launch_weights_unpack(const WeightsArgs& a, int dtype, hipStream_t s);
+hipError_t launch_linear4(const LinearArgs& a, int dtype, hipStream_t s);
+hipError_t launch_moe_route(const MoeArgs& a, int64_t T, int dtype, hipStream_t s);
+hipError_t launch_moe_experts(const MoeArgs& a, int dtype, hipStream_t s);
 
 // Lockstep launches: how many workgroups of one lockstep kernel (one per CU)
 // the current device runs at once; 0 if it cannot be queried.

@@ -136,6 +136,85 @@ BwdWs bwd_ws(const twell_desc* d, int64_t max_dense_rows) {
 
 twell_status from_hip(hipError_t e) { return e == hipSuccess ? TWELL_OK : TWELL_EHIP; }
 
+// ---------------------------------------------------------------- few-token products
+constexpr int32_t kMaxSide = 1 << 20;           // rows, inputs and tokens of the few-token products
+constexpr int64_t kMaxMatrix = int64_t(1) << 34;  // rows x inputs of one matrix
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+bool known_dtype(int32_t t) { return t == TWELL_FP32 || t == TWELL_BF16; }
+bool elem_aligned(const void* p, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == TWELL_BF16 ? 1u : 3u)) == 0;
+}
+int32_t tiles_of(int32_t rows) { return (rows + 15) / 16; }
+int32_t blocks_of(int32_t cols) { return (cols + 127) / 128; }
+
+twell_status check_wdesc(const twell_wdesc* d) {
+  if (!d || d->experts <= 0 || d->rows <= 0 || d->cols <= 0) return TWELL_EINVAL;
+  if (d->bits != 4 && d->bits != 16) return TWELL_EINVAL;
+  if (d->bits == 16 ? d->group != 0 : (d->group != 32 && d->group != 64 && d->group != 128)) return TWELL_EINVAL;
+  if (d->experts > twell::kMoeMaxExperts || d->rows > kMaxSide || d->cols > kMaxSide) return TWELL_EUNSUPPORTED;
+  if (static_cast<int64_t>(d->rows) * d->cols > kMaxMatrix) return TWELL_EUNSUPPORTED;
+  return TWELL_OK;
+}
+
+twell_status check_planes(const twell_wdesc* d, const twell_wplanes& p) {
+  if (!p.codes || !aligned16(p.codes)) return TWELL_EINVAL;
+  if (d->bits == 4 && (!p.scales || !aligned16(p.scales))) return TWELL_EINVAL;
+  return TWELL_OK;
+}
+
+twell::WeightsArgs weights_args(const twell_wdesc* d, const twell_wplanes& p) {
+  twell::WeightsArgs a{};
+  a.codes = static_cast<uint8_t*>(p.codes);
+  a.scales = static_cast<uint16_t*>(p.scales);
+  a.experts = d->experts;
+  a.N = d->rows;
+  a.K = d->cols;
+  a.bits = d->bits;
+  a.group = d->group;
+  a.tiles = tiles_of(d->rows);
+  a.blocks = blocks_of(d->cols);
+  return a;
+}
+
+twell_wdesc moe_in_desc(const twell_moe_desc* d) { return {d->experts, d->d_ff, d->d_model, d->bits, d->group}; }
+twell_wdesc moe_out_desc(const twell_moe_desc* d) { return {d->experts, d->d_model, d->d_ff, d->bits, d->group}; }
+
+twell_status check_moe(const twell_moe_desc* d) {
+  if (!d || d->T < 0 || d->top_k <= 0 || d->top_k > d->experts) return TWELL_EINVAL;
+  if (!known_dtype(d->dtype)) return TWELL_EINVAL;
+  if (d->act != TWELL_RELU && d->act != TWELL_SILU) return TWELL_EINVAL;
+  if (d->renorm != 0 && d->renorm != 1) return TWELL_EINVAL;
+  const twell_wdesc in = moe_in_desc(d);
+  TWELL_TRY(check_wdesc(&in));
+  if (d->ldx < d->d_model || d->ldy < d->d_model) return TWELL_EINVAL;
+  if (d->top_k > twell::kMoeMaxTopK || d->T > kMaxSide || d->ldx > kMaxStride || d->ldy > kMaxStride)
+    return TWELL_EUNSUPPORTED;
+  return TWELL_OK;
+}
+
+// Workspace of the mixture of experts: the hidden values of one block of
+// tokens, then the list of chosen experts and their pairs.
+struct MoeWs {
+  size_t h, n_chosen, chosen, pairs, total;
+  int64_t h_plane, h_row;
+  int32_t block_tokens;
+};
+MoeWs moe_ws(const twell_moe_desc* d) {
+  MoeWs w{};
+  w.block_tokens = static_cast<int32_t>(d->T < twell::kMoeBlockTokens ? d->T : twell::kMoeBlockTokens);
+  const int64_t pairs = static_cast<int64_t>(w.block_tokens) * d->top_k;
+  w.h_row = static_cast<int64_t>(blocks_of(d->d_ff)) * 128;
+  w.h_plane = pairs * w.h_row;
+  size_t o = 0;
+  w.h = o;        o += align256(static_cast<size_t>(w.h_plane) * 2 * (d->dtype == TWELL_BF16 ? 2 : 3));
+  w.n_chosen = o; o += 256;
+  w.chosen = o;   o += align256(static_cast<size_t>(d->experts) * sizeof(twell::MoeChosen));
+  w.pairs = o;    o += align256(static_cast<size_t>(pairs) * 4);
+  w.total = o;
+  return w;
+}
+
 }  // namespace
 
 namespace twell {
@@ -486,6 +565,137 @@ twell_status twell_dense_ffn_fwd(const twell_desc* d, const void* x, const void*
   dn.d = d->d_model;
   dn.F = d->d_ff;
   return from_hip(twell::launch_dense256(g, dn, d->dtype, s));
+}
+
+twell_status twell_weights_sizes(const twell_wdesc* d, twell_wsizes_t* out) {
+  TWELL_TRY(check_wdesc(d));
+  if (!out) return TWELL_EINVAL;
+  const size_t blocks = static_cast<size_t>(d->experts) * static_cast<size_t>(tiles_of(d->rows)) *
+                        static_cast<size_t>(blocks_of(d->cols));
+  out->codes = blocks * (d->bits == 4 ? 1024 : 4096);
+  out->scales = d->bits == 4 ? blocks * 16 * static_cast<size_t>(128 / d->group) * 2 : 0;
+  return TWELL_OK;
+}
+
+twell_status twell_weights_pack(const twell_wdesc* d, const void* w, int32_t w_dtype, int32_t transposed,
+                                twell_wplanes out, void* stream) {
+  TWELL_TRY(check_wdesc(d));
+  if (!known_dtype(w_dtype) || (transposed != 0 && transposed != 1)) return TWELL_EINVAL;
+  if (d->bits == 16 && w_dtype != TWELL_BF16) return TWELL_EUNSUPPORTED;  // would round
+  if (!w || !elem_aligned(w, w_dtype)) return TWELL_EINVAL;
+  TWELL_TRY(check_planes(d, out));
+  twell::WeightsArgs a = weights_args(d, out);
+  a.w = w;
+  return from_hip(twell::launch_weights_pack(a, w_dtype, transposed != 0, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_weights_unpack(const twell_wdesc* d, twell_wplanes in, void* w, int32_t w_dtype, void* stream) {
+  TWELL_TRY(check_wdesc(d));
+  if (!known_dtype(w_dtype)) return TWELL_EINVAL;
+  if (d->bits == 16 && w_dtype != TWELL_BF16) return TWELL_EUNSUPPORTED;
+  if (!w || !elem_aligned(w, w_dtype)) return TWELL_EINVAL;
+  TWELL_TRY(check_planes(d, in));
+  twell::WeightsArgs a = weights_args(d, in);
+  a.out = w;
+  return from_hip(twell::launch_weights_unpack(a, w_dtype, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_linear_fwd(const twell_wdesc* d, twell_wplanes w, int64_t T, int32_t dtype, const void* x,
+                              int64_t ldx, void* y, int64_t ldy, void* stream) {
+  TWELL_TRY(check_wdesc(d));
+  if (T < 0 || !known_dtype(dtype) || ldx < d->cols || ldy < d->rows) return TWELL_EINVAL;
+  if (d->experts != 1 || d->bits != 4 || T > kMaxSide || ldx > kMaxStride || ldy > kMaxStride)
+    return TWELL_EUNSUPPORTED;
+  if (T == 0) return TWELL_OK;
+  if (!x || !y || !elem_aligned(x, dtype) || !elem_aligned(y, dtype)) return TWELL_EINVAL;
+  TWELL_TRY(check_planes(d, w));
+  twell::LinearArgs a{};
+  a.x = x;
+  a.y = y;
+  a.codes = static_cast<const uint8_t*>(w.codes);
+  a.scales = static_cast<const uint16_t*>(w.scales);
+  a.T = T;
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.N = d->rows;
+  a.K = d->cols;
+  a.group = d->group;
+  a.tiles = tiles_of(d->rows);
+  a.blocks = blocks_of(d->cols);
+  return from_hip(twell::launch_linear4(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_moe_sizes(const twell_moe_desc* d, size_t* ws) {
+  TWELL_TRY(check_moe(d));
+  if (!ws) return TWELL_EINVAL;
+  *ws = moe_ws(d).total;
+  return TWELL_OK;
+}
+
+twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w_router, const float* router_bias,
+                           twell_wplanes gate, twell_wplanes up, twell_wplanes down, void* y, int32_t* ids,
+                           float* weights, void* ws, size_t ws_bytes, void* stream) {
+  TWELL_TRY(check_moe(d));
+  if (d->T == 0) return TWELL_OK;
+  if (!x || !w_router || !y || !ids || !weights) return TWELL_EINVAL;
+  if (!elem_aligned(x, d->dtype) || !elem_aligned(w_router, d->dtype) || !elem_aligned(y, d->dtype))
+    return TWELL_EINVAL;
+  if (!aligned4(ids) || !aligned4(weights) || (router_bias && !aligned4(router_bias))) return TWELL_EINVAL;
+  const twell_wdesc in = moe_in_desc(d);
+  TWELL_TRY(check_planes(&in, gate));
+  TWELL_TRY(check_planes(&in, up));
+  TWELL_TRY(check_planes(&in, down));
+  const MoeWs w = moe_ws(d);
+  if (!ws || !aligned16(ws) || ws_bytes < w.total) return TWELL_EINVAL;
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* wsb = static_cast<char*>(ws);
+  twell::MoeArgs a{};
+  a.x = x;
+  a.y = y;
+  a.router = w_router;
+  a.bias = router_bias;
+  a.ids = ids;
+  a.weights = weights;
+  a.gate_codes = static_cast<const uint8_t*>(gate.codes);
+  a.up_codes = static_cast<const uint8_t*>(up.codes);
+  a.down_codes = static_cast<const uint8_t*>(down.codes);
+  a.gate_scales = static_cast<const uint16_t*>(gate.scales);
+  a.up_scales = static_cast<const uint16_t*>(up.scales);
+  a.down_scales = static_cast<const uint16_t*>(down.scales);
+  a.ldx = d->ldx;
+  a.ldy = d->ldy;
+  a.E = d->experts;
+  a.k = d->top_k;
+  a.d = d->d_model;
+  a.f = d->d_ff;
+  a.bits = d->bits;
+  a.group = d->group;
+  a.act = d->act;
+  a.renorm = d->renorm;
+  a.tiles_f = tiles_of(d->d_ff);
+  a.blocks_d = blocks_of(d->d_model);
+  a.tiles_d = tiles_of(d->d_model);
+  a.blocks_f = blocks_of(d->d_ff);
+  a.h = reinterpret_cast<uint16_t*>(wsb + w.h);
+  a.h_plane = w.h_plane;
+  a.h_row = w.h_row;
+  a.n_chosen = reinterpret_cast<int32_t*>(wsb + w.n_chosen);
+  a.chosen = reinterpret_cast<twell::MoeChosen*>(wsb + w.chosen);
+  a.pairs = reinterpret_cast<int32_t*>(wsb + w.pairs);
+  TWELL_TRY(from_hip(twell::launch_moe_route(a, d->T, d->dtype, s)));
+  const int64_t eb = d->dtype == TWELL_BF16 ? 2 : 4;
+  for (int64_t t0 = 0; t0 < d->T; t0 += w.block_tokens) {
+    a.T = static_cast<int32_t>(d->T - t0 < w.block_tokens ? d->T - t0 : w.block_tokens);
+    a.x = static_cast<const char*>(x) + t0 * d->ldx * eb;
+    a.y = static_cast<char*>(y) + t0 * d->ldy * eb;
+    a.ids = ids + t0 * d->top_k;
+    a.weights = weights + t0 * d->top_k;
+    const int64_t pairs = static_cast<int64_t>(a.T) * d->top_k;
+    a.most_chosen = static_cast<int32_t>(pairs < d->experts ? pairs : d->experts);
+    TWELL_TRY(from_hip(twell::launch_moe_experts(a, d->dtype, s)));
+  }
+  return TWELL_OK;
 }
 
 const char* twell_status_str(twell_status s) {

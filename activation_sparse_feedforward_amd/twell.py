@@ -25,7 +25,9 @@ NOALLOC_SCRATCH_BYTES = 128 << 20  # TWELL_NOALLOC_SCRATCH_BYTES
 TWELL_FP32, TWELL_BF16 = 0, 1
 
 EXPORTED = ("twell_sizes", "twell_pack", "twell_pack_classic", "twell_ffn_fwd", "twell_ffn_fwd_hybrid",
-            "twell_ffn_bwd", "twell_dense_ffn_fwd", "twell_status_str", "twell_ffn_fwd_hybrid_noalloc")
+            "twell_ffn_bwd", "twell_dense_ffn_fwd", "twell_status_str", "twell_ffn_fwd_hybrid_noalloc",
+            "twell_weights_sizes", "twell_weights_pack", "twell_weights_unpack", "twell_linear_fwd",
+            "twell_moe_sizes", "twell_moe_fwd")
 
 
 class TwellError(RuntimeError):
@@ -54,6 +56,26 @@ class CSizes(ctypes.Structure):
                 ("ws_pack_classic", ctypes.c_size_t)]
 
 
+class CWDesc(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("bits", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class CPlanes(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class CWSizes(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_size_t), ("scales", ctypes.c_size_t)]
+
+
+class CMoeDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("d_model", ctypes.c_int32), ("d_ff", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("dtype", ctypes.c_int32), ("bits", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("act", ctypes.c_int32), ("renorm", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -65,7 +87,7 @@ def library() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m activation_sparse_feedforward_amd.build` (no CPU fallback exists)")
         lib = ctypes.CDLL(LIB_PATH)
-        P, I64, SZ, ST = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+        P, I32, I64, SZ, ST = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
         D = ctypes.POINTER(CDesc)
         R = ctypes.POINTER(CRoute)
         sig = {
@@ -78,6 +100,12 @@ def library() -> ctypes.CDLL:
             "twell_ffn_fwd": (ST, [D, P, CAct, P, P, P, P]),
             "twell_dense_ffn_fwd": (ST, [D, P, P, P, P, P, P, SZ, P]),
             "twell_status_str": (ctypes.c_char_p, [ST]),
+            "twell_weights_sizes": (ST, [ctypes.POINTER(CWDesc), ctypes.POINTER(CWSizes)]),
+            "twell_weights_pack": (ST, [ctypes.POINTER(CWDesc), P, I32, I32, CPlanes, P]),
+            "twell_weights_unpack": (ST, [ctypes.POINTER(CWDesc), CPlanes, P, I32, P]),
+            "twell_linear_fwd": (ST, [ctypes.POINTER(CWDesc), CPlanes, I64, I32, P, I64, P, I64, P]),
+            "twell_moe_sizes": (ST, [ctypes.POINTER(CMoeDesc), ctypes.POINTER(SZ)]),
+            "twell_moe_fwd": (ST, [ctypes.POINTER(CMoeDesc), P, P, P, CPlanes, CPlanes, CPlanes, P, P, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -309,3 +337,195 @@ def twell_dense_ffn_fwd(desc: Desc, x, w_gate_t, w_up_t, w_down, y, ws, stream=N
         _ptr(w_down, "w_down", desc.d_ff * desc.d_model * e, dt),
         _ptr(y, "y", desc.T * desc.d_model * e, dt), _ptr(ws, "ws", need),
         ctypes.c_size_t(ws.numel() * ws.element_size() if ws is not None else 0), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- serving a few tokens
+ACTIVATIONS = {"relu": 0, "silu": 1}
+_TORCH = {"bf16": torch.bfloat16, "fp32": torch.float32}
+_CODE = {torch.bfloat16: TWELL_BF16, torch.float32: TWELL_FP32}
+
+
+@dataclass(frozen=True)
+class WDesc:
+    """``experts`` matrices of ``rows`` outputs x ``cols`` inputs, held in 4 bits with a scale for every ``group``
+    inputs of a row (32, 64 or 128), or in bf16 (``bits`` 16, ``group`` 0)."""
+    experts: int
+    rows: int
+    cols: int
+    bits: int
+    group: int = 0
+
+
+class Weights(NamedTuple):
+    """The planes of laid-out weights as device tensors."""
+    codes: torch.Tensor   # uint8
+    scales: torch.Tensor  # bf16; empty for 16 bits
+
+
+@dataclass(frozen=True)
+class MoeDesc:
+    """A mixture-of-experts layer for T tokens; ``bits`` and ``group`` are those of the experts' weights."""
+    T: int
+    d_model: int
+    d_ff: int
+    experts: int
+    top_k: int
+    dtype: str  # "fp32" | "bf16": x, the router's weights and y
+    bits: int
+    group: int = 0
+    act: str = "silu"  # "relu" | "silu"
+    renorm: bool = True
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return _TORCH[self.dtype]
+
+    @property
+    def in_desc(self) -> WDesc:
+        """Of the gate and the up projections: d_model -> d_ff."""
+        return WDesc(self.experts, self.d_ff, self.d_model, self.bits, self.group)
+
+    @property
+    def out_desc(self) -> WDesc:
+        """Of the down projections: d_ff -> d_model."""
+        return WDesc(self.experts, self.d_model, self.d_ff, self.bits, self.group)
+
+
+class MoeWeights(NamedTuple):
+    gate: Weights
+    up: Weights
+    down: Weights
+
+
+class MoeOut(NamedTuple):
+    y: torch.Tensor        # dtype [T, d_model]
+    ids: torch.Tensor      # int32 [T, top_k]: the chosen experts, best first
+    weights: torch.Tensor  # fp32 [T, top_k]
+
+
+@functools.lru_cache(maxsize=256)
+def _cwdesc(desc: WDesc) -> CWDesc:
+    return CWDesc(int(desc.experts), int(desc.rows), int(desc.cols), int(desc.bits), int(desc.group))
+
+
+@functools.lru_cache(maxsize=256)
+def _weights_sizes(desc: WDesc) -> tuple:
+    out = CWSizes()
+    _check("twell_weights_sizes", library().twell_weights_sizes(ctypes.byref(_cwdesc(desc)), ctypes.byref(out)))
+    return int(out.codes), int(out.scales)
+
+
+@functools.lru_cache(maxsize=256)
+def _cmoedesc(desc: MoeDesc, ldx: int, ldy: int) -> CMoeDesc:
+    if desc.act not in ACTIVATIONS or desc.dtype not in _TORCH:
+        raise ValueError(f"act {desc.act!r}, dtype {desc.dtype!r}: expected one of {tuple(ACTIVATIONS)} and "
+                         f"{tuple(_TORCH)}")
+    return CMoeDesc(int(desc.T), int(ldx), int(ldy), int(desc.d_model), int(desc.d_ff), int(desc.experts),
+                    int(desc.top_k), TWELL_BF16 if desc.dtype == "bf16" else TWELL_FP32, int(desc.bits),
+                    int(desc.group), ACTIVATIONS[desc.act], int(bool(desc.renorm)))
+
+
+@functools.lru_cache(maxsize=256)
+def moe_ws_bytes(desc: MoeDesc) -> int:
+    out = ctypes.c_size_t()
+    _check("twell_moe_sizes", library().twell_moe_sizes(
+        ctypes.byref(_cmoedesc(desc, desc.d_model, desc.d_model)), ctypes.byref(out)))
+    return int(out.value)
+
+
+def alloc_weights(desc: WDesc, device="cuda") -> Weights:
+    codes, scales = _weights_sizes(desc)
+    return Weights(torch.empty(codes, dtype=torch.uint8, device=device),
+                   torch.empty(scales // 2, dtype=torch.bfloat16, device=device))
+
+
+def alloc_moe_weights(desc: MoeDesc, device="cuda") -> MoeWeights:
+    return MoeWeights(alloc_weights(desc.in_desc, device), alloc_weights(desc.in_desc, device),
+                      alloc_weights(desc.out_desc, device))
+
+
+def alloc_moe_out(desc: MoeDesc, device="cuda") -> MoeOut:
+    return MoeOut(torch.empty((desc.T, desc.d_model), dtype=desc.torch_dtype, device=device),
+                  torch.empty((desc.T, desc.top_k), dtype=torch.int32, device=device),
+                  torch.empty((desc.T, desc.top_k), dtype=torch.float32, device=device))
+
+
+def alloc_moe_ws(desc: MoeDesc, device="cuda") -> torch.Tensor:
+    return torch.empty(moe_ws_bytes(desc), dtype=torch.uint8, device=device)
+
+
+def _planes(desc: WDesc, w: Weights, name: str) -> CPlanes:
+    codes, scales = _weights_sizes(desc)
+    return CPlanes(_ptr(w.codes, name + ".codes", codes, torch.uint8),
+                   _ptr(w.scales, name + ".scales", scales, torch.bfloat16) if scales else 0)
+
+
+def _rows(t: torch.Tensor, name: str, n: int, width: int, dtype: torch.dtype) -> tuple:
+    """Pointer and row stride of n rows of ``width`` elements, each row contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a GPU tensor (got {t.device})")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n, width)}")
+    s0, s1 = t.stride()
+    if width > 1 and s1 != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if n > 1 and s0 < width:
+        raise ValueError(f"{name}: rows overlap (stride {s0} for {width} elements)")
+    return t.data_ptr(), s0 if n > 1 else width
+
+
+def twell_weights_pack(desc: WDesc, w, planes: Weights, transposed: bool = False, stream=None):
+    """Lay out w [experts, rows, cols] ([experts, cols, rows] if transposed; bf16, or fp32 for 4 bits) into planes."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w: expected a torch.Tensor")
+    if w.dtype not in _CODE:
+        raise ValueError(f"w: dtype {w.dtype}, expected torch.bfloat16 or torch.float32")
+    n = desc.experts * desc.rows * desc.cols
+    _check("twell_weights_pack", library().twell_weights_pack(
+        ctypes.byref(_cwdesc(desc)), _ptr(w, "w", n * w.element_size()), _CODE[w.dtype], int(bool(transposed)),
+        _planes(desc, planes, "planes"), _stream(stream)))
+
+
+def twell_weights_unpack(desc: WDesc, planes: Weights, w, stream=None):
+    """Write the values that planes stand for to w [experts, rows, cols] (bf16, or fp32 for 4 bits)."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w: expected a torch.Tensor")
+    if w.dtype not in _CODE:
+        raise ValueError(f"w: dtype {w.dtype}, expected torch.bfloat16 or torch.float32")
+    n = desc.experts * desc.rows * desc.cols
+    _check("twell_weights_unpack", library().twell_weights_unpack(
+        ctypes.byref(_cwdesc(desc)), _planes(desc, planes, "planes"), _ptr(w, "w", n * w.element_size()),
+        _CODE[w.dtype], _stream(stream)))
+
+
+def twell_linear_fwd(desc: WDesc, planes: Weights, x, y, stream=None):
+    """y [T, rows] = x [T, cols] times one matrix of 4-bit weights; x and y in bf16 or fp32, rows may be strided."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _CODE or x.dim() != 2:
+        raise ValueError("x: expected a 2-d torch.bfloat16 or torch.float32 tensor")
+    T = x.shape[0]
+    px, ldx = _rows(x, "x", T, desc.cols, x.dtype)
+    py, ldy = _rows(y, "y", T, desc.rows, x.dtype)
+    _check("twell_linear_fwd", library().twell_linear_fwd(
+        ctypes.byref(_cwdesc(desc)), _planes(desc, planes, "planes"), T, _CODE[x.dtype], px, ldx, py, ldy,
+        _stream(stream)))
+
+
+def twell_moe_fwd(desc: MoeDesc, x, w_router, weights: MoeWeights, out: MoeOut, ws, router_bias=None, stream=None):
+    """Router, chosen experts and their weighted sum for desc.T tokens (see include/twell.h).  x and out.y may have
+    strided rows; ws holds moe_ws_bytes(desc) bytes."""
+    dt = desc.torch_dtype
+    px, ldx = _rows(x, "x", desc.T, desc.d_model, dt)
+    py, ldy = _rows(out.y, "out.y", desc.T, desc.d_model, dt)
+    din, dout = desc.in_desc, desc.out_desc
+    pairs = desc.T * desc.top_k * 4
+    _check("twell_moe_fwd", library().twell_moe_fwd(
+        ctypes.byref(_cmoedesc(desc, ldx, ldy)), px,
+        _ptr(w_router, "w_router", desc.experts * desc.d_model * (2 if desc.dtype == "bf16" else 4), dt),
+        _ptr(router_bias, "router_bias", desc.experts * 4, torch.float32), _planes(din, weights.gate, "gate"),
+        _planes(din, weights.up, "up"), _planes(dout, weights.down, "down"), py,
+        _ptr(out.ids, "out.ids", pairs, torch.int32), _ptr(out.weights, "out.weights", pairs, torch.float32),
+        _ptr(ws, "ws", moe_ws_bytes(desc)), ctypes.c_size_t(ws.nbytes if ws is not None else 0), _stream(stream)))

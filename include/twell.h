@@ -258,6 +258,117 @@ twell_status twell_dense_ffn_fwd(const twell_desc* d, const void* x, const void*
                                  const void* w_up_t, const void* w_down, void* y, void* ws,
                                  size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Serving a few tokens: weights laid out once (in 4 bits or bf16), a product
+ * with 4-bit weights, and a mixture-of-experts gated feed-forward layer.
+ *
+ * These entry points take odd widths and strided rows.  x, y, w and w_router
+ * need only the alignment of their elements; planes and workspaces are 16-byte
+ * aligned.  Rows of x and y are ldx / ldy elements apart (>= their width), and
+ * x and y must not overlap.  Limits: rows, inputs and tokens up to 2^20, rows x
+ * inputs of one matrix up to 2^34, 1024 experts, top_k up to 32, strides up to
+ * 2^40 elements (TWELL_EUNSUPPORTED beyond). */
+
+/* `experts` matrices of `rows` outputs x `cols` inputs held in `bits` (4 or 16)
+ * per weight.  bits = 4: `group` (32, 64 or 128) consecutive inputs of a row
+ * share one scale (the last group of a row may be short); bits = 16: group = 0. */
+typedef struct {
+  int32_t experts;
+  int32_t rows;
+  int32_t cols;
+  int32_t bits;
+  int32_t group;
+} twell_wdesc;
+
+/* Laid-out weights (device pointers; scales is not used for 16 bits).  Blocks
+ * of 16 rows x 128 inputs, [experts][ceil(rows/16)][ceil(cols/128)], padded with
+ * zeros.  In a block, lane l (0..63) holds row l % 16 and inputs 32 s + 8 (l / 16)
+ * + 0..7 for s = 0..3:
+ *   bits = 16: bf16 [s][l][8]                                        4096 bytes
+ *   bits = 4:  32-bit words [l][s], input 2j of the eight in bits 4j..4j+3 and
+ *              input 2j+1 in bits 16+4j..16+4j+3, as q + 8            1024 bytes
+ *              and scales bf16 [16 rows][128 / group]. */
+typedef struct {
+  void* codes;
+  void* scales;
+} twell_wplanes;
+
+typedef struct {
+  size_t codes;
+  size_t scales;
+} twell_wsizes_t;
+
+/* Byte sizes of the planes.  Host only. */
+twell_status twell_weights_sizes(const twell_wdesc* d, twell_wsizes_t* out);
+
+/* Lay weights out.  w: [experts][rows][cols], or with transposed = 1
+ * [experts][cols][rows] (w_down as the layer above keeps it, one row per
+ * neuron, is the transposed form of its d_model x d_ff matrix); contiguous,
+ * bf16, or fp32 when bits = 4.
+ * bits = 4: scale s = bf16(max|w| / 7) of the group (fp32 quotient), code
+ * q = w / s rounded to nearest even and clamped to -7 .. 7 (0 where s = 0).  A group that
+ * holds an infinity or a NaN gets a NaN scale: all its values become NaN. */
+twell_status twell_weights_pack(const twell_wdesc* d, const void* w, int32_t w_dtype, int32_t transposed,
+                                twell_wplanes out, void* stream);
+
+/* The values the planes stand for, q * s (exact in fp32) or the bf16 weights,
+ * written to w [experts][rows][cols] (bf16, or fp32 when bits = 4). */
+twell_status twell_weights_unpack(const twell_wdesc* d, twell_wplanes in, void* w, int32_t w_dtype, void* stream);
+
+/* y[t, n] = sum_k x[t, k] q[n, k] s[n, k / group]: the product of T tokens with
+ * one matrix of 4-bit weights (experts = 1, bits = 4), fp32 sums.
+ *   x [T x cols], y [T x rows] in dtype, rows ldx / ldy apart.
+ * Made for few tokens: the weights are read once per 32 tokens.  T = 0 is a
+ * no-op.  Codes are multiplied as q + 24 and the 24 taken off again inside the
+ * sum, so an infinite input gives NaN, and inputs beyond about 1e36 may
+ * overflow.  Deterministic. */
+twell_status twell_linear_fwd(const twell_wdesc* d, twell_wplanes w, int64_t T, int32_t dtype, const void* x,
+                              int64_t ldx, void* y, int64_t ldy, void* stream);
+
+typedef enum { TWELL_RELU = 0, TWELL_SILU = 1 } twell_activation;
+
+/* Mixture of experts: T tokens, `experts` gated feed-forward layers of d_model x
+ * d_ff, top_k of them per token; dtype of x, w_router and y; bits and group of
+ * the experts' weights; renorm = 1 divides the chosen weights by their sum. */
+typedef struct {
+  int64_t T;
+  int64_t ldx;
+  int64_t ldy;
+  int32_t d_model;
+  int32_t d_ff;
+  int32_t experts;
+  int32_t top_k;
+  int32_t dtype; /* twell_dtype */
+  int32_t bits;
+  int32_t group;
+  int32_t act; /* twell_activation */
+  int32_t renorm;
+} twell_moe_desc;
+
+/* Workspace bytes of twell_moe_fwd.  Host only. */
+twell_status twell_moe_sizes(const twell_moe_desc* d, size_t* ws);
+
+/* The whole layer:
+ *   l[t, e] = x[t] . w_router[e] + router_bias[e]        (fp32)
+ *   ids[t]  = the top_k largest l[t], in descending order; equal ones in ascending
+ *             order of e; a NaN counts as the largest
+ *   weights[t] = softmax(l[t]) over all experts, at ids[t]  (/ their sum if renorm)
+ *   y[t] = sum_i weights[t, i] W_down_e (act(W_gate_e x[t]) * (W_up_e x[t])), e = ids[t, i]
+ * gate, up: planes of {experts, d_ff, d_model, bits, group}; down: planes of
+ * {experts, d_model, d_ff, bits, group}.  w_router [experts x d_model] dtype,
+ * contiguous; router_bias [experts] fp32 or NULL (-inf takes an expert out).
+ * Outputs: y, ids int32 [T x top_k], weights fp32 [T x top_k].
+ * An expert whose weight is 0 adds nothing (its product is not formed), so a
+ * row whose logits are all -inf has weights 0 and y = 0.  A NaN logit makes its
+ * token's weights and y NaN, no other token's.
+ * Hidden values are kept to 16 bits of mantissa (bf16 data) or 24 (fp32); sums
+ * are fp32.  Deterministic.  ws: twell_moe_sizes() bytes; nothing in it needs
+ * to start at zero.  Made for few tokens: experts' weights are read once per
+ * 64 tokens.  T = 0 is a no-op. */
+twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w_router, const float* router_bias,
+                           twell_wplanes gate, twell_wplanes up, twell_wplanes down, void* y, int32_t* ids,
+                           float* weights, void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* twell_status_str(twell_status s);
 

@@ -1,0 +1,167 @@
+"""CPU tests of the few-token entry points: sizes, and bad arguments mapped to
+status codes before any HIP call."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from activation_sparse_feedforward_amd import twell as T
+
+pytestmark = pytest.mark.skipif(not os.path.exists(T.LIB_PATH), reason="libtwell.so not built")
+
+P = 0x10000
+PL = T.CPlanes(P, P)
+
+
+def _w(experts=1, rows=64, cols=128, bits=4, group=64):
+    return T.CWDesc(experts, rows, cols, bits, group)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({}, T.TWELL_OK),
+    ({"bits": 16, "group": 0}, T.TWELL_OK),
+    ({"rows": 1, "cols": 1}, T.TWELL_OK),
+    ({"experts": 0}, T.TWELL_EINVAL),
+    ({"rows": 0}, T.TWELL_EINVAL),
+    ({"cols": -1}, T.TWELL_EINVAL),
+    ({"bits": 8}, T.TWELL_EINVAL),
+    ({"group": 16}, T.TWELL_EINVAL),
+    ({"group": 0}, T.TWELL_EINVAL),
+    ({"bits": 16, "group": 64}, T.TWELL_EINVAL),
+    ({"experts": 1025}, T.TWELL_EUNSUPPORTED),
+    ({"rows": (1 << 20) + 1}, T.TWELL_EUNSUPPORTED),
+    ({"rows": 1 << 20, "cols": 1 << 15}, T.TWELL_EUNSUPPORTED),
+])
+def test_weights_descriptor(kw, code):
+    d, out = _w(**kw), T.CWSizes()
+    assert T.library().twell_weights_sizes(ctypes.byref(d), ctypes.byref(out)) == code
+
+
+def test_weights_sizes_pad_to_blocks():
+    lib = T.library()
+    assert lib.twell_weights_sizes(None, ctypes.byref(T.CWSizes())) == T.TWELL_EINVAL
+    assert lib.twell_weights_sizes(ctypes.byref(_w()), None) == T.TWELL_EINVAL
+    for rows, cols in ((16, 128), (17, 128), (16, 129), (1, 1), (1001, 707)):
+        blocks = -(-rows // 16) * -(-cols // 128)
+        assert T._weights_sizes(T.WDesc(3, rows, cols, 16)) == (3 * blocks * 4096, 0)
+        for group in (32, 64, 128):
+            assert T._weights_sizes(T.WDesc(3, rows, cols, 4, group)) == (3 * blocks * 1024,
+                                                                          3 * blocks * 16 * (128 // group) * 2)
+
+
+def test_pack_and_unpack_refuse():
+    lib = T.library()
+    d, d16 = ctypes.byref(_w()), ctypes.byref(_w(bits=16, group=0))
+    for f in (lambda w, t, pl, d=d: lib.twell_weights_pack(d, w, t, 0, pl, None),
+              lambda w, t, pl, d=d: lib.twell_weights_unpack(d, pl, w, t, None)):
+        assert f(None, T.TWELL_BF16, PL) == T.TWELL_EINVAL
+        assert f(P + 1, T.TWELL_BF16, PL) == T.TWELL_EINVAL
+        assert f(P + 2, T.TWELL_FP32, PL) == T.TWELL_EINVAL
+        assert f(P, 7, PL) == T.TWELL_EINVAL
+        assert f(P, T.TWELL_BF16, T.CPlanes(0, P)) == T.TWELL_EINVAL
+        assert f(P, T.TWELL_BF16, T.CPlanes(P, 0)) == T.TWELL_EINVAL
+        assert f(P, T.TWELL_BF16, T.CPlanes(P + 8, P)) == T.TWELL_EINVAL
+        assert f(P, T.TWELL_FP32, PL, d16) == T.TWELL_EUNSUPPORTED  # bf16 planes hold bf16 weights
+    assert lib.twell_weights_pack(d, P, T.TWELL_BF16, 2, PL, None) == T.TWELL_EINVAL
+    assert lib.twell_weights_pack(None, P, T.TWELL_BF16, 0, PL, None) == T.TWELL_EINVAL
+
+
+def test_linear_refuses():
+    lib = T.library()
+    f = lib.twell_linear_fwd
+    d, bf = ctypes.byref(_w()), T.TWELL_BF16
+    assert f(d, T.CPlanes(0, 0), 0, bf, None, 128, None, 64, None) == T.TWELL_OK  # no tokens: nothing is read
+    assert f(d, PL, -1, bf, P, 128, P, 64, None) == T.TWELL_EINVAL
+    assert f(d, PL, 1, 5, P, 128, P, 64, None) == T.TWELL_EINVAL
+    assert f(d, PL, 1, bf, P, 127, P, 64, None) == T.TWELL_EINVAL  # rows overlap
+    assert f(d, PL, 1, bf, P, 128, P, 63, None) == T.TWELL_EINVAL
+    assert f(d, PL, 1, bf, None, 128, P, 64, None) == T.TWELL_EINVAL
+    assert f(d, PL, 1, bf, P, 128, None, 64, None) == T.TWELL_EINVAL
+    assert f(d, PL, 1, bf, P + 1, 128, P, 64, None) == T.TWELL_EINVAL
+    assert f(d, PL, 1, T.TWELL_FP32, P, 128, P + 2, 64, None) == T.TWELL_EINVAL
+    assert f(d, T.CPlanes(P, 0), 1, bf, P, 128, P, 64, None) == T.TWELL_EINVAL
+    assert f(d, PL, (1 << 20) + 1, bf, P, 128, P, 64, None) == T.TWELL_EUNSUPPORTED
+    assert f(d, PL, 1, bf, P, (1 << 40) + 1, P, 64, None) == T.TWELL_EUNSUPPORTED
+    assert f(ctypes.byref(_w(experts=2)), PL, 1, bf, P, 128, P, 64, None) == T.TWELL_EUNSUPPORTED
+    assert f(ctypes.byref(_w(bits=16, group=0)), PL, 1, bf, P, 128, P, 64, None) == T.TWELL_EUNSUPPORTED
+
+
+def _m(**kw):
+    base = dict(T=4, ldx=128, ldy=128, d_model=128, d_ff=64, experts=8, top_k=2, dtype=T.TWELL_BF16, bits=4, group=64,
+                act=0, renorm=1)
+    base.update(kw)
+    return T.CMoeDesc(**base)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({}, T.TWELL_OK),
+    ({"T": 0}, T.TWELL_OK),
+    ({"T": 100000}, T.TWELL_OK),
+    ({"bits": 16, "group": 0}, T.TWELL_OK),
+    ({"T": -1}, T.TWELL_EINVAL),
+    ({"top_k": 0}, T.TWELL_EINVAL),
+    ({"top_k": 9}, T.TWELL_EINVAL),
+    ({"dtype": 2}, T.TWELL_EINVAL),
+    ({"act": 2}, T.TWELL_EINVAL),
+    ({"renorm": 2}, T.TWELL_EINVAL),
+    ({"ldx": 127}, T.TWELL_EINVAL),
+    ({"ldy": 127}, T.TWELL_EINVAL),
+    ({"d_ff": 0}, T.TWELL_EINVAL),
+    ({"bits": 5}, T.TWELL_EINVAL),
+    ({"experts": 2000}, T.TWELL_EUNSUPPORTED),
+    ({"experts": 64, "top_k": 33}, T.TWELL_EUNSUPPORTED),
+    ({"T": 1 << 21}, T.TWELL_EUNSUPPORTED),
+    ({"ldx": 1 << 41}, T.TWELL_EUNSUPPORTED),
+])
+def test_moe_descriptor(kw, code):
+    n = ctypes.c_size_t()
+    assert T.library().twell_moe_sizes(ctypes.byref(_m(**kw)), ctypes.byref(n)) == code
+
+
+def test_moe_refuses():
+    lib = T.library()
+    d = _m()
+    n = ctypes.c_size_t()
+    assert lib.twell_moe_sizes(ctypes.byref(d), None) == T.TWELL_EINVAL
+    assert lib.twell_moe_sizes(ctypes.byref(d), ctypes.byref(n)) == T.TWELL_OK
+    good = dict(d=ctypes.byref(d), x=P, r=P, bias=None, g=PL, u=PL, dn=PL, y=P, ids=P, w=P, ws=P, n=n.value)
+
+    def call(**kw):
+        a = dict(good, **kw)
+        return lib.twell_moe_fwd(a["d"], a["x"], a["r"], a["bias"], a["g"], a["u"], a["dn"], a["y"], a["ids"], a["w"],
+                                 a["ws"], a["n"], None)
+
+    for bad in (dict(x=None), dict(r=None), dict(y=None), dict(ids=None), dict(w=None), dict(ws=None), dict(x=P + 1),
+                dict(y=P + 1), dict(r=P + 1), dict(ids=P + 2), dict(w=P + 2), dict(bias=P + 2), dict(ws=P + 8),
+                dict(n=n.value - 1), dict(g=T.CPlanes(0, P)), dict(u=T.CPlanes(P, 0)), dict(dn=T.CPlanes(P + 4, P)),
+                dict(d=None)):
+        assert call(**bad) == T.TWELL_EINVAL, bad
+    e = _m(T=0)
+    none = T.CPlanes(0, 0)
+    assert call(d=ctypes.byref(e), x=None, r=None, y=None, ids=None, w=None, ws=None, n=0, g=none, u=none,
+                dn=none) == T.TWELL_OK
+
+
+def test_moe_workspace_stops_growing_with_the_batch():
+    big = [T.moe_ws_bytes(T.MoeDesc(t, 128, 64, 8, 2, "bf16", 4, 64)) for t in (64, 65, 4096)]
+    assert big[0] == big[1] == big[2] >= 64 * 2 * 128 * 2 * 2
+
+
+def test_binding_refuses_host_tensors_and_bad_shapes():
+    wd = T.WDesc(1, 64, 128, 4, 64)
+    pl = T.alloc_weights(wd, device="cpu")
+    with pytest.raises(ValueError):
+        T.twell_weights_pack(wd, torch.zeros(64, 128, dtype=torch.bfloat16), pl)
+    with pytest.raises(ValueError):
+        T.twell_weights_pack(wd, torch.zeros(64, 128, dtype=torch.float16), pl)
+    with pytest.raises(TypeError):
+        T.twell_weights_unpack(wd, pl, None)
+    with pytest.raises(ValueError):
+        T.twell_linear_fwd(wd, pl, torch.zeros(1, 128, dtype=torch.bfloat16), torch.zeros(1, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        T.twell_linear_fwd(wd, pl, torch.zeros(128), torch.zeros(64))
+    with pytest.raises(ValueError):
+        T.moe_ws_bytes(T.MoeDesc(1, 128, 64, 8, 2, "bf16", 4, 64, act="tanh"))
+    with pytest.raises(T.TwellError):
+        T.moe_ws_bytes(T.MoeDesc(1, 128, 64, 8, 9, "bf16", 4, 64))
