@@ -194,24 +194,26 @@ struct Tile {
   const uint16_t* scales;
 };
 
-// The G scales of lane's row in one block, as fp32.
+// The G scales of lane's row in one block, as loaded; at(i): as fp32.
 template <int G>
-__device__ __forceinline__ void load_scales(const uint16_t* p, int lane, float (&s)[G]) {
-  const uint16_t* q = p + (lane & 15) * G;
-  if constexpr (G == 1) {
-    s[0] = bf16_bits_to_f32(q[0]);
-  } else if constexpr (G == 2) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(q);
-    s[0] = __uint_as_float(v << 16);
-    s[1] = __uint_as_float(v & 0xffff0000u);
-  } else {
-    const u32x2_t v = *reinterpret_cast<const u32x2_t*>(q);
-    s[0] = __uint_as_float(v[0] << 16);
-    s[1] = __uint_as_float(v[0] & 0xffff0000u);
-    s[2] = __uint_as_float(v[1] << 16);
-    s[3] = __uint_as_float(v[1] & 0xffff0000u);
+struct Scales {
+  uint32_t v[(G + 1) / 2];
+  __device__ __forceinline__ void load(const uint16_t* p, int lane) {
+    const uint16_t* q = p + (lane & 15) * G;
+    if constexpr (G == 1) {
+      v[0] = q[0];
+    } else if constexpr (G == 2) {
+      v[0] = *reinterpret_cast<const uint32_t*>(q);
+    } else {
+      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(q);
+      v[0] = w[0];
+      v[1] = w[1];
+    }
   }
-}
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i & 1 ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16);
+  }
+};
 
 // acc += tokens x weights over blocks [b0, b1) of NR tiles.  TQ: quads of
 // tokens (1: up to 4 tokens, 4 / 8 / 16: up to 16 / 32 / 64); MT = tiles of 16
@@ -219,13 +221,17 @@ __device__ __forceinline__ void load_scales(const uint16_t* p, int lane, float (
 // blocks whose inputs are all below K.
 template <int TQ>
 constexpr int token_tiles() { return (TQ + 3) / 4; }
+// Result registers in use per tile of 16 tokens.
+template <int TQ>
+constexpr int token_regs() { return TQ < 4 ? TQ : 4; }
 
 template <int BITS, int G, int TQ, int NR, class Row>
 struct Product {
   static constexpr int MT = token_tiles<TQ>();
   static constexpr int P = Row::kPlanes;
-  static constexpr int kRegs = TQ < 4 ? TQ : 4;  // result registers in use per tile
-  static constexpr bool kExact = P == 3;  // fp32 data: codes without the offset
+  static constexpr int kRegs = token_regs<TQ>();
+  static constexpr int kAll = NR * MT * kRegs;  // result registers
+  static constexpr bool kExact = P == 3;        // fp32 data: codes without the offset
   f32x4_t acc[MT][NR];
 
   __device__ __forceinline__ void clear() {
@@ -236,24 +242,24 @@ struct Product {
   }
 
   struct Loaded {
-    Block<BITS> w[NR];
-    float s[NR][G];
     bf16x8_t x[MT][4][P];
+    Block<BITS> w[NR];
+    Scales<G> s[NR];
   };
 
-  __device__ __forceinline__ void fetch(Loaded& q, const Row (&row)[MT], const Tile (&tile)[NR], int b, bool whole,
-                                        int lane) const {
-#pragma unroll
-    for (int r = 0; r < NR; ++r) q.w[r].load(tile[r].codes + static_cast<int64_t>(b) * Block<BITS>::kBytes, lane);
-    if constexpr (BITS == 4) {
-#pragma unroll
-      for (int r = 0; r < NR; ++r) load_scales<G>(tile[r].scales + static_cast<int64_t>(b) * (16 * G), lane, q.s[r]);
-    }
+  static __device__ __forceinline__ void fetch(Loaded& q, const Row (&row)[MT], const Tile (&tile)[NR], int b,
+                                               bool whole, int lane) {
     const int k = b * kBlockK + (lane >> 4) * 8;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int s = 0; s < 4; ++s) row[m].load(k + 32 * s, whole, q.x[m][s]);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) q.w[r].load(tile[r].codes + static_cast<int64_t>(b) * Block<BITS>::kBytes, lane);
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) q.s[r].load(tile[r].scales + static_cast<int64_t>(b) * (16 * G), lane);
+    }
   }
 
   __device__ __forceinline__ void use(const Loaded& q) {
@@ -297,33 +303,62 @@ struct Product {
 #pragma unroll
               for (int p = P - 1; p >= 0; --p) t[m] = mfma16(q.x[m][gr * kSteps + s][p], b, t[m]);
           }
+          const float sc = q.s[r].at(gr);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < kRegs; ++i) acc[m][r][i] = fmaf(q.s[r][gr], t[m][i], acc[m][r][i]);
+            for (int i = 0; i < kRegs; ++i) acc[m][r][i] = fmaf(sc, t[m][i], acc[m][r][i]);
         }
       }
     }
   }
 
+  // U blocks are fetched together.
   template <int U>
   __device__ __forceinline__ void run(const Row (&row)[MT], const Tile (&tile)[NR], int b0, int b1, int nfull,
                                       int lane) {
     int b = b0;
     const int whole_end = b1 < nfull ? b1 : nfull;
-    for (; b + U <= whole_end; b += U) {
-      Loaded q[U];
+    if constexpr (U > 1) {
+      for (; b + U <= whole_end; b += U) {
+        Loaded q[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) fetch(q[u], row, tile, b + u, true, lane);
+        for (int u = 0; u < U; ++u) fetch(q[u], row, tile, b + u, true, lane);
 #pragma unroll
-      for (int u = 0; u < U; ++u) use(q[u]);
+        for (int u = 0; u < U; ++u) use(q[u]);
+      }
+    }
+    for (; b < whole_end; ++b) {
+      Loaded q;
+      fetch(q, row, tile, b, true, lane);
+      use(q);
     }
     for (; b < b1; ++b) {
       Loaded q;
-      fetch(q, row, tile, b, b < nfull, lane);
+      fetch(q, row, tile, b, false, lane);
       use(q);
     }
   }
+
+  // The wave's sums to LDS: register j = (r, m, i) of lane l at
+  // red[(wave * kAll + j) * 64 + l].
+  __device__ __forceinline__ void put(float* red, int wave, int lane) const {
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) red[(wave * kAll + (r * MT + m) * kRegs + i) * 64 + lane] = acc[m][r][i];
+  }
 };
+
+// Sum over the waves, in their order, of element o (register * 64 + lane) of
+// kAll * 64 put there by Product::put.
+template <int kAll>
+__device__ __forceinline__ float joined(const float* red, int waves, int o) {
+  float v = 0.f;
+  for (int w = 0; w < waves; ++w) v += red[w * kAll * 64 + o];
+  return v;
+}
 
 }  // namespace twell

@@ -188,9 +188,6 @@ struct LinearArgs {
 constexpr int kMoeBlockTokens = 64;
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 32;
-struct MoeChosen {
-  int32_t expert, first, n, pad;  // its entries in the pair list
-};
 struct MoeArgs {
   const void* x;
   void* y;
@@ -206,9 +203,7 @@ struct MoeArgs {
   // workspace
   uint16_t* h;         // [planes][T * k][blocks_f * 128] hidden values of each (token, choice) pair
   int64_t h_plane, h_row;
-  int32_t* n_chosen;   // experts with a token
-  MoeChosen* chosen;   // [most_chosen], ascending experts
-  int32_t* pairs;      // [T * k] (token, choice) pairs by expert
+  float* z;            // [T * k][d] the pairs' outputs (more than four tokens)
 };
 
 // dtype: 0 = fp32, 1 = bf16.  Each returns hipSuccess or the launch error.

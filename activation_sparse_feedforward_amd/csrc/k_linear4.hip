@@ -10,18 +10,18 @@
 namespace twell {
 namespace {
 
-// More tokens need more registers, so fewer waves per workgroup.
-template <int TQ>
-constexpr int max_waves() { return TQ <= 4 ? 16 : 8; }
+// More results per wave need more registers, so fewer waves per workgroup.
+template <int TQ, int NR>
+constexpr int max_waves() { return NR * token_tiles<TQ>() * token_regs<TQ>() <= 16 ? 16 : 8; }
 
 template <class E, int G, int TQ, int NR>
-__global__ __launch_bounds__(max_waves<TQ>() * kWave) void linear4_kernel(LinearArgs a) {
+__global__ __launch_bounds__((max_waves<TQ, NR>() * kWave)) void linear4_kernel(LinearArgs a) {
   extern __shared__ float red[];
   using Row = std::conditional_t<E::kBytes == 2, RowBf16, RowF32>;
   using Elem = typename E::storage;
   using Prod = Product<4, G, TQ, NR, Row>;
   constexpr int MT = Prod::MT;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * (4 * TQ);
   const int T = a.T - t0 < 4 * TQ ? static_cast<int>(a.T - t0) : 4 * TQ;
@@ -44,21 +44,11 @@ __global__ __launch_bounds__(max_waves<TQ>() * kWave) void linear4_kernel(Linear
   Prod p;
   p.clear();
   const int b0 = a.blocks * wave / waves, b1 = a.blocks * (wave + 1) / waves;
-  p.template run<(TQ <= 4 && E::kBytes == 2) ? 2 : 1>(row, tile, b0, b1, a.K / kBlockK, lane);
-
-  // register j = (r, m, i) of lane l at red[(wave * kAll + j) * 64 + l]
-  constexpr int kAll = NR * MT * Prod::kRegs;
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < Prod::kRegs; ++i)
-        red[(wave * kAll + (r * MT + m) * Prod::kRegs + i) * 64 + lane] = p.acc[m][r][i];
+  p.template run<(Prod::kAll <= 4 && E::kBytes == 2) ? 2 : 1>(row, tile, b0, b1, a.K / kBlockK, lane);
+  p.put(red, wave, lane);
   __syncthreads();
-  for (int o = threadIdx.x; o < kAll * 64; o += blockDim.x) {
-    float v = 0.f;
-    for (int w = 0; w < waves; ++w) v += red[w * kAll * 64 + o];
+  for (int o = threadIdx.x; o < Prod::kAll * 64; o += blockDim.x) {
+    const float v = joined<Prod::kAll>(red, waves, o);
     const int j = o >> 6, l = o & 63;
     const int i = j % Prod::kRegs, m = (j / Prod::kRegs) % MT, r = j / (Prod::kRegs * MT);
     const int t = m * 16 + result_token(i, l);
@@ -73,18 +63,32 @@ __global__ __launch_bounds__(max_waves<TQ>() * kWave) void linear4_kernel(Linear
 
 template <class E, int G, int TQ, int NR>
 void go(const LinearArgs& a, hipStream_t s) {
-  constexpr int kAll = NR * token_tiles<TQ>() * (TQ < 4 ? TQ : 4);
-  int waves = max_waves<TQ>();
+  constexpr int kAll = NR * token_tiles<TQ>() * token_regs<TQ>();
+  int waves = max_waves<TQ, NR>();
   while (waves > 1 && waves > a.blocks) waves >>= 1;
   const dim3 grid((a.tiles + NR - 1) / NR, static_cast<unsigned>((a.T + 4 * TQ - 1) / (4 * TQ)));
   linear4_kernel<E, G, TQ, NR><<<grid, waves * kWave, waves * kAll * 64 * sizeof(float), s>>>(a);
 }
 
+// The most tiles per workgroup that still leave a workgroup for every CU.
+template <class E, int G, int TQ, int NR>
+void by_rows(const LinearArgs& a, int cus, hipStream_t s) {
+  const int64_t groups = (a.T + 4 * TQ - 1) / (4 * TQ);
+  if constexpr (NR > 1) {
+    if ((a.tiles + NR - 1) / NR * groups < cus) {
+      by_rows<E, G, TQ, NR / 2>(a, cus, s);
+      return;
+    }
+  }
+  go<E, G, TQ, NR>(a, s);
+}
+
 template <class E, int G>
 void by_tokens(const LinearArgs& a, hipStream_t s) {
-  if (a.T <= 4) go<E, G, 1, 1>(a, s);
-  else if (a.T <= 16) go<E, G, 4, 1>(a, s);
-  else go<E, G, 8, 2>(a, s);
+  const int cus = 256;
+  if (a.T <= 4) by_rows<E, G, 1, (E::kBytes == 2 ? 8 : 4) / (G == 4 ? 4 : 1)>(a, cus, s);
+  else if (a.T <= 16) by_rows<E, G, 4, 4>(a, cus, s);
+  else by_rows<E, G, 8, E::kBytes == 2 ? 2 : 1>(a, cus, s);
 }
 
 template <class E>

@@ -3,15 +3,15 @@
 //   l[t,e] = x[t] . r[e] + b[e];  the top_k largest per token, softmax weights w
 //   y[t]   = sum_i w_i  W_down_e ( act(W_gate_e x) * (W_up_e x) ),   e = ids[t,i]
 //
-// Three kernels.  (1) moe_route_kernel: one workgroup per token, logits in
-// fp32, selection by one wave.  (2) moe_up_kernel: one workgroup per (chosen
-// expert, 16 neurons); it gathers the expert's tokens, computes gate and up
-// together and writes w * act(g) * u.  (3) moe_down_kernel: one workgroup per 16
-// outputs; its waves split the chosen experts' neurons, add each expert's
-// products to the rows of its tokens in a private LDS tile and join the tiles
-// in wave order, so y is written once and does not depend on timing.
-// Only chosen experts' weights are read, each once per call of up to 64
-// tokens.  Bound by reading them.
+// (1) moe_route_kernel: one workgroup per token, logits in fp32, selection by
+// one wave.  (2) moe_up_kernel: one workgroup per (chosen expert, NT tiles of
+// 16 neurons); it gathers the expert's tokens, computes gate and up together
+// and writes h = w * act(g) * u.  (3) Up to four tokens: moe_down_few_kernel,
+// one workgroup per 16 outputs for all choices.  More: moe_down_kernel, one
+// workgroup per (chosen expert, NT tiles of 16 outputs), writes every pair's
+// part and moe_join_kernel adds them up in the order of the choices.
+// Nothing depends on timing.  Only chosen experts' weights are read, each once
+// per 16 of its tokens.  Bound by reading them.
 #include "few_token.hpp"
 #include "internal.hpp"
 
@@ -22,13 +22,16 @@ namespace {
 constexpr int kRouteWaves = 16;
 constexpr int kRouteAhead = 4;  // experts a wave computes side by side
 
+// Largest value over the 64 lanes (the steps of wave_sum).
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const uint32_t o = __shfl_xor(v, m);
-    v = v > o ? v : o;
-  }
-  return v;
+  auto most = [](uint32_t a, int b) { return a > static_cast<uint32_t>(b) ? a : static_cast<uint32_t>(b); };
+  v = most(v, dpp_take<0xB1>(static_cast<int>(v)));
+  v = most(v, dpp_take<0x4E>(static_cast<int>(v)));
+  v = most(v, dpp_take<0x141>(static_cast<int>(v)));
+  v = most(v, dpp_take<0x140>(static_cast<int>(v)));
+  v = most(v, dpp_take<0x142, 0xa>(static_cast<int>(v)));
+  v = most(v, dpp_take<0x143, 0xc>(static_cast<int>(v)));
+  return static_cast<uint32_t>(wave_last(static_cast<int>(v)));
 }
 
 // Unsigned key in the order of the logits: NaN above everything, -0 = +0, 0
@@ -42,50 +45,71 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
+// Eight inputs as loaded, and as fp32.
 template <class E>
-__device__ __forceinline__ void load8(const typename E::storage* p, int k, int K, float (&f)[8]) {
-  if (k + 8 <= K) {
+struct Eight {
+  u32x4_t v[E::kBytes / 2];
+  __device__ __forceinline__ void load(const typename E::storage* p) {
     if constexpr (E::kBytes == 2) {
-      const u32x4_t v = *reinterpret_cast<const u32x4_a2_t*>(p + k);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(v[i] << 16);
-        f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-      }
+      v[0] = *reinterpret_cast<const u32x4_a2_t*>(p);
     } else {
-      const u32x4_t a = *reinterpret_cast<const u32x4_a4_t*>(p + k);
-      const u32x4_t b = *reinterpret_cast<const u32x4_a4_t*>(p + k + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] = __uint_as_float(a[i]);
-        f[4 + i] = __uint_as_float(b[i]);
-      }
+      v[0] = *reinterpret_cast<const u32x4_a4_t*>(p);
+      v[1] = *reinterpret_cast<const u32x4_a4_t*>(p + 4);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = k + i < K ? load_elem<E>(p, k + i) : 0.f;
   }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (E::kBytes == 2) return __uint_as_float(i & 1 ? v[0][i >> 1] & 0xffff0000u : v[0][i >> 1] << 16);
+    else return __uint_as_float(v[i >> 2][i & 3]);
+  }
+};
+
+// s[j] += x . r[j] over inputs [k0, k0 + 512 U), eight per lane and 512; all
+// loads ahead of all sums, since one workgroup has a CU's share of the
+// bandwidth to itself and is bound by how much it has in flight.
+template <class E, int U>
+__device__ __forceinline__ void route_dots(const typename E::storage* x, const typename E::storage* const (&r)[kRouteAhead],
+                                           int k, float (&s)[kRouteAhead]) {
+  Eight<E> xv[U], rv[U][kRouteAhead];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    xv[u].load(x + k + 512 * u);
+#pragma unroll
+    for (int j = 0; j < kRouteAhead; ++j) rv[u][j].load(r[j] + k + 512 * u);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = 0; j < kRouteAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[j] = fmaf(xv[u].at(i), rv[u][j].at(i), s[j]);
 }
 
-template <class E>
+// kRegs * 64 >= E.
+template <class E, int kRegs>
 __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a) {
-  __shared__ float logit[kMoeMaxExperts];
+  __shared__ float logit[kRegs * 64];
   using Elem = typename E::storage;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int U = 2;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x;
   const Elem* x = static_cast<const Elem*>(a.x) + t * a.ldx;
   for (int e0 = wave * kRouteAhead; e0 < a.E; e0 += kRouteWaves * kRouteAhead) {
+    const Elem* r[kRouteAhead];
+#pragma unroll
+    for (int j = 0; j < kRouteAhead; ++j)
+      r[j] = static_cast<const Elem*>(a.router) + static_cast<int64_t>(e0 + j < a.E ? e0 + j : a.E - 1) * a.d;
     float s[kRouteAhead] = {};
-    for (int k = lane * 8; k < a.d; k += 512) {
-      float xv[8];
-      load8<E>(x, k, a.d, xv);
+    int k0 = 0;
+    for (; k0 + 512 * U <= a.d; k0 += 512 * U) route_dots<E, U>(x, r, k0 + lane * 8, s);
+    for (; k0 + 512 <= a.d; k0 += 512) route_dots<E, 1>(x, r, k0 + lane * 8, s);
+    const int k = k0 + lane * 8;
+    if (k + 8 <= a.d) {
+      route_dots<E, 1>(x, r, k, s);
+    } else {
+      for (int i = k; i < a.d; ++i) {
+        const float xv = load_elem<E>(x, i);
 #pragma unroll
-      for (int j = 0; j < kRouteAhead; ++j) {
-        const int e = e0 + j < a.E ? e0 + j : a.E - 1;
-        float rv[8];
-        load8<E>(static_cast<const Elem*>(a.router) + static_cast<int64_t>(e) * a.d, k, a.d, rv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[j] = fmaf(xv[i], rv[i], s[j]);
+        for (int j = 0; j < kRouteAhead; ++j) s[j] = fmaf(xv, load_elem<E>(r[j], i), s[j]);
       }
     }
 #pragma unroll
@@ -98,17 +122,18 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
   if (wave != 0) return;
 
   // expert e = 64 r + lane is in key[r]
-  constexpr int kRegs = kMoeMaxExperts / 64;
   uint32_t key[kRegs];
-#pragma unroll
-  for (int r = 0; r < kRegs; ++r) key[r] = r * 64 + lane < a.E ? order_key(logit[r * 64 + lane]) : 0u;
   uint32_t top = 0;
 #pragma unroll
-  for (int r = 0; r < kRegs; ++r) top = key[r] > top ? key[r] : top;
+  for (int r = 0; r < kRegs; ++r) {
+    key[r] = r * 64 + lane < a.E ? order_key(logit[r * 64 + lane]) : 0u;
+    top = key[r] > top ? key[r] : top;
+  }
   const float most = key_value(wave_umax(top));
   const bool none = most == -INFINITY;  // every expert is masked off: all weights 0
   float sum = 0.f;
-  for (int r = 0; r * 64 < a.E; ++r)
+#pragma unroll
+  for (int r = 0; r < kRegs; ++r)
     if (r * 64 + lane < a.E) sum += expf(logit[r * 64 + lane] - most);
   sum = wave_sum(sum);
 
@@ -143,61 +168,112 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
   }
 }
 
-// ---------------------------------------------------------------- shared parts
-template <class Prod, int NR>
-__device__ __forceinline__ void put_partial(const Prod& p, float* red, int wave, int lane) {
-  constexpr int kAll = NR * Prod::MT * Prod::kRegs;
+// ---------------------------------------------------------------- expert lists
+constexpr int kExpertWaves = 8;
+constexpr int kPairsAhead = 8;  // pairs per lane held at once
+
+// Where one wave works out its expert and the expert's pairs.  Every wave does
+// so for itself, without a barrier: the pairs come from the L2 once, and
+// what follows are LDS and lane operations of a few hundred cycles.
+struct WaveList {
+  uint32_t taken[kMoeMaxExperts / 32];
+  int pair[kMoeBlockTokens];
+};
+
+// Finds the `which`-th chosen expert (ascending) and its (token, choice) pairs
+// (ascending) in the lists of the router; a choice of weight 0 is no choice, a
+// NaN weight is one.  Returns the expert, or -1 if there are not that many; n:
+// its pairs.
+__device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList& l, int lane, int& n) {
+  const int pairs = a.T * a.k;
+  n = 0;
+  if (lane < kMoeMaxExperts / 32) l.taken[lane] = 0;
+  int id[kPairsAhead];
+  auto fetch = [&](int i0) {
 #pragma unroll
-  for (int r = 0; r < NR; ++r)
+    for (int u = 0; u < kPairsAhead; ++u) {
+      const int i = i0 + u * 64 + lane;
+      id[u] = -1;
+      if (i < pairs) {
+        const int e = a.ids[i];
+        if (a.weights[i] != 0.f) id[u] = e;
+      }
+    }
+  };
+  for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
+    fetch(i0);
 #pragma unroll
-    for (int m = 0; m < Prod::MT; ++m)
+    for (int u = 0; u < kPairsAhead; ++u)
+      if (id[u] >= 0) atomicOr(&l.taken[id[u] >> 5], 1u << (id[u] & 31));
+  }
+  __builtin_amdgcn_wave_barrier();
+  uint32_t word = lane < kMoeMaxExperts / 32 ? l.taken[lane] : 0u;
+  const int count = __popc(word);
+  const int upto = wave_incl_scan(count);
+  const uint64_t at = __ballot(which < upto);
+  if (at == 0) return -1;
+  const int owner = __builtin_ctzll(at);
+  const int skip = which - (upto - count);  // set bits before it, in the owner's word
+  for (int i = 0; i < __builtin_amdgcn_readlane(skip, owner); ++i) word &= word - 1;
+  const int expert = owner * 32 + __builtin_ctz(__builtin_amdgcn_readlane(word, owner));
+  for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
+    if (pairs > kPairsAhead * 64) fetch(i0);
 #pragma unroll
-      for (int i = 0; i < Prod::kRegs; ++i)
-        red[(wave * kAll + (r * Prod::MT + m) * Prod::kRegs + i) * 64 + lane] = p.acc[m][r][i];
+    for (int u = 0; u < kPairsAhead; ++u) {
+      const uint64_t has = __ballot(id[u] == expert);
+      if (id[u] == expert) l.pair[n + __popcll(has & ((1ull << lane) - 1))] = i0 + u * 64 + lane;
+      n += __popcll(has);
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  return expert;
 }
 
 // ---------------------------------------------------------------- gate and up
-constexpr int kUpWaves = 8;
-constexpr int kUpPairs = kMoeBlockTokens * kMoeMaxTopK;
-
-// h = w act(g) u for the tokens list[0 .. n) of one expert and 16 neurons.
-template <class E, int BITS, int G, int TQ>
-__device__ __forceinline__ void up_tokens(const MoeArgs& a, const Tile (&tile)[2], const int* list, int n, int neuron0,
-                                          float* red, int lane, int wave) {
+// h = w act(g) u for n pairs of one expert and the neurons of NT tiles from
+// tile ti on.
+template <class E, int BITS, int G, int TQ, int NT>
+__device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, const int* pair, int n, float* red,
+                                         int lane, int wave) {
   using Row = std::conditional_t<E::kBytes == 2, RowBf16, RowF32>;
   using Elem = typename E::storage;
-  using Prod = Product<BITS, G, TQ, 2, Row>;
-  constexpr int MT = Prod::MT;
+  using Prod = Product<BITS, G, TQ, 2 * NT, Row>;
+  constexpr int MT = Prod::MT, kOne = MT * Prod::kRegs;  // registers of one tile
   Row row[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int i = m * 16 + lane_token(lane);
     row[m].K = a.d;
-    row[m].p = i < n ? static_cast<const Elem*>(a.x) + static_cast<int64_t>(list[i] / a.k) * a.ldx : nullptr;
+    row[m].p = i < n ? static_cast<const Elem*>(a.x) + static_cast<int64_t>(pair[i] / a.k) * a.ldx : nullptr;
+  }
+  Tile tile[2 * NT];
+#pragma unroll
+  for (int r = 0; r < NT; ++r) {
+    const int i = ti + r < a.tiles_f ? ti + r : a.tiles_f - 1;
+    const int64_t blk = (static_cast<int64_t>(expert) * a.tiles_f + i) * a.blocks_d;
+    tile[2 * r] = {a.gate_codes + blk * Block<BITS>::kBytes, a.gate_scales + blk * (16 * G)};
+    tile[2 * r + 1] = {a.up_codes + blk * Block<BITS>::kBytes, a.up_scales + blk * (16 * G)};
   }
   Prod p;
   p.clear();
-  p.template run<(TQ <= 4 && E::kBytes == 2) ? 2 : 1>(row, tile, a.blocks_d * wave / kUpWaves, a.blocks_d * (wave + 1) / kUpWaves, a.d / kBlockK, lane);
-  put_partial<Prod, 2>(p, red, wave, lane);
+  p.template run<(NT == 1 && MT == 1 && E::kBytes == 2) ? 2 : 1>(
+      row, tile, a.blocks_d * wave / kExpertWaves, a.blocks_d * (wave + 1) / kExpertWaves, a.d / kBlockK, lane);
+  p.put(red, wave, lane);
   __syncthreads();
-  constexpr int kOne = MT * Prod::kRegs;  // registers of one matrix
-  for (int o = threadIdx.x; o < kOne * 64; o += kUpWaves * kWave) {
-    float g = 0.f, u = 0.f;
-    for (int w = 0; w < kUpWaves; ++w) {
-      g += red[w * 2 * kOne * 64 + o];
-      u += red[(w * 2 + 1) * kOne * 64 + o];
-    }
-    const int j = o >> 6, l = o & 63;
+  for (int o = threadIdx.x; o < NT * kOne * 64; o += kExpertWaves * kWave) {
+    const int r = o / (kOne * 64), j = o / 64 % kOne, l = o & 63;
     const int i = (j / Prod::kRegs) * 16 + result_token(j % Prod::kRegs, l);
     if (i >= n) continue;
-    const int slot = list[i];
+    const float g = joined<Prod::kAll>(red, kExpertWaves, o + r * kOne * 64);
+    const float u = joined<Prod::kAll>(red, kExpertWaves, o + (r + 1) * kOne * 64);
     // a NaN gate stays NaN under both activations
     const float act = a.act == 0 ? (g < 0.f ? 0.f : g) : g / (1.f + expf(-g));
-    float h = a.weights[slot] * act * u;
+    float h = a.weights[pair[i]] * act * u;
+    if (ti + r >= a.tiles_f) h = 0.f;  // neurons that fill the last block of 128
     // the down projection reads h as bf16 values whose sum is h: two of them
     // keep 16 bits, so that only the output's own rounding is seen in bf16;
     // three keep all 24 for fp32
-    uint16_t* out = a.h + static_cast<int64_t>(slot) * a.h_row + neuron0 + (l & 15);
+    uint16_t* out = a.h + static_cast<int64_t>(pair[i]) * a.h_row + (ti + r) * kTileRows + (l & 15);
 #pragma unroll
     for (int s = 0; s < (E::kBytes == 2 ? 2 : 3); ++s) {
       const uint16_t b = bf16_of(h);
@@ -205,191 +281,198 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, const Tile (&tile)[2
       h -= bf16_bits_to_f32(b);
     }
   }
-  __syncthreads();
 }
 
-template <class E, int BITS, int G, int TQ>
-__global__ __launch_bounds__(kUpWaves* kWave) void moe_up_kernel(MoeArgs a) {
-  __shared__ int ids[kUpPairs];
-  __shared__ int list[kMoeBlockTokens];
-  __shared__ uint8_t taken[kMoeMaxExperts];
-  __shared__ float red[kUpWaves * 2 * token_tiles<TQ>() * (TQ < 4 ? TQ : 4) * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int which = blockIdx.y;  // of the chosen experts, in ascending order
-  const int pairs = a.T * a.k;
-  for (int e = threadIdx.x; e < a.E; e += kUpWaves * kWave) taken[e] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += kUpWaves * kWave) {
-    // a choice of weight 0 is no choice; a NaN weight is one
-    const int id = a.weights[i] == 0.f ? -1 : a.ids[i];
-    ids[i] = id;
-    if (id >= 0) taken[id] = 1;
-  }
-  __syncthreads();
-  int expert = -1, chosen = 0;
-  for (int e0 = 0; e0 < a.E; e0 += 64) {
-    uint64_t has = __ballot(e0 + lane < a.E && taken[e0 + lane] != 0);
-    const int c = __popcll(has);
-    if (expert < 0 && which < chosen + c) {
-      for (int i = chosen; i < which; ++i) has &= has - 1;
-      expert = e0 + __builtin_ctzll(has);
-    }
-    chosen += c;
-  }
-  const bool first = blockIdx.x == 0 && wave == 0;
-  if (first && which == 0 && lane == 0) *a.n_chosen = chosen;
+template <class E, int BITS, int G, int TQ, int NT>
+__global__ __launch_bounds__(kExpertWaves* kWave, 4) void moe_up_kernel(MoeArgs a) {
+  __shared__ WaveList lists[kExpertWaves];
+  __shared__ float red[kExpertWaves * 2 * NT * token_regs<TQ>() * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  WaveList& list = lists[wave];
+  int n;
+  const int expert = find_expert(a, blockIdx.y, list, lane, n);
   if (expert < 0) return;  // the whole workgroup
-  if (wave == 0) {
-    int n = 0, before = 0;
-    for (int i0 = 0; i0 < pairs; i0 += 64) {
-      const int id = i0 + lane < pairs ? ids[i0 + lane] : -1;
-      const uint64_t has = __ballot(id == expert);
-      if (id == expert) list[n + __popcll(has & ((1ull << lane) - 1))] = i0 + lane;
-      n += __popcll(has);
-      before += __popcll(__ballot(id >= 0 && id < expert));
-    }
-    if (lane == 0) ids[0] = n;  // every id has been read
-    if (first) {
-      for (int i = lane; i < n; i += 64) a.pairs[before + i] = list[i];
-      if (lane == 0) a.chosen[which] = MoeChosen{expert, before, n, 0};
-    }
-  }
-  __syncthreads();
-  const int n = ids[0];
-  const int ti = blockIdx.x;
-  const int neuron0 = ti * kTileRows;
-  if (ti >= a.tiles_f) {  // the neurons that fill the last block of 128
-    for (int o = threadIdx.x; o < n * kTileRows; o += kUpWaves * kWave) {
-      uint16_t* out = a.h + static_cast<int64_t>(list[o / kTileRows]) * a.h_row + neuron0 + o % kTileRows;
-#pragma unroll
-      for (int s = 0; s < (E::kBytes == 2 ? 2 : 3); ++s) out[s * a.h_plane] = 0;
-    }
-    return;
-  }
-  const int64_t blk = (static_cast<int64_t>(expert) * a.tiles_f + ti) * a.blocks_d;
-  const Tile tile[2] = {{a.gate_codes + blk * Block<BITS>::kBytes, a.gate_scales + blk * (16 * G)},
-                        {a.up_codes + blk * Block<BITS>::kBytes, a.up_scales + blk * (16 * G)}};
-  if constexpr (TQ <= 4) {
-    up_tokens<E, BITS, G, TQ>(a, tile, list, n, neuron0, red, lane, wave);
-  } else {
-    if (n <= 16) {
-      up_tokens<E, BITS, G, 4>(a, tile, list, n, neuron0, red, lane, wave);
-    } else {
-      for (int i = 0; i < n; i += 4 * TQ)
-        up_tokens<E, BITS, G, TQ>(a, tile, list + i, n - i < 4 * TQ ? n - i : 4 * TQ, neuron0, red, lane, wave);
-    }
+  const int ti = blockIdx.x * NT;
+  for (int i = 0; i < n; i += 16) {
+    if (i > 0) __syncthreads();
+    up_pairs<E, BITS, G, TQ, NT>(a, expert, ti, list.pair + i, n - i < 16 ? n - i : 16, red, lane, wave);
   }
 }
 
 // ---------------------------------------------------------------- down
-// Waves of the down kernel: more than 16 tokens need more registers.
-template <int TQ>
-constexpr int down_waves() { return TQ <= 4 ? 16 : 8; }
-// row sums, pair list and chosen experts of the largest call
-constexpr int kDownLds =
-    (8 * kMoeBlockTokens * kTileRows + kUpPairs) * 4 + kMoeMaxExperts * static_cast<int>(sizeof(MoeChosen));
-
-// Adds blocks [b0, b1) of one expert's down products to its tokens' rows.
-template <int BITS, int G, int TQ, int P>
-__device__ __forceinline__ void down_tokens(const MoeArgs& a, const Tile (&tile)[1], const int* list, int n, int b0,
-                                            int b1, float* mine, int lane) {
+// z[pair] = W_down_e h[pair] for n pairs of one expert and the outputs of NT
+// tiles from tile ti on.
+template <int BITS, int G, int TQ, int NT, int P>
+__device__ __forceinline__ void down_pairs(const MoeArgs& a, int expert, int ti, const int* pair, int n, float* red,
+                                           int lane, int wave) {
   using Row = RowPlanes<P>;
-  using Prod = Product<BITS, G, TQ, 1, Row>;
-  constexpr int MT = Prod::MT;
+  using Prod = Product<BITS, G, TQ, NT, Row>;
+  constexpr int MT = Prod::MT, kOne = MT * Prod::kRegs;
   Row row[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int i = m * 16 + lane_token(lane);
     row[m].stride = a.h_plane;
-    row[m].p = i < n ? a.h + static_cast<int64_t>(list[i]) * a.h_row : nullptr;
+    row[m].p = i < n ? a.h + static_cast<int64_t>(pair[i]) * a.h_row : nullptr;
+  }
+  Tile tile[NT];
+#pragma unroll
+  for (int r = 0; r < NT; ++r) {
+    const int i = ti + r < a.tiles_d ? ti + r : a.tiles_d - 1;
+    const int64_t blk = (static_cast<int64_t>(expert) * a.tiles_d + i) * a.blocks_f;
+    tile[r] = {a.down_codes + blk * Block<BITS>::kBytes, a.down_scales + blk * (16 * G)};
   }
   Prod p;
   p.clear();
-  p.template run<(TQ <= 4 && P == 2 && BITS == 4) ? 2 : 1>(row, tile, b0, b1, b1, lane);
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < Prod::kRegs; ++i) {
-      const int s = m * 16 + result_token(i, lane);
-      if (s < n) mine[(list[s] / a.k) * kTileRows + (lane & 15)] += p.acc[m][0][i];
-    }
+  p.template run<1>(row, tile, a.blocks_f * wave / kExpertWaves, a.blocks_f * (wave + 1) / kExpertWaves, a.blocks_f, lane);
+  p.put(red, wave, lane);
+  __syncthreads();
+  for (int o = threadIdx.x; o < NT * kOne * 64; o += kExpertWaves * kWave) {
+    const int r = o / (kOne * 64), j = o / 64 % kOne, l = o & 63;
+    const int i = (j / Prod::kRegs) * 16 + result_token(j % Prod::kRegs, l);
+    const int out = (ti + r) * kTileRows + (l & 15);
+    if (i < n && out < a.d) a.z[static_cast<int64_t>(pair[i]) * a.d + out] = joined<Prod::kAll>(red, kExpertWaves, o);
+  }
 }
 
-template <class E, int BITS, int G, int TQ>
-__global__ __launch_bounds__(down_waves<TQ>() * kWave) void moe_down_kernel(MoeArgs a) {
+template <class E, int BITS, int G, int TQ, int NT>
+__global__ __launch_bounds__(kExpertWaves* kWave, 4) void moe_down_kernel(MoeArgs a) {
+  __shared__ WaveList lists[kExpertWaves];
+  __shared__ float red[kExpertWaves * NT * token_regs<TQ>() * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  WaveList& list = lists[wave];
+  int n;
+  const int expert = find_expert(a, blockIdx.y, list, lane, n);
+  if (expert < 0) return;
+  const int ti = blockIdx.x * NT;
+  for (int i = 0; i < n; i += 16) {
+    if (i > 0) __syncthreads();
+    down_pairs<BITS, G, TQ, NT, E::kBytes == 2 ? 2 : 3>(a, expert, ti, list.pair + i, n - i < 16 ? n - i : 16, red, lane,
+                                                        wave);
+  }
+}
+
+// y[t] = sum over the choices of z, in the order of the choices.
+template <class E>
+__global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = blockIdx.y;
+  if (n >= a.d) return;
+  float v = 0.f;
+  for (int i = 0; i < a.k; ++i)
+    if (a.weights[t * a.k + i] != 0.f) v += a.z[(t * a.k + i) * a.d + n];
+  const int64_t at = t * a.ldy + n;
+  if constexpr (E::kBytes == 2) static_cast<uint16_t*>(a.y)[at] = bf16_of(v);
+  else static_cast<float*>(a.y)[at] = v;
+}
+
+// Up to four tokens: one workgroup per 16 outputs takes all pairs, its waves
+// splitting (pair, block) among them, and writes y at once.  A pair's hidden
+// values are in its token's row alone, so the sums over the choices form in
+// the result registers.
+constexpr int kFewWaves = 16;
+
+template <class E, int BITS, int G>
+__global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs a) {
   constexpr int P = E::kBytes == 2 ? 2 : 3;
-  constexpr int kDownWaves = down_waves<TQ>();
-  extern __shared__ float lds[];
-  float* sums = lds;  // [waves][T][16]
-  MoeChosen* chosen = reinterpret_cast<MoeChosen*>(sums + kDownWaves * a.T * kTileRows);
-  int* pairs = reinterpret_cast<int*>(chosen + a.most_chosen);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n_chosen = *a.n_chosen;
-  for (int i = threadIdx.x; i < kDownWaves * a.T * kTileRows; i += kDownWaves * kWave) sums[i] = 0.f;
-  for (int i = threadIdx.x; i < n_chosen; i += kDownWaves * kWave) chosen[i] = a.chosen[i];
-  // entries beyond the list's end are not used
-  for (int i = threadIdx.x; i < a.T * a.k; i += kDownWaves * kWave) pairs[i] = a.pairs[i];
-  __syncthreads();
-
-  float* mine = sums + wave * a.T * kTileRows;
+  using Row = RowPlanes<P>;
+  using Prod = Product<BITS, G, 1, 1, Row>;
+  __shared__ float red[kFewWaves * Prod::kAll * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ti = blockIdx.x;
-  const int total = n_chosen * a.blocks_f;
-  int b = static_cast<int>(static_cast<int64_t>(total) * wave / kDownWaves);
-  const int end = static_cast<int>(static_cast<int64_t>(total) * (wave + 1) / kDownWaves);
+  const int total = a.T * a.k * a.blocks_f;
+  int b = total * wave / kFewWaves;
+  const int end = total * (wave + 1) / kFewWaves;
+  Prod p;
+  p.clear();
   while (b < end) {
-    const int c = b / a.blocks_f, b0 = b % a.blocks_f;
+    const int pair = b / a.blocks_f, b0 = b % a.blocks_f;
     const int b1 = b0 + (end - b) < a.blocks_f ? b0 + (end - b) : a.blocks_f;
-    const MoeChosen q = chosen[c];
-    const int64_t blk = (static_cast<int64_t>(q.expert) * a.tiles_d + ti) * a.blocks_f;
-    const Tile tile[1] = {{a.down_codes + blk * Block<BITS>::kBytes, a.down_scales + blk * (16 * G)}};
-    const int* list = pairs + q.first;
-    if constexpr (TQ <= 4) {
-      down_tokens<BITS, G, TQ, P>(a, tile, list, q.n, b0, b1, mine, lane);
-    } else {
-      if (q.n <= 16) {
-        down_tokens<BITS, G, 4, P>(a, tile, list, q.n, b0, b1, mine, lane);
-      } else {
-        for (int i = 0; i < q.n; i += 4 * TQ)
-          down_tokens<BITS, G, TQ, P>(a, tile, list + i, q.n - i < 4 * TQ ? q.n - i : 4 * TQ, b0, b1, mine, lane);
-      }
-    }
     b += b1 - b0;
+    if (a.weights[pair] == 0.f) continue;
+    const int expert = a.ids[pair];
+    Row row[1];
+    row[0].stride = a.h_plane;
+    row[0].p = lane_token(lane) == pair / a.k ? a.h + static_cast<int64_t>(pair) * a.h_row : nullptr;
+    const int64_t blk = (static_cast<int64_t>(expert) * a.tiles_d + ti) * a.blocks_f;
+    const Tile tile[1] = {{a.down_codes + blk * Block<BITS>::kBytes, a.down_scales + blk * (16 * G)}};
+    p.template run<(P == 3 ? 1 : 2)>(row, tile, b0, b1, b1, lane);
   }
+  p.put(red, wave, lane);
   __syncthreads();
-  for (int o = threadIdx.x; o < a.T * kTileRows; o += kDownWaves * kWave) {
-    float v = 0.f;
-    for (int w = 0; w < kDownWaves; ++w) v += sums[w * a.T * kTileRows + o];
-    const int n = ti * kTileRows + o % kTileRows;
-    if (n < a.d) {
-      const int64_t at = static_cast<int64_t>(o / kTileRows) * a.ldy + n;
-      if constexpr (E::kBytes == 2) static_cast<uint16_t*>(a.y)[at] = bf16_of(v);
-      else static_cast<float*>(a.y)[at] = v;
-    }
+  if (threadIdx.x >= 64) return;
+  const int t = result_token(0, lane), n = ti * kTileRows + (lane & 15);
+  if (t < a.T && n < a.d) {
+    const float v = joined<Prod::kAll>(red, kFewWaves, lane);
+    const int64_t at = static_cast<int64_t>(t) * a.ldy + n;
+    if constexpr (E::kBytes == 2) static_cast<uint16_t*>(a.y)[at] = bf16_of(v);
+    else static_cast<float*>(a.y)[at] = v;
   }
 }
 
-template <class E, int BITS, int G, int TQ>
-hipError_t go(const MoeArgs& a, hipStream_t s) {
-  const dim3 up(static_cast<unsigned>(a.blocks_f * (kBlockK / kTileRows)), static_cast<unsigned>(a.most_chosen));
-  moe_up_kernel<E, BITS, G, TQ><<<up, kUpWaves * kWave, 0, s>>>(a);
+template <class E>
+void go_route(const MoeArgs& a, int64_t T, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(T)), block(kRouteWaves * kWave);
+  if (a.E <= 64) moe_route_kernel<E, 1><<<grid, block, 0, s>>>(a);
+  else if (a.E <= 256) moe_route_kernel<E, 4><<<grid, block, 0, s>>>(a);
+  else moe_route_kernel<E, kMoeMaxExperts / 64><<<grid, block, 0, s>>>(a);
+}
+
+template <class E, int BITS, int G, int TQ, int NT>
+hipError_t go_up(const MoeArgs& a, hipStream_t s) {
+  // the tiles that fill the last block of neurons are written too
+  const dim3 grid(static_cast<unsigned>(a.blocks_f * (kBlockK / kTileRows) / NT), static_cast<unsigned>(a.most_chosen));
+  moe_up_kernel<E, BITS, G, TQ, NT><<<grid, kExpertWaves * kWave, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <class E, int BITS, int G, int NT>
+hipError_t go_down(const MoeArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.tiles_d + NT - 1) / NT), static_cast<unsigned>(a.most_chosen));
+  moe_down_kernel<E, BITS, G, 4, NT><<<grid, kExpertWaves * kWave, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  constexpr int kDownWaves = down_waves<TQ>();
-  const size_t lds = (static_cast<size_t>(kDownWaves) * a.T * kTileRows + a.T * a.k) * 4 + a.most_chosen * sizeof(MoeChosen);
-  // the row sums of 64 tokens with the longest lists pass the default limit
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_down_kernel<E, BITS, G, TQ>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kDownLds);
-  if (attr != hipSuccess) return attr;
-  moe_down_kernel<E, BITS, G, TQ><<<a.tiles_d, kDownWaves * kWave, lds, s>>>(a);
+  const dim3 join(static_cast<unsigned>((a.d + 255) / 256), static_cast<unsigned>(a.T));
+  moe_join_kernel<E><<<join, 256, 0, s>>>(a);
   return hipGetLastError();
+}
+
+// Tiles per workgroup: the more, the more of a 4-bit stream is in flight and
+// the less often tokens are fetched, as far as 128 registers go; fewer while
+// that would leave less than two workgroups for a CU.  A tile of bf16 weights
+// is 4 KB a block by itself.
+template <class E, int BITS, int G>
+constexpr int up_tiles() { return BITS == 16 ? 1 : (E::kBytes == 2 ? 4 : 2) / (G == 4 ? 2 : 1); }
+template <class E, int BITS, int G>
+constexpr int down_tiles() { return BITS == 16 ? 2 : E::kBytes == 4 && G == 4 ? 2 : 4; }
+constexpr int64_t kFill = 512;
+
+template <class E, int BITS, int G, int NT>
+hipError_t by_up_tiles(const MoeArgs& a, hipStream_t s) {
+  if constexpr (NT > 1) {
+    if (static_cast<int64_t>(a.tiles_f) * a.most_chosen < NT * kFill) return by_up_tiles<E, BITS, G, NT / 2>(a, s);
+  }
+  return go_up<E, BITS, G, 4, NT>(a, s);
+}
+template <class E, int BITS, int G, int NT>
+hipError_t by_down_tiles(const MoeArgs& a, hipStream_t s) {
+  if constexpr (NT > 1) {
+    if (static_cast<int64_t>(a.tiles_d) * a.most_chosen < NT * kFill) return by_down_tiles<E, BITS, G, NT / 2>(a, s);
+  }
+  return go_down<E, BITS, G, NT>(a, s);
 }
 
 template <class E, int BITS, int G>
 hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
-  if (a.T <= 4) return go<E, BITS, G, 1>(a, s);
-  if (a.T <= 16) return go<E, BITS, G, 4>(a, s);
-  return go<E, BITS, G, 8>(a, s);
+  if (a.T <= 4) {
+    const hipError_t e = go_up<E, BITS, G, 1, 1>(a, s);
+    if (e != hipSuccess) return e;
+    moe_down_few_kernel<E, BITS, G><<<a.tiles_d, kFewWaves * kWave, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const hipError_t e = by_up_tiles<E, BITS, G, up_tiles<E, BITS, G>()>(a, s);
+  if (e != hipSuccess) return e;
+  return by_down_tiles<E, BITS, G, down_tiles<E, BITS, G>()>(a, s);
 }
 
 template <class E>
@@ -403,9 +486,8 @@ hipError_t by_weights(const MoeArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_moe_route(const MoeArgs& a, int64_t T, int dtype, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(T));
-  if (dtype == 0) moe_route_kernel<EF32><<<grid, kRouteWaves * kWave, 0, s>>>(a);
-  else moe_route_kernel<EBf16><<<grid, kRouteWaves * kWave, 0, s>>>(a);
+  if (dtype == 0) go_route<EF32>(a, T, s);
+  else go_route<EBf16>(a, T, s);
   return hipGetLastError();
 }
 

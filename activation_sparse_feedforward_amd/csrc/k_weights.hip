@@ -169,8 +169,8 @@ __global__ __launch_bounds__(kPackWaves* kWave) void weights_unpack_kernel(Weigh
   constexpr int G = scales_per_block<BITS, GROUP>();
   Block<BITS> q;
   q.load(a.codes + blk * Block<BITS>::kBytes, lane);
-  float sc[G];
-  if constexpr (BITS == 4) load_scales<G>(a.scales + blk * (16 * G), lane, sc);
+  Scales<G> sc;
+  if constexpr (BITS == 4) sc.load(a.scales + blk * (16 * G), lane);
   if (row >= a.N) return;
   const int64_t row_off = (e * a.N + row) * a.K;
 #pragma unroll
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(kPackWaves* kWave) void weights_unpack_kernel(Weigh
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int u = static_cast<int>((q.c[s] >> (4 * (i >> 1) + 16 * (i & 1))) & 15u);
-        f[i] = static_cast<float>(u - 8) * sc[s * G / 4];
+        f[i] = static_cast<float>(u - 8) * sc.at(s * G / 4);
       }
     }
     const int k = b * kBlockK + 32 * s + 8 * (lane >> 4);

@@ -194,9 +194,9 @@ twell_status check_moe(const twell_moe_desc* d) {
 }
 
 // Workspace of the mixture of experts: the hidden values of one block of
-// tokens, then the list of chosen experts and their pairs.
+// tokens' (token, choice) pairs, then the pairs' outputs.
 struct MoeWs {
-  size_t h, n_chosen, chosen, pairs, total;
+  size_t h, z, total;
   int64_t h_plane, h_row;
   int32_t block_tokens;
 };
@@ -208,9 +208,7 @@ MoeWs moe_ws(const twell_moe_desc* d) {
   w.h_plane = pairs * w.h_row;
   size_t o = 0;
   w.h = o;        o += align256(static_cast<size_t>(w.h_plane) * 2 * (d->dtype == TWELL_BF16 ? 2 : 3));
-  w.n_chosen = o; o += 256;
-  w.chosen = o;   o += align256(static_cast<size_t>(d->experts) * sizeof(twell::MoeChosen));
-  w.pairs = o;    o += align256(static_cast<size_t>(pairs) * 4);
+  w.z = o;        o += align256(static_cast<size_t>(pairs) * static_cast<size_t>(d->d_model) * 4);
   w.total = o;
   return w;
 }
@@ -680,9 +678,7 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
   a.h = reinterpret_cast<uint16_t*>(wsb + w.h);
   a.h_plane = w.h_plane;
   a.h_row = w.h_row;
-  a.n_chosen = reinterpret_cast<int32_t*>(wsb + w.n_chosen);
-  a.chosen = reinterpret_cast<twell::MoeChosen*>(wsb + w.chosen);
-  a.pairs = reinterpret_cast<int32_t*>(wsb + w.pairs);
+  a.z = reinterpret_cast<float*>(wsb + w.z);
   TWELL_TRY(from_hip(twell::launch_moe_route(a, d->T, d->dtype, s)));
   const int64_t eb = d->dtype == TWELL_BF16 ? 2 : 4;
   for (int64_t t0 = 0; t0 < d->T; t0 += w.block_tokens) {
