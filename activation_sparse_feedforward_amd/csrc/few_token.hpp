@@ -75,58 +75,63 @@ typedef uint32_t u32x4_a2_t __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_a4_t __attribute__((ext_vector_type(4), aligned(4)));
 
 // ---------------------------------------------------------------- token operands
-// One row of the token operand per lane: inputs k .. k+7 as kPlanes bf16
-// operands whose sum is the value.  `whole` says that k + 8 <= K for every lane
-// of the wave; otherwise inputs from K on read as zero.
-struct RowBf16 {
-  static constexpr int kPlanes = 1;
-  const uint16_t* p;  // row, or null for a row without a token
+// The matrix instruction wants 16 tokens at 16 neighbouring lanes, 16 bytes of
+// each: loaded like that, every 16 lanes touch 16 cache lines, which the L1
+// serves one at a time (13 bytes a clock measured, of 64).  More than four
+// tokens therefore come in by rows (16 lanes read 256 consecutive bytes) and
+// go through a piece of LDS that belongs to the wave alone, without a barrier:
+// 16-byte pieces, piece c of row r at place c ^ (r % 16), which spreads both
+// the writes and the reads over the banks.  Up to four tokens are loaded
+// directly (four lines).
+//
+// Source: what a row looks like.  A block of 128 inputs is kParts parts of 16
+// pieces of 16 bytes; kPlanes bf16 operands whose sum is the value come out.
+
+// Rows of bf16 values.
+struct SourceBf16 {
+  using Elem = uint16_t;
+  static constexpr int kPlanes = 1, kParts = 1, kReads = 1;
   int K;
-  __device__ __forceinline__ void load(int k, bool whole, bf16x8_t (&v)[1]) const {
+  // piece c of a part of block b of row p
+  __device__ __forceinline__ u32x4_t piece(const Elem* p, int b, int, int c, bool whole) const {
+    const int k = b * kBlockK + c * 8;
+    if (whole) return *reinterpret_cast<const u32x4_a2_t*>(p + k);
     u32x4_t r{0, 0, 0, 0};
-    if (p != nullptr) {
-      if (whole) {
-        r = *reinterpret_cast<const u32x4_a2_t*>(p + k);
-      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (k + i < K) r[i >> 1] |= static_cast<uint32_t>(p[k + i]) << (16 * (i & 1));
-        }
-      }
-    }
-    v[0] = __builtin_bit_cast(bf16x8_t, r);
+    for (int i = 0; i < 8; ++i)
+      if (k + i < K) r[i >> 1] |= static_cast<uint32_t>(p[k + i]) << (16 * (i & 1));
+    return r;
+  }
+  // the kReads pieces of step s and lane group g (part * 16 + piece), and the
+  // operands made of them
+  static __device__ __forceinline__ int place(int s, int g, int) { return 4 * s + g; }
+  static __device__ __forceinline__ void operands(const u32x4_t (&v)[1], bf16x8_t (&x)[1]) {
+    x[0] = __builtin_bit_cast(bf16x8_t, v[0]);
   }
 };
 
-// An fp32 value is cut (truncated, so that each rest is exact) into three bf16
-// values: 24 bits of mantissa, so products with bf16 weights lose nothing
-// before the fp32 sum.
-struct RowF32 {
-  static constexpr int kPlanes = 3;
-  const float* p;
+// Rows of fp32 values, cut (truncated, so that each rest is exact) into three
+// bf16 values: 24 bits of mantissa, so that products with bf16 weights lose
+// nothing before the fp32 sum.
+struct SourceF32 {
+  using Elem = float;
+  static constexpr int kPlanes = 3, kParts = 2, kReads = 2;
   int K;
-  __device__ __forceinline__ void load(int k, bool whole, bf16x8_t (&v)[3]) const {
-    float f[8] = {};
-    if (p != nullptr) {
-      if (whole) {
-        const u32x4_t a = *reinterpret_cast<const u32x4_a4_t*>(p + k);
-        const u32x4_t b = *reinterpret_cast<const u32x4_a4_t*>(p + k + 4);
+  __device__ __forceinline__ u32x4_t piece(const Elem* p, int b, int part, int c, bool whole) const {
+    const int k = b * kBlockK + part * 64 + c * 4;
+    if (whole) return *reinterpret_cast<const u32x4_a4_t*>(p + k);
+    u32x4_t r{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[i] = __uint_as_float(a[i]);
-          f[4 + i] = __uint_as_float(b[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (k + i < K) f[i] = p[k + i];
-        }
-      }
-    }
+    for (int i = 0; i < 4; ++i)
+      if (k + i < K) r[i] = __float_as_uint(p[k + i]);
+    return r;
+  }
+  static __device__ __forceinline__ int place(int s, int g, int i) { return 8 * s + 2 * g + i; }
+  static __device__ __forceinline__ void operands(const u32x4_t (&v)[2], bf16x8_t (&x)[3]) {
     u32x4_t out[3];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float a = f[2 * j], b = f[2 * j + 1];
+      float a = __uint_as_float(v[j >> 1][2 * (j & 1)]), b = __uint_as_float(v[j >> 1][2 * (j & 1) + 1]);
 #pragma unroll
       for (int s = 0; s < 3; ++s) {
         const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
@@ -136,23 +141,23 @@ struct RowF32 {
       }
     }
 #pragma unroll
-    for (int s = 0; s < 3; ++s) v[s] = __builtin_bit_cast(bf16x8_t, out[s]);
+    for (int s = 0; s < 3; ++s) x[s] = __builtin_bit_cast(bf16x8_t, out[s]);
   }
 };
 
-// A row already cut into P bf16 planes, padded with zeros to whole blocks.
+// Rows already cut into P bf16 planes, padded with zeros to whole blocks.
 template <int P>
-struct RowPlanes {
-  static constexpr int kPlanes = P;
-  const uint16_t* p;
+struct SourcePlanes {
+  using Elem = uint16_t;
+  static constexpr int kPlanes = P, kParts = P, kReads = P;
   int64_t stride;  // between planes, in elements
-  __device__ __forceinline__ void load(int k, bool, bf16x8_t (&v)[P]) const {
+  __device__ __forceinline__ u32x4_t piece(const Elem* p, int b, int part, int c, bool) const {
+    return *reinterpret_cast<const u32x4_t*>(p + (part * stride + b * kBlockK) + c * 8);
+  }
+  static __device__ __forceinline__ int place(int s, int g, int i) { return 16 * i + 4 * s + g; }
+  static __device__ __forceinline__ void operands(const u32x4_t (&v)[P], bf16x8_t (&x)[P]) {
 #pragma unroll
-    for (int s = 0; s < P; ++s) {
-      u32x4_t r{0, 0, 0, 0};
-      if (p != nullptr) r = *reinterpret_cast<const u32x4_t*>(p + s * stride + k);
-      v[s] = __builtin_bit_cast(bf16x8_t, r);
-    }
+    for (int i = 0; i < P; ++i) x[i] = __builtin_bit_cast(bf16x8_t, v[i]);
   }
 };
 
@@ -160,6 +165,92 @@ struct RowPlanes {
 __device__ __forceinline__ int lane_token(int lane) { return ((lane & 3) << 2) | ((lane >> 2) & 3); }
 // Token of result register i in lane l.
 __device__ __forceinline__ int result_token(int i, int lane) { return 4 * i + (lane >> 4); }
+
+// Up to four tokens, loaded as operands.  at(t): the row of token t, null where
+// there is none: it counts as zeros, so that sums over several operands may
+// leave tokens out.
+template <class Src>
+struct DirectTokens {
+  static constexpr int kLdsBytes = 0;
+  Src src;
+  const typename Src::Elem* row;  // of lane_token(lane)
+  struct Loaded {
+    u32x4_t v[4][Src::kReads];
+  };
+  template <class F>
+  __device__ __forceinline__ DirectTokens(Src s, F at, char*, int lane) : src(s), row(at(lane_token(lane))) {}
+  __device__ __forceinline__ void fetch(Loaded& q, int b, bool whole, int lane) const {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < Src::kReads; ++i) {
+        const int at = Src::place(s, lane >> 4, i);
+        q.v[s][i] = u32x4_t{0, 0, 0, 0};
+        if (row != nullptr) q.v[s][i] = src.piece(row, b, at >> 4, at & 15, whole);
+      }
+  }
+  __device__ __forceinline__ void store(const Loaded&, int) const {}
+  __device__ __forceinline__ void step(const Loaded& q, int s, int, int, bf16x8_t (&x)[Src::kPlanes]) const {
+    Src::operands(q.v[s], x);
+  }
+};
+
+// Up to 16 MT tokens, by rows and through LDS.
+template <class Src, int MT>
+struct StagedTokens {
+  static constexpr int kPartBytes = MT * 16 * 256;
+  static constexpr int kLdsBytes = Src::kParts * kPartBytes;  // of one wave
+  static constexpr int kRows = MT * 4;                        // a load takes four rows
+  Src src;
+  const typename Src::Elem* row[kRows];  // row[j]: of token 4 j + lane / 16
+  char* lds;
+  struct Loaded {
+    u32x4_t v[kRows][Src::kParts];
+  };
+  static __device__ __forceinline__ int piece_at(int r, int place) {
+    return (place >> 4) * kPartBytes + r * 256 + (((place & 15) ^ (r & 15)) << 4);
+  }
+  template <class F>
+  __device__ __forceinline__ StagedTokens(Src s, F at, char* lds_, int lane) : src(s), lds(lds_) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) row[j] = at(4 * j + (lane >> 4));
+  }
+  __device__ __forceinline__ void fetch(Loaded& q, int b, bool whole, int lane) const {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+#pragma unroll
+      for (int i = 0; i < Src::kParts; ++i) {
+        q.v[j][i] = u32x4_t{0, 0, 0, 0};
+        if (row[j] != nullptr) q.v[j][i] = src.piece(row[j], b, i, lane & 15, whole);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const Loaded& q, int lane) const {
+    __builtin_amdgcn_wave_barrier();  // the block before has been read
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int i = 0; i < Src::kParts; ++i)
+        *reinterpret_cast<u32x4_t*>(lds + piece_at(4 * j + (lane >> 4), 16 * i + (lane & 15))) = q.v[j][i];
+    __builtin_amdgcn_wave_barrier();
+  }
+  __device__ __forceinline__ void step(const Loaded&, int s, int m, int lane, bf16x8_t (&x)[Src::kPlanes]) const {
+    u32x4_t v[Src::kReads];
+#pragma unroll
+    for (int i = 0; i < Src::kReads; ++i)
+      v[i] = *reinterpret_cast<const u32x4_t*>(lds + piece_at(m * 16 + lane_token(lane), Src::place(s, lane >> 4, i)));
+    Src::operands(v, x);
+  }
+};
+
+// The operand for TQ quads of tokens.
+template <int TQ>
+constexpr int token_tiles() { return (TQ + 3) / 4; }
+// Result registers in use per tile of 16 tokens.
+template <int TQ>
+constexpr int token_regs() { return TQ < 4 ? TQ : 4; }
+template <class Src, int TQ>
+using Tokens = std::conditional_t<TQ == 1, DirectTokens<Src>, StagedTokens<Src, token_tiles<TQ>()>>;
 
 // ---------------------------------------------------------------- weights
 template <int BITS>
@@ -219,16 +310,11 @@ struct Scales {
 // tokens (1: up to 4 tokens, 4 / 8 / 16: up to 16 / 32 / 64); MT = tiles of 16
 // tokens.  G: 4-bit scales per block (1, 2, 4), unused for 16 bits.  nfull:
 // blocks whose inputs are all below K.
-template <int TQ>
-constexpr int token_tiles() { return (TQ + 3) / 4; }
-// Result registers in use per tile of 16 tokens.
-template <int TQ>
-constexpr int token_regs() { return TQ < 4 ? TQ : 4; }
-
-template <int BITS, int G, int TQ, int NR, class Row>
+template <int BITS, int G, int TQ, int NR, class Src>
 struct Product {
+  using X = Tokens<Src, TQ>;
   static constexpr int MT = token_tiles<TQ>();
-  static constexpr int P = Row::kPlanes;
+  static constexpr int P = Src::kPlanes;
   static constexpr int kRegs = token_regs<TQ>();
   static constexpr int kAll = NR * MT * kRegs;  // result registers
   static constexpr bool kExact = P == 3;        // fp32 data: codes without the offset
@@ -242,18 +328,14 @@ struct Product {
   }
 
   struct Loaded {
-    bf16x8_t x[MT][4][P];
+    typename X::Loaded x;
     Block<BITS> w[NR];
     Scales<G> s[NR];
   };
 
-  static __device__ __forceinline__ void fetch(Loaded& q, const Row (&row)[MT], const Tile (&tile)[NR], int b,
-                                               bool whole, int lane) {
-    const int k = b * kBlockK + (lane >> 4) * 8;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) row[m].load(k + 32 * s, whole, q.x[m][s]);
+  static __device__ __forceinline__ void fetch(Loaded& q, const X& x, const Tile (&tile)[NR], int b, bool whole,
+                                               int lane) {
+    x.fetch(q.x, b, whole, lane);
 #pragma unroll
     for (int r = 0; r < NR; ++r) q.w[r].load(tile[r].codes + static_cast<int64_t>(b) * Block<BITS>::kBytes, lane);
     if constexpr (BITS == 4) {
@@ -262,18 +344,22 @@ struct Product {
     }
   }
 
-  __device__ __forceinline__ void use(const Loaded& q) {
+  __device__ __forceinline__ void use(const Loaded& q, const X& x, int lane) {
+    x.store(q.x, lane);
+    const f32x4_t zero{0.f, 0.f, 0.f, 0.f};
     if constexpr (BITS == 16) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < 4; ++s) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const bf16x8_t b = q.w[r].template step<true>(s);
+        for (int m = 0; m < MT; ++m) {
+          bf16x8_t v[P];
+          x.step(q.x, s, m, lane, v);
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int p = P - 1; p >= 0; --p) acc[m][r] = mfma16(q.x[m][s][p], b, acc[m][r]);
+            for (int p = P - 1; p >= 0; --p) acc[m][r] = mfma16(v[p], q.w[r].template step<true>(s), acc[m][r]);
         }
+      }
     } else {
       constexpr int kSteps = 4 / G;  // steps that share a scale
       const bf16x8_t off = offset_operand();
@@ -281,33 +367,70 @@ struct Product {
       for (int gr = 0; gr < G; ++gr) {
         f32x4_t base[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          base[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int m = 0; m < MT; ++m) base[m] = zero;
+        auto offset = [&](int m, const bf16x8_t(&v)[P]) {
           if constexpr (!kExact) {
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-              for (int p = P - 1; p >= 0; --p) base[m] = mfma16(q.x[m][gr * kSteps + s][p], off, base[m]);
+            for (int p = P - 1; p >= 0; --p) base[m] = mfma16(v[p], off, base[m]);
           }
-        }
+        };
+        auto product = [&](f32x4_t& t, const bf16x8_t(&v)[P], bf16x8_t w) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          f32x4_t t[MT];
-#pragma unroll
-          for (int m = 0; m < MT; ++m) t[m] = base[m];
-#pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            const bf16x8_t b = q.w[r].template step<kExact>(gr * kSteps + s);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int p = P - 1; p >= 0; --p) t[m] = mfma16(q.x[m][gr * kSteps + s][p], b, t[m]);
-          }
+          for (int p = P - 1; p >= 0; --p) t = mfma16(v[p], w, t);
+        };
+        auto scaled = [&](int m, int r, const f32x4_t& t) {
           const float sc = q.s[r].at(gr);
+#pragma unroll
+          for (int i = 0; i < kRegs; ++i) acc[m][r][i] = fmaf(sc, kExact ? t[i] : t[i] + base[m][i], acc[m][r][i]);
+        };
+        if constexpr (kSteps * P <= NR) {  // fewer registers: all steps' tokens, then tile by tile
+          bf16x8_t v[MT][kSteps][P];
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < kRegs; ++i) acc[m][r][i] = fmaf(sc, t[m][i], acc[m][r][i]);
+            for (int i = 0; i < kSteps; ++i) {
+              x.step(q.x, gr * kSteps + i, m, lane, v[m][i]);
+              offset(m, v[m][i]);
+            }
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            f32x4_t t[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) t[m] = zero;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              const bf16x8_t w = q.w[r].template step<kExact>(gr * kSteps + i);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) product(t[m], v[m][i], w);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) scaled(m, r, t[m]);
+          }
+        } else {  // step by step, all tiles
+          f32x4_t t[MT][NR];
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) t[m][r] = zero;
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            bf16x8_t v[MT][P];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              x.step(q.x, gr * kSteps + i, m, lane, v[m]);
+              offset(m, v[m]);
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const bf16x8_t w = q.w[r].template step<kExact>(gr * kSteps + i);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) product(t[m][r], v[m], w);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) scaled(m, r, t[m][r]);
         }
       }
     }
@@ -315,28 +438,27 @@ struct Product {
 
   // U blocks are fetched together.
   template <int U>
-  __device__ __forceinline__ void run(const Row (&row)[MT], const Tile (&tile)[NR], int b0, int b1, int nfull,
-                                      int lane) {
+  __device__ __forceinline__ void run(const X& x, const Tile (&tile)[NR], int b0, int b1, int nfull, int lane) {
     int b = b0;
     const int whole_end = b1 < nfull ? b1 : nfull;
     if constexpr (U > 1) {
       for (; b + U <= whole_end; b += U) {
         Loaded q[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) fetch(q[u], row, tile, b + u, true, lane);
+        for (int u = 0; u < U; ++u) fetch(q[u], x, tile, b + u, true, lane);
 #pragma unroll
-        for (int u = 0; u < U; ++u) use(q[u]);
+        for (int u = 0; u < U; ++u) use(q[u], x, lane);
       }
     }
     for (; b < whole_end; ++b) {
       Loaded q;
-      fetch(q, row, tile, b, true, lane);
-      use(q);
+      fetch(q, x, tile, b, true, lane);
+      use(q, x, lane);
     }
     for (; b < b1; ++b) {
       Loaded q;
-      fetch(q, row, tile, b, false, lane);
-      use(q);
+      fetch(q, x, tile, b, false, lane);
+      use(q, x, lane);
     }
   }
 

@@ -183,8 +183,7 @@ struct LinearArgs {
   int32_t N, K, group, tiles, blocks;
 };
 
-// Mixture of experts for at most kMoeBlockTokens tokens at a time (the router
-// takes any number).
+// Mixture of experts for at most kMoeBlockTokens tokens at a time.
 constexpr int kMoeBlockTokens = 64;
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 32;
@@ -201,6 +200,7 @@ struct MoeArgs {
   int32_t T, E, k, d, f, bits, group, act, renorm;
   int32_t tiles_f, blocks_d, tiles_d, blocks_f, most_chosen;
   // workspace
+  int32_t* live;       // [T x k] ids, or -1 where the weight is 0
   uint16_t* h;         // [planes][T * k][blocks_f * 128] hidden values of each (token, choice) pair
   int64_t h_plane, h_row;
   float* z;            // [T * k][d] the pairs' outputs (more than four tokens)
@@ -229,8 +229,7 @@ hipError_t launch_bwd_dense(const BwdArgs& a, int dtype, hipStream_t s);
 hipError_t launch_weights_pack(const WeightsArgs& a, int dtype, bool transposed, hipStream_t s);
 hipError_t launch_weights_unpack(const WeightsArgs& a, int dtype, hipStream_t s);
 hipError_t launch_linear4(const LinearArgs& a, int dtype, hipStream_t s);
-hipError_t launch_moe_route(const MoeArgs& a, int64_t T, int dtype, hipStream_t s);
-hipError_t launch_moe_experts(const MoeArgs& a, int dtype, hipStream_t s);
+hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t s);
 
 // Lockstep launches: how many workgroups of one lockstep kernel (one per CU)
 // the current device runs at once; 0 if it cannot be queried.

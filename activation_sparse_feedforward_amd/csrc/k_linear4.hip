@@ -10,29 +10,27 @@
 namespace twell {
 namespace {
 
-// More results per wave need more registers, so fewer waves per workgroup.
-template <int TQ, int NR>
-constexpr int max_waves() { return NR * token_tiles<TQ>() * token_regs<TQ>() <= 16 ? 16 : 8; }
+// Waves of a workgroup, as registers and LDS (the waves' sums) allow.
+template <class E, int TQ, int NR>
+constexpr int max_waves() {
+  return E::kBytes == 2 ? (NR * token_tiles<TQ>() <= 6 ? 16 : 8) : TQ == 1 || (TQ == 4 && NR <= 3) ? 16 : 8;
+}
 
 template <class E, int G, int TQ, int NR>
-__global__ __launch_bounds__((max_waves<TQ, NR>() * kWave)) void linear4_kernel(LinearArgs a) {
-  extern __shared__ float red[];
-  using Row = std::conditional_t<E::kBytes == 2, RowBf16, RowF32>;
+__global__ __launch_bounds__((max_waves<E, TQ, NR>() * kWave)) void linear4_kernel(LinearArgs a) {
+  extern __shared__ __align__(16) char lds[];  // the waves' token pieces, then their sums
+  using Src = std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>;
   using Elem = typename E::storage;
-  using Prod = Product<4, G, TQ, NR, Row>;
+  using Prod = Product<4, G, TQ, NR, Src>;
   constexpr int MT = Prod::MT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * (4 * TQ);
   const int T = a.T - t0 < 4 * TQ ? static_cast<int>(a.T - t0) : 4 * TQ;
 
-  Row row[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int t = m * 16 + lane_token(lane);
-    row[m].K = a.K;
-    row[m].p = t < T ? static_cast<const Elem*>(a.x) + (t0 + t) * a.ldx : nullptr;
-  }
+  const typename Prod::X x(
+      Src{a.K}, [&](int t) { return t < T ? static_cast<const Elem*>(a.x) + (t0 + t) * a.ldx : nullptr; },
+      lds + wave * Prod::X::kLdsBytes, lane);
   Tile tile[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
@@ -44,7 +42,9 @@ __global__ __launch_bounds__((max_waves<TQ, NR>() * kWave)) void linear4_kernel(
   Prod p;
   p.clear();
   const int b0 = a.blocks * wave / waves, b1 = a.blocks * (wave + 1) / waves;
-  p.template run<(Prod::kAll <= 4 && E::kBytes == 2) ? 2 : 1>(row, tile, b0, b1, a.K / kBlockK, lane);
+  p.template run<1>(x, tile, b0, b1, a.K / kBlockK, lane);
+  float* red = reinterpret_cast<float*>(lds);
+  if constexpr (Prod::X::kLdsBytes > 0) __syncthreads();  // the pieces have been read
   p.put(red, wave, lane);
   __syncthreads();
   for (int o = threadIdx.x; o < Prod::kAll * 64; o += blockDim.x) {
@@ -62,48 +62,58 @@ __global__ __launch_bounds__((max_waves<TQ, NR>() * kWave)) void linear4_kernel(
 }
 
 template <class E, int G, int TQ, int NR>
-void go(const LinearArgs& a, hipStream_t s) {
-  constexpr int kAll = NR * token_tiles<TQ>() * token_regs<TQ>();
-  int waves = max_waves<TQ, NR>();
+hipError_t go(const LinearArgs& a, hipStream_t s) {
+  using Prod = Product<4, G, TQ, NR, std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>>;
+  constexpr int kPerWave = Prod::kAll * 256 > Prod::X::kLdsBytes ? Prod::kAll * 256 : Prod::X::kLdsBytes;
+  constexpr int kWaves = max_waves<E, TQ, NR>();
+  if constexpr (kWaves * kPerWave > 64 * 1024) {
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear4_kernel<E, G, TQ, NR>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kWaves * kPerWave);
+    if (attr != hipSuccess) return attr;
+  }
+  int waves = kWaves;
   while (waves > 1 && waves > a.blocks) waves >>= 1;
   const dim3 grid((a.tiles + NR - 1) / NR, static_cast<unsigned>((a.T + 4 * TQ - 1) / (4 * TQ)));
-  linear4_kernel<E, G, TQ, NR><<<grid, waves * kWave, waves * kAll * 64 * sizeof(float), s>>>(a);
+  linear4_kernel<E, G, TQ, NR><<<grid, waves * kWave, waves * kPerWave, s>>>(a);
+  return hipGetLastError();
 }
 
-// The most tiles per workgroup that still leave a workgroup for every CU.
-template <class E, int G, int TQ, int NR>
-void by_rows(const LinearArgs& a, int cus, hipStream_t s) {
+// The fewest tiles per workgroup that leave no more than one workgroup for a
+// CU, so that all run at once.
+template <class E, int G, int TQ, int NR, int kMost>
+hipError_t by_rows(const LinearArgs& a, int cus, hipStream_t s) {
   const int64_t groups = (a.T + 4 * TQ - 1) / (4 * TQ);
-  if constexpr (NR > 1) {
-    if ((a.tiles + NR - 1) / NR * groups < cus) {
-      by_rows<E, G, TQ, NR / 2>(a, cus, s);
-      return;
-    }
+  if constexpr (NR < kMost) {
+    if ((a.tiles + NR - 1) / NR * groups > cus) return by_rows<E, G, TQ, NR + 1, kMost>(a, cus, s);
   }
-  go<E, G, TQ, NR>(a, s);
+  return go<E, G, TQ, NR>(a, s);
 }
 
 template <class E, int G>
-void by_tokens(const LinearArgs& a, hipStream_t s) {
-  const int cus = 256;
-  if (a.T <= 4) by_rows<E, G, 1, (E::kBytes == 2 ? 8 : 4) / (G == 4 ? 4 : 1)>(a, cus, s);
-  else if (a.T <= 16) by_rows<E, G, 4, 4>(a, cus, s);
-  else by_rows<E, G, 8, E::kBytes == 2 ? 2 : 1>(a, cus, s);
+hipError_t by_tokens(const LinearArgs& a, hipStream_t s) {
+  const int cus = lockstep_resident() > 0 ? lockstep_resident() : 256;
+  if (a.T <= 4) return by_rows<E, G, 1, 1, 4>(a, cus, s);
+  if (a.T <= 16) return by_rows<E, G, 4, 1, 4>(a, cus, s);
+  if constexpr (E::kBytes == 2) {
+    // 64 tokens a workgroup save unpacking the codes twice, once that still
+    // leaves a workgroup for every CU
+    if (a.T > 32 && (a.tiles + 2) / 3 * ((a.T + 63) / 64) >= cus) return go<E, G, 16, 3>(a, s);
+    return by_rows<E, G, 8, 1, 4>(a, cus, s);
+  }
+  return by_rows<E, G, 8, 1, 2>(a, cus, s);
 }
 
 template <class E>
-void by_group(const LinearArgs& a, hipStream_t s) {
-  if (a.group == 32) by_tokens<E, 4>(a, s);
-  else if (a.group == 64) by_tokens<E, 2>(a, s);
-  else by_tokens<E, 1>(a, s);
+hipError_t by_group(const LinearArgs& a, hipStream_t s) {
+  if (a.group == 32) return by_tokens<E, 4>(a, s);
+  if (a.group == 64) return by_tokens<E, 2>(a, s);
+  return by_tokens<E, 1>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_linear4(const LinearArgs& a, int dtype, hipStream_t s) {
-  if (dtype == 0) by_group<EF32>(a, s);
-  else by_group<EBf16>(a, s);
-  return hipGetLastError();
+  return dtype == 0 ? by_group<EF32>(a, s) : by_group<EBf16>(a, s);
 }
 
 }  // namespace twell

@@ -137,7 +137,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
     if (r * 64 + lane < a.E) sum += expf(logit[r * 64 + lane] - most);
   sum = wave_sum(sum);
 
-  float mine = 0.f, chosen = 0.f;  // lane i keeps choice i
+  uint32_t mine_key = 0;  // lane i keeps choice i
   int mine_id = 0;
   for (int i = 0; i < a.k; ++i) {
     uint32_t m = 0;
@@ -154,23 +154,23 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
         if (lane == l) key[r] = 0;
       }
     }
-    const float w = none ? 0.f : expf(key_value(m) - most) / sum;
-    chosen += w;
     if (lane == i) {
-      mine = w;
+      mine_key = m;
       mine_id = id;
     }
   }
-  if (a.renorm && !none) mine /= chosen;
+  float mine = lane < a.k && !none ? expf(key_value(mine_key) - most) / sum : 0.f;
+  if (a.renorm && !none) mine /= wave_sum(mine);
   if (lane < a.k) {
     a.ids[t * a.k + lane] = mine_id;
     a.weights[t * a.k + lane] = mine;
+    // a choice of weight 0 is no choice; a NaN weight is one
+    a.live[t * a.k + lane] = mine == 0.f ? -1 : mine_id;
   }
 }
 
 // ---------------------------------------------------------------- expert lists
 constexpr int kExpertWaves = 8;
-constexpr int kPairsAhead = 8;  // pairs per lane held at once
 
 // Where one wave works out its expert and the expert's pairs.  Every wave does
 // so for itself, without a barrier: the pairs come from the L2 once, and
@@ -181,9 +181,10 @@ struct WaveList {
 };
 
 // Finds the `which`-th chosen expert (ascending) and its (token, choice) pairs
-// (ascending) in the lists of the router; a choice of weight 0 is no choice, a
-// NaN weight is one.  Returns the expert, or -1 if there are not that many; n:
+// (ascending) in the list of the router (a.live).  Returns the expert, or -1 if there are not that many; n:
 // its pairs.
+// kPairsAhead: pairs per lane held at once.
+template <int kPairsAhead>
 __device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList& l, int lane, int& n) {
   const int pairs = a.T * a.k;
   n = 0;
@@ -193,12 +194,11 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList
 #pragma unroll
     for (int u = 0; u < kPairsAhead; ++u) {
       const int i = i0 + u * 64 + lane;
-      id[u] = -1;
-      if (i < pairs) {
-        const int e = a.ids[i];
-        if (a.weights[i] != 0.f) id[u] = e;
-      }
+      id[u] = a.live[i < pairs ? i : pairs - 1];  // all loads at once: no branch
     }
+#pragma unroll
+    for (int u = 0; u < kPairsAhead; ++u)
+      if (i0 + u * 64 + lane >= pairs) id[u] = -1;
   };
   for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
     fetch(i0);
@@ -229,23 +229,27 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList
   return expert;
 }
 
+// LDS of the token pieces, and of the waves' sums after them.
+template <class Prod>
+constexpr int expert_lds() {
+  return kExpertWaves * (Prod::kAll * 256 > Prod::X::kLdsBytes ? Prod::kAll * 256 : Prod::X::kLdsBytes);
+}
+
 // ---------------------------------------------------------------- gate and up
 // h = w act(g) u for n pairs of one expert and the neurons of NT tiles from
 // tile ti on.
 template <class E, int BITS, int G, int TQ, int NT>
-__device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, const int* pair, int n, float* red,
+__device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, const int* pair, int n, char* lds,
                                          int lane, int wave) {
-  using Row = std::conditional_t<E::kBytes == 2, RowBf16, RowF32>;
+  using Src = std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>;
   using Elem = typename E::storage;
-  using Prod = Product<BITS, G, TQ, 2 * NT, Row>;
+  using Prod = Product<BITS, G, TQ, 2 * NT, Src>;
   constexpr int MT = Prod::MT, kOne = MT * Prod::kRegs;  // registers of one tile
-  Row row[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int i = m * 16 + lane_token(lane);
-    row[m].K = a.d;
-    row[m].p = i < n ? static_cast<const Elem*>(a.x) + static_cast<int64_t>(pair[i] / a.k) * a.ldx : nullptr;
-  }
+  const typename Prod::X x(
+      Src{a.d},
+      [&](int i) { return i < n ? static_cast<const Elem*>(a.x) + static_cast<int64_t>(pair[i] / a.k) * a.ldx : nullptr; },
+      lds + wave * Prod::X::kLdsBytes, lane);
+  float* red = reinterpret_cast<float*>(lds);
   Tile tile[2 * NT];
 #pragma unroll
   for (int r = 0; r < NT; ++r) {
@@ -256,8 +260,9 @@ __device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, c
   }
   Prod p;
   p.clear();
-  p.template run<(NT == 1 && MT == 1 && E::kBytes == 2) ? 2 : 1>(
-      row, tile, a.blocks_d * wave / kExpertWaves, a.blocks_d * (wave + 1) / kExpertWaves, a.d / kBlockK, lane);
+  p.template run<TQ == 1 && E::kBytes == 2 ? 2 : 1>(
+      x, tile, a.blocks_d * wave / kExpertWaves, a.blocks_d * (wave + 1) / kExpertWaves, a.d / kBlockK, lane);
+  if constexpr (Prod::X::kLdsBytes > 0) __syncthreads();  // the token pieces have been read
   p.put(red, wave, lane);
   __syncthreads();
   for (int o = threadIdx.x; o < NT * kOne * 64; o += kExpertWaves * kWave) {
@@ -286,16 +291,17 @@ __device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, c
 template <class E, int BITS, int G, int TQ, int NT>
 __global__ __launch_bounds__(kExpertWaves* kWave, 4) void moe_up_kernel(MoeArgs a) {
   __shared__ WaveList lists[kExpertWaves];
-  __shared__ float red[kExpertWaves * 2 * NT * token_regs<TQ>() * 64];
+  using Src = std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>;
+  __shared__ __align__(16) char lds[expert_lds<Product<BITS, G, TQ, 2 * NT, Src>>()];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   WaveList& list = lists[wave];
   int n;
-  const int expert = find_expert(a, blockIdx.y, list, lane, n);
+  const int expert = find_expert<(TQ == 1 ? 2 : 8)>(a, blockIdx.y, list, lane, n);
   if (expert < 0) return;  // the whole workgroup
   const int ti = blockIdx.x * NT;
   for (int i = 0; i < n; i += 16) {
     if (i > 0) __syncthreads();
-    up_pairs<E, BITS, G, TQ, NT>(a, expert, ti, list.pair + i, n - i < 16 ? n - i : 16, red, lane, wave);
+    up_pairs<E, BITS, G, TQ, NT>(a, expert, ti, list.pair + i, n - i < 16 ? n - i : 16, lds, lane, wave);
   }
 }
 
@@ -303,18 +309,15 @@ __global__ __launch_bounds__(kExpertWaves* kWave, 4) void moe_up_kernel(MoeArgs 
 // z[pair] = W_down_e h[pair] for n pairs of one expert and the outputs of NT
 // tiles from tile ti on.
 template <int BITS, int G, int TQ, int NT, int P>
-__device__ __forceinline__ void down_pairs(const MoeArgs& a, int expert, int ti, const int* pair, int n, float* red,
+__device__ __forceinline__ void down_pairs(const MoeArgs& a, int expert, int ti, const int* pair, int n, char* lds,
                                            int lane, int wave) {
-  using Row = RowPlanes<P>;
-  using Prod = Product<BITS, G, TQ, NT, Row>;
+  using Src = SourcePlanes<P>;
+  using Prod = Product<BITS, G, TQ, NT, Src>;
   constexpr int MT = Prod::MT, kOne = MT * Prod::kRegs;
-  Row row[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int i = m * 16 + lane_token(lane);
-    row[m].stride = a.h_plane;
-    row[m].p = i < n ? a.h + static_cast<int64_t>(pair[i]) * a.h_row : nullptr;
-  }
+  const typename Prod::X x(
+      Src{a.h_plane}, [&](int i) { return i < n ? a.h + static_cast<int64_t>(pair[i]) * a.h_row : nullptr; },
+      lds + wave * Prod::X::kLdsBytes, lane);
+  float* red = reinterpret_cast<float*>(lds);
   Tile tile[NT];
 #pragma unroll
   for (int r = 0; r < NT; ++r) {
@@ -324,7 +327,8 @@ __device__ __forceinline__ void down_pairs(const MoeArgs& a, int expert, int ti,
   }
   Prod p;
   p.clear();
-  p.template run<1>(row, tile, a.blocks_f * wave / kExpertWaves, a.blocks_f * (wave + 1) / kExpertWaves, a.blocks_f, lane);
+  p.template run<1>(x, tile, a.blocks_f * wave / kExpertWaves, a.blocks_f * (wave + 1) / kExpertWaves, a.blocks_f, lane);
+  if constexpr (Prod::X::kLdsBytes > 0) __syncthreads();  // the token pieces have been read
   p.put(red, wave, lane);
   __syncthreads();
   for (int o = threadIdx.x; o < NT * kOne * 64; o += kExpertWaves * kWave) {
@@ -338,17 +342,17 @@ __device__ __forceinline__ void down_pairs(const MoeArgs& a, int expert, int ti,
 template <class E, int BITS, int G, int TQ, int NT>
 __global__ __launch_bounds__(kExpertWaves* kWave, 4) void moe_down_kernel(MoeArgs a) {
   __shared__ WaveList lists[kExpertWaves];
-  __shared__ float red[kExpertWaves * NT * token_regs<TQ>() * 64];
+  constexpr int P = E::kBytes == 2 ? 2 : 3;
+  __shared__ __align__(16) char lds[expert_lds<Product<BITS, G, TQ, NT, SourcePlanes<P>>>()];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   WaveList& list = lists[wave];
   int n;
-  const int expert = find_expert(a, blockIdx.y, list, lane, n);
+  const int expert = find_expert<(TQ == 1 ? 2 : 8)>(a, blockIdx.y, list, lane, n);
   if (expert < 0) return;
   const int ti = blockIdx.x * NT;
   for (int i = 0; i < n; i += 16) {
     if (i > 0) __syncthreads();
-    down_pairs<BITS, G, TQ, NT, E::kBytes == 2 ? 2 : 3>(a, expert, ti, list.pair + i, n - i < 16 ? n - i : 16, red, lane,
-                                                        wave);
+    down_pairs<BITS, G, TQ, NT, P>(a, expert, ti, list.pair + i, n - i < 16 ? n - i : 16, lds, lane, wave);
   }
 }
 
@@ -360,7 +364,7 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
   if (n >= a.d) return;
   float v = 0.f;
   for (int i = 0; i < a.k; ++i)
-    if (a.weights[t * a.k + i] != 0.f) v += a.z[(t * a.k + i) * a.d + n];
+    if (a.live[t * a.k + i] >= 0) v += a.z[(t * a.k + i) * a.d + n];
   const int64_t at = t * a.ldy + n;
   if constexpr (E::kBytes == 2) static_cast<uint16_t*>(a.y)[at] = bf16_of(v);
   else static_cast<float*>(a.y)[at] = v;
@@ -375,8 +379,8 @@ constexpr int kFewWaves = 16;
 template <class E, int BITS, int G>
 __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs a) {
   constexpr int P = E::kBytes == 2 ? 2 : 3;
-  using Row = RowPlanes<P>;
-  using Prod = Product<BITS, G, 1, 1, Row>;
+  using Src = SourcePlanes<P>;
+  using Prod = Product<BITS, G, 1, 1, Src>;
   __shared__ float red[kFewWaves * Prod::kAll * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ti = blockIdx.x;
@@ -389,14 +393,15 @@ __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs 
     const int pair = b / a.blocks_f, b0 = b % a.blocks_f;
     const int b1 = b0 + (end - b) < a.blocks_f ? b0 + (end - b) : a.blocks_f;
     b += b1 - b0;
-    if (a.weights[pair] == 0.f) continue;
-    const int expert = a.ids[pair];
-    Row row[1];
-    row[0].stride = a.h_plane;
-    row[0].p = lane_token(lane) == pair / a.k ? a.h + static_cast<int64_t>(pair) * a.h_row : nullptr;
+    const int expert = a.live[pair];
+    if (expert < 0) continue;
+    const typename Prod::X x(
+        Src{a.h_plane},
+        [&](int t) { return t == pair / a.k ? a.h + static_cast<int64_t>(pair) * a.h_row : nullptr; },
+        nullptr, lane);
     const int64_t blk = (static_cast<int64_t>(expert) * a.tiles_d + ti) * a.blocks_f;
     const Tile tile[1] = {{a.down_codes + blk * Block<BITS>::kBytes, a.down_scales + blk * (16 * G)}};
-    p.template run<(P == 3 ? 1 : 2)>(row, tile, b0, b1, b1, lane);
+    p.template run<(P == 3 ? 1 : 2)>(x, tile, b0, b1, b1, lane);
   }
   p.put(red, wave, lane);
   __syncthreads();
@@ -411,11 +416,12 @@ __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs 
 }
 
 template <class E>
-void go_route(const MoeArgs& a, int64_t T, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(T)), block(kRouteWaves * kWave);
+hipError_t go_route(const MoeArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.T)), block(kRouteWaves * kWave);
   if (a.E <= 64) moe_route_kernel<E, 1><<<grid, block, 0, s>>>(a);
   else if (a.E <= 256) moe_route_kernel<E, 4><<<grid, block, 0, s>>>(a);
   else moe_route_kernel<E, kMoeMaxExperts / 64><<<grid, block, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 template <class E, int BITS, int G, int TQ, int NT>
@@ -477,6 +483,8 @@ hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
 
 template <class E>
 hipError_t by_weights(const MoeArgs& a, hipStream_t s) {
+  const hipError_t e = go_route<E>(a, s);
+  if (e != hipSuccess) return e;
   if (a.bits == 16) return by_tokens<E, 16, 1>(a, s);
   if (a.group == 32) return by_tokens<E, 4, 4>(a, s);
   if (a.group == 64) return by_tokens<E, 4, 2>(a, s);
@@ -485,13 +493,7 @@ hipError_t by_weights(const MoeArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_moe_route(const MoeArgs& a, int64_t T, int dtype, hipStream_t s) {
-  if (dtype == 0) go_route<EF32>(a, T, s);
-  else go_route<EBf16>(a, T, s);
-  return hipGetLastError();
-}
-
-hipError_t launch_moe_experts(const MoeArgs& a, int dtype, hipStream_t s) {
+hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t s) {
   return dtype == 0 ? by_weights<EF32>(a, s) : by_weights<EBf16>(a, s);
 }
 

@@ -194,9 +194,10 @@ twell_status check_moe(const twell_moe_desc* d) {
 }
 
 // Workspace of the mixture of experts: the hidden values of one block of
-// tokens' (token, choice) pairs, then the pairs' outputs.
+// tokens' (token, choice) pairs, the pairs' outputs, and the choices that
+// count.
 struct MoeWs {
-  size_t h, z, total;
+  size_t h, z, live, total;
   int64_t h_plane, h_row;
   int32_t block_tokens;
 };
@@ -209,6 +210,7 @@ MoeWs moe_ws(const twell_moe_desc* d) {
   size_t o = 0;
   w.h = o;        o += align256(static_cast<size_t>(w.h_plane) * 2 * (d->dtype == TWELL_BF16 ? 2 : 3));
   w.z = o;        o += align256(static_cast<size_t>(pairs) * static_cast<size_t>(d->d_model) * 4);
+  w.live = o;     o += align256(static_cast<size_t>(pairs) * 4);
   w.total = o;
   return w;
 }
@@ -679,7 +681,7 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
   a.h_plane = w.h_plane;
   a.h_row = w.h_row;
   a.z = reinterpret_cast<float*>(wsb + w.z);
-  TWELL_TRY(from_hip(twell::launch_moe_route(a, d->T, d->dtype, s)));
+  a.live = reinterpret_cast<int32_t*>(wsb + w.live);
   const int64_t eb = d->dtype == TWELL_BF16 ? 2 : 4;
   for (int64_t t0 = 0; t0 < d->T; t0 += w.block_tokens) {
     a.T = static_cast<int32_t>(d->T - t0 < w.block_tokens ? d->T - t0 : w.block_tokens);
@@ -689,7 +691,7 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
     a.weights = weights + t0 * d->top_k;
     const int64_t pairs = static_cast<int64_t>(a.T) * d->top_k;
     a.most_chosen = static_cast<int32_t>(pairs < d->experts ? pairs : d->experts);
-    TWELL_TRY(from_hip(twell::launch_moe_experts(a, d->dtype, s)));
+    TWELL_TRY(from_hip(twell::launch_moe(a, d->dtype, s)));
   }
   return TWELL_OK;
 }
