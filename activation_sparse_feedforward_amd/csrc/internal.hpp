@@ -187,6 +187,9 @@ struct LinearArgs {
 constexpr int kMoeBlockTokens = 64;
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 32;
+struct MoeChosen {
+  int32_t expert, n;  // -1: none; pairs
+};
 struct MoeArgs {
   const void* x;
   void* y;
@@ -203,6 +206,8 @@ struct MoeArgs {
   int32_t* live;       // [T x k] ids, or -1 where the weight is 0
   uint16_t* h;         // [planes][T * k][blocks_f * 128] hidden values of each (token, choice) pair
   int64_t h_plane, h_row;
+  MoeChosen* chosen;   // [most_chosen] experts with a token, ascending
+  int32_t* chosen_pairs;  // [most_chosen][kMoeBlockTokens] their (token, choice) pairs, ascending
   float* z;            // [T * k][d] the pairs' outputs (more than four tokens)
 };
 

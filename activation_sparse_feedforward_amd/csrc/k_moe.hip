@@ -45,7 +45,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-// Eight inputs as loaded, and as fp32.
+// Eight inputs of a row.
 template <class E>
 struct Eight {
   u32x4_t v[E::kBytes / 2];
@@ -57,9 +57,18 @@ struct Eight {
       v[1] = *reinterpret_cast<const u32x4_a4_t*>(p + 4);
     }
   }
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (E::kBytes == 2) return __uint_as_float(i & 1 ? v[0][i >> 1] & 0xffff0000u : v[0][i >> 1] << 16);
-    else return __uint_as_float(v[i >> 2][i & 3]);
+  // s += this . o; bf16 by pairs: products of bf16 values are exact in fp32
+  __device__ __forceinline__ float dot(const Eight& o, float s) const {
+    if constexpr (E::kBytes == 2) {
+      const bf16x8_t a = __builtin_bit_cast(bf16x8_t, v[0]), b = __builtin_bit_cast(bf16x8_t, o.v[0]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{a[2 * i], a[2 * i + 1]}, bf16x2_t{b[2 * i], b[2 * i + 1]}, s, false);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(__uint_as_float(v[i >> 2][i & 3]), __uint_as_float(o.v[i >> 2][i & 3]), s);
+    }
+    return s;
   }
 };
 
@@ -79,9 +88,7 @@ __device__ __forceinline__ void route_dots(const typename E::storage* x, const t
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int j = 0; j < kRouteAhead; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[j] = fmaf(xv[u].at(i), rv[u][j].at(i), s[j]);
+    for (int j = 0; j < kRouteAhead; ++j) s[j] = xv[u].dot(rv[u][j], s[j]);
 }
 
 // kRegs * 64 >= E.
@@ -89,7 +96,7 @@ template <class E, int kRegs>
 __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a) {
   __shared__ float logit[kRegs * 64];
   using Elem = typename E::storage;
-  constexpr int U = 2;
+  constexpr int U = E::kBytes == 2 ? 4 : 2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x;
   const Elem* x = static_cast<const Elem*>(a.x) + t * a.ldx;
@@ -170,25 +177,38 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
 }
 
 // ---------------------------------------------------------------- expert lists
-constexpr int kExpertWaves = 8;
+// Waves of a workgroup.  Four workgroups of four waves on a CU are more often at
+// different points of their work than two of eight (64 tokens, 64 experts, 4
+// bits: down 27.6 -> 23.7 us); with few tokens there is one wave of workgroups
+// and more waves have more in flight (1 token: up 7.6 -> 7.1 us).
+template <int TQ>
+constexpr int expert_waves() { return TQ == 1 ? 8 : 4; }
 
 // Where one wave works out its expert and the expert's pairs.  Every wave does
 // so for itself, without a barrier: the pairs come from the L2 once, and
 // what follows are LDS and lane operations of a few hundred cycles.
 struct WaveList {
-  uint32_t taken[kMoeMaxExperts / 32];
+  uint8_t taken[kMoeMaxExperts];  // more than 64 experts
   int pair[kMoeBlockTokens];
 };
 
+__device__ __forceinline__ uint32_t wave_or(uint32_t v) {
+  v |= dpp_take<0xB1>(static_cast<int>(v));
+  v |= dpp_take<0x4E>(static_cast<int>(v));
+  v |= dpp_take<0x141>(static_cast<int>(v));
+  v |= dpp_take<0x140>(static_cast<int>(v));
+  v |= dpp_take<0x142, 0xa>(static_cast<int>(v));
+  v |= dpp_take<0x143, 0xc>(static_cast<int>(v));
+  return static_cast<uint32_t>(wave_last(static_cast<int>(v)));
+}
+
 // Finds the `which`-th chosen expert (ascending) and its (token, choice) pairs
-// (ascending) in the list of the router (a.live).  Returns the expert, or -1 if there are not that many; n:
-// its pairs.
-// kPairsAhead: pairs per lane held at once.
+// (ascending) in the list of the router (a.live).  Returns the expert, or -1 if
+// there are not that many; n: its pairs.  kPairsAhead: pairs per lane held at
+// once.
 template <int kPairsAhead>
 __device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList& l, int lane, int& n) {
   const int pairs = a.T * a.k;
-  n = 0;
-  if (lane < kMoeMaxExperts / 32) l.taken[lane] = 0;
   int id[kPairsAhead];
   auto fetch = [&](int i0) {
 #pragma unroll
@@ -200,22 +220,41 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList
     for (int u = 0; u < kPairsAhead; ++u)
       if (i0 + u * 64 + lane >= pairs) id[u] = -1;
   };
-  for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
-    fetch(i0);
+  int expert = -1, before = 0;  // chosen experts below the 64 looked at
+  auto look = [&](int e0, uint64_t has) {
+    const int c = __popcll(has);
+    if (expert < 0 && which < before + c) {
+      for (int i = before; i < which; ++i) has &= has - 1;
+      expert = e0 + __builtin_ctzll(has);
+    }
+    before += c;
+  };
+  if (a.E <= 64) {
+    uint32_t lo = 0, hi = 0;
+    for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
+      fetch(i0);
 #pragma unroll
-    for (int u = 0; u < kPairsAhead; ++u)
-      if (id[u] >= 0) atomicOr(&l.taken[id[u] >> 5], 1u << (id[u] & 31));
+      for (int u = 0; u < kPairsAhead; ++u) {
+        const uint32_t bit = id[u] < 0 ? 0u : 1u << (id[u] & 31);
+        lo |= id[u] < 32 ? bit : 0u;
+        hi |= id[u] < 32 ? 0u : bit;
+      }
+    }
+    look(0, static_cast<uint64_t>(wave_or(hi)) << 32 | wave_or(lo));
+  } else {
+    reinterpret_cast<u32x4_t*>(l.taken)[lane] = u32x4_t{0, 0, 0, 0};
+    __builtin_amdgcn_wave_barrier();
+    for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
+      fetch(i0);
+#pragma unroll
+      for (int u = 0; u < kPairsAhead; ++u)
+        if (id[u] >= 0) l.taken[id[u]] = 1;
+    }
+    __builtin_amdgcn_wave_barrier();
+    for (int e0 = 0; e0 < a.E; e0 += 64) look(e0, __ballot(l.taken[e0 + lane] != 0));
   }
-  __builtin_amdgcn_wave_barrier();
-  uint32_t word = lane < kMoeMaxExperts / 32 ? l.taken[lane] : 0u;
-  const int count = __popc(word);
-  const int upto = wave_incl_scan(count);
-  const uint64_t at = __ballot(which < upto);
-  if (at == 0) return -1;
-  const int owner = __builtin_ctzll(at);
-  const int skip = which - (upto - count);  // set bits before it, in the owner's word
-  for (int i = 0; i < __builtin_amdgcn_readlane(skip, owner); ++i) word &= word - 1;
-  const int expert = owner * 32 + __builtin_ctz(__builtin_amdgcn_readlane(word, owner));
+  if (expert < 0) return -1;
+  n = 0;
   for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
     if (pairs > kPairsAhead * 64) fetch(i0);
 #pragma unroll
@@ -230,7 +269,7 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList
 }
 
 // LDS of the token pieces, and of the waves' sums after them.
-template <class Prod>
+template <class Prod, int kExpertWaves>
 constexpr int expert_lds() {
   return kExpertWaves * (Prod::kAll * 256 > Prod::X::kLdsBytes ? Prod::kAll * 256 : Prod::X::kLdsBytes);
 }
@@ -244,6 +283,7 @@ __device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, c
   using Src = std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>;
   using Elem = typename E::storage;
   using Prod = Product<BITS, G, TQ, 2 * NT, Src>;
+  constexpr int kExpertWaves = expert_waves<TQ>();
   constexpr int MT = Prod::MT, kOne = MT * Prod::kRegs;  // registers of one tile
   const typename Prod::X x(
       Src{a.d},
@@ -289,14 +329,19 @@ __device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, c
 }
 
 template <class E, int BITS, int G, int TQ, int NT>
-__global__ __launch_bounds__(kExpertWaves* kWave, 4) void moe_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(expert_waves<TQ>() * kWave, 4) void moe_up_kernel(MoeArgs a) {
+  constexpr int kExpertWaves = expert_waves<TQ>();
   __shared__ WaveList lists[kExpertWaves];
   using Src = std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>;
-  __shared__ __align__(16) char lds[expert_lds<Product<BITS, G, TQ, 2 * NT, Src>>()];
+  __shared__ __align__(16) char lds[expert_lds<Product<BITS, G, TQ, 2 * NT, Src>, kExpertWaves>()];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   WaveList& list = lists[wave];
-  int n;
+  int n = 0;
   const int expert = find_expert<(TQ == 1 ? 2 : 8)>(a, blockIdx.y, list, lane, n);
+  if (TQ > 1 && blockIdx.x == 0 && wave == 0) {  // for the down kernel
+    if (lane == 0) a.chosen[blockIdx.y] = MoeChosen{expert, n};
+    if (lane < n) a.chosen_pairs[blockIdx.y * kMoeBlockTokens + lane] = list.pair[lane];
+  }
   if (expert < 0) return;  // the whole workgroup
   const int ti = blockIdx.x * NT;
   for (int i = 0; i < n; i += 16) {
@@ -313,6 +358,7 @@ __device__ __forceinline__ void down_pairs(const MoeArgs& a, int expert, int ti,
                                            int lane, int wave) {
   using Src = SourcePlanes<P>;
   using Prod = Product<BITS, G, TQ, NT, Src>;
+  constexpr int kExpertWaves = expert_waves<TQ>();
   constexpr int MT = Prod::MT, kOne = MT * Prod::kRegs;
   const typename Prod::X x(
       Src{a.h_plane}, [&](int i) { return i < n ? a.h + static_cast<int64_t>(pair[i]) * a.h_row : nullptr; },
@@ -340,31 +386,44 @@ __device__ __forceinline__ void down_pairs(const MoeArgs& a, int expert, int ti,
 }
 
 template <class E, int BITS, int G, int TQ, int NT>
-__global__ __launch_bounds__(kExpertWaves* kWave, 4) void moe_down_kernel(MoeArgs a) {
-  __shared__ WaveList lists[kExpertWaves];
+__global__ __launch_bounds__(expert_waves<TQ>() * kWave, 4) void moe_down_kernel(MoeArgs a) {
+  constexpr int kExpertWaves = expert_waves<TQ>();
   constexpr int P = E::kBytes == 2 ? 2 : 3;
-  __shared__ __align__(16) char lds[expert_lds<Product<BITS, G, TQ, NT, SourcePlanes<P>>>()];
+  __shared__ __align__(16) char lds[expert_lds<Product<BITS, G, TQ, NT, SourcePlanes<P>>, kExpertWaves>()];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  WaveList& list = lists[wave];
-  int n;
-  const int expert = find_expert<(TQ == 1 ? 2 : 8)>(a, blockIdx.y, list, lane, n);
+  const MoeChosen c = a.chosen[blockIdx.y];
+  const int expert = c.expert, n = c.n;
   if (expert < 0) return;
+  const int* pair = a.chosen_pairs + blockIdx.y * kMoeBlockTokens;
   const int ti = blockIdx.x * NT;
   for (int i = 0; i < n; i += 16) {
     if (i > 0) __syncthreads();
-    down_pairs<BITS, G, TQ, NT, P>(a, expert, ti, list.pair + i, n - i < 16 ? n - i : 16, lds, lane, wave);
+    down_pairs<BITS, G, TQ, NT, P>(a, expert, ti, pair + i, n - i < 16 ? n - i : 16, lds, lane, wave);
   }
 }
 
 // y[t] = sum over the choices of z, in the order of the choices.
 template <class E>
 __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
+  constexpr int U = 8;
   const int n = blockIdx.x * 256 + threadIdx.x;
   const int64_t t = blockIdx.y;
   if (n >= a.d) return;
+  const int* live = a.live + t * a.k;
+  const float* z = a.z + t * a.k * a.d + n;
   float v = 0.f;
-  for (int i = 0; i < a.k; ++i)
-    if (a.live[t * a.k + i] >= 0) v += a.z[(t * a.k + i) * a.d + n];
+  for (int i0 = 0; i0 < a.k; i0 += U) {
+    float part[U];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u < a.k ? i0 + u : a.k - 1;
+      part[u] = z[static_cast<int64_t>(i) * a.d];  // of a choice that does not count: anything
+      on[u] = (i0 + u < a.k) & (live[i] >= 0);  // no branch: all loads at once
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) v += on[u] ? part[u] : 0.f;
+  }
   const int64_t at = t * a.ldy + n;
   if constexpr (E::kBytes == 2) static_cast<uint16_t*>(a.y)[at] = bf16_of(v);
   else static_cast<float*>(a.y)[at] = v;
@@ -428,14 +487,14 @@ template <class E, int BITS, int G, int TQ, int NT>
 hipError_t go_up(const MoeArgs& a, hipStream_t s) {
   // the tiles that fill the last block of neurons are written too
   const dim3 grid(static_cast<unsigned>(a.blocks_f * (kBlockK / kTileRows) / NT), static_cast<unsigned>(a.most_chosen));
-  moe_up_kernel<E, BITS, G, TQ, NT><<<grid, kExpertWaves * kWave, 0, s>>>(a);
+  moe_up_kernel<E, BITS, G, TQ, NT><<<grid, expert_waves<TQ>() * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <class E, int BITS, int G, int NT>
 hipError_t go_down(const MoeArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.tiles_d + NT - 1) / NT), static_cast<unsigned>(a.most_chosen));
-  moe_down_kernel<E, BITS, G, 4, NT><<<grid, kExpertWaves * kWave, 0, s>>>(a);
+  moe_down_kernel<E, BITS, G, 4, NT><<<grid, expert_waves<4>() * kWave, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 join(static_cast<unsigned>((a.d + 255) / 256), static_cast<unsigned>(a.T));

@@ -194,10 +194,10 @@ twell_status check_moe(const twell_moe_desc* d) {
 }
 
 // Workspace of the mixture of experts: the hidden values of one block of
-// tokens' (token, choice) pairs, the pairs' outputs, and the choices that
-// count.
+// tokens' (token, choice) pairs, the pairs' outputs, the choices that count, and
+// the chosen experts with their pairs.
 struct MoeWs {
-  size_t h, z, live, total;
+  size_t h, z, live, chosen, chosen_pairs, total;
   int64_t h_plane, h_row;
   int32_t block_tokens;
 };
@@ -211,6 +211,9 @@ MoeWs moe_ws(const twell_moe_desc* d) {
   w.h = o;        o += align256(static_cast<size_t>(w.h_plane) * 2 * (d->dtype == TWELL_BF16 ? 2 : 3));
   w.z = o;        o += align256(static_cast<size_t>(pairs) * static_cast<size_t>(d->d_model) * 4);
   w.live = o;     o += align256(static_cast<size_t>(pairs) * 4);
+  const size_t chosen = static_cast<size_t>(pairs < d->experts ? pairs : d->experts);
+  w.chosen = o;       o += align256(chosen * sizeof(twell::MoeChosen));
+  w.chosen_pairs = o; o += align256(chosen * twell::kMoeBlockTokens * 4);
   w.total = o;
   return w;
 }
@@ -682,6 +685,8 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
   a.h_row = w.h_row;
   a.z = reinterpret_cast<float*>(wsb + w.z);
   a.live = reinterpret_cast<int32_t*>(wsb + w.live);
+  a.chosen = reinterpret_cast<twell::MoeChosen*>(wsb + w.chosen);
+  a.chosen_pairs = reinterpret_cast<int32_t*>(wsb + w.chosen_pairs);
   const int64_t eb = d->dtype == TWELL_BF16 ? 2 : 4;
   for (int64_t t0 = 0; t0 < d->T; t0 += w.block_tokens) {
     a.T = static_cast<int32_t>(d->T - t0 < w.block_tokens ? d->T - t0 : w.block_tokens);
