@@ -11,8 +11,9 @@
 //   16 bits: step s of lane l is the 16-byte piece (s * 64 + l) of the block (4 KB).
 //    4 bits: the 16-byte piece l of the block (1 KB) is lane l's four words,
 //            one per step; a word holds the codes u = q + 8 of its eight
-//            inputs, input 2j in bits 4j .. 4j+3 and input 2j+1 in bits
-//            16+4j .. 16+4j+3.  Scales: bf16, [block][16 rows][128 / group].
+//            inputs, rotated left by three bits: input 2j in bits 4j+3 .. 4j+6
+//            and input 2j+1 in bits 4j+19 .. 4j+22 (bit numbers modulo 32).
+//            Scales: bf16, [block][16 rows][128 / group].
 //
 // The matrix instruction takes tokens as its 16 rows and weight rows as its 16
 // columns, so a lane's four results belong to one weight row: the group scale
@@ -35,17 +36,23 @@ __device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
 // fp32 -> bf16 bits, round to nearest even, NaN stays NaN.
 __device__ __forceinline__ uint16_t bf16_of(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
 
-// Eight 4-bit codes as bf16 values 16 + u: u lands in mantissa bits 3 .. 6 of
-// 16.0 (bit pattern 0x4180), so a pair costs one shift and one and-or.  The
-// offset 16 + 8 is taken off again by a product with -24 (offset_operand).  For
-// bf16 data: its sums are rounded to 8 bits in the end.
+// A constant in a vector register: v_and_or_b32 takes no literals and one scalar.
+__device__ __forceinline__ uint32_t vector_constant(uint32_t c) {
+  uint32_t v;
+  asm("v_mov_b32 %0, %1" : "=v"(v) : "s"(c));
+  return v;
+}
+
+// Eight 4-bit codes as bf16 values 16 + u: u belongs into mantissa bits 3 .. 6 of
+// 16.0 (bit pattern 0x4180), where the first pair is already; the other pairs
+// cost one rotation, every pair one and-or.  The offset 16 + 8 is taken off
+// again by a product with -24 (offset_operand).  For bf16 data: its sums are
+// rounded to 8 bits in the end.
 __device__ __forceinline__ bf16x8_t codes_operand(uint32_t w) {
-  constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;
+  const uint32_t mask = vector_constant(0x00780078u), base = vector_constant(0x41804180u);
   u32x4_t r;
-  r[0] = ((w << 3) & kMask) | kBase;
-  r[1] = ((w >> 1) & kMask) | kBase;
-  r[2] = ((w >> 5) & kMask) | kBase;
-  r[3] = ((w >> 9) & kMask) | kBase;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = (__builtin_rotateright32(w, 4 * j) & mask) | base;
   return __builtin_bit_cast(bf16x8_t, r);
 }
 __device__ __forceinline__ bf16x8_t offset_operand() {
@@ -59,7 +66,7 @@ __device__ __forceinline__ bf16x8_t offset_operand() {
 // an error of 1.1e-6 of the result's norm (64 x 4096 weights, groups of 32),
 // one-sided; fp32 products of the plain kind have 3e-7.
 __device__ __forceinline__ bf16x8_t exact_codes_operand(uint32_t w) {
-  const int v = static_cast<int>(w ^ 0x88888888u);  // u = q + 8 to two's complement
+  const int v = static_cast<int>(__builtin_rotateright32(w, 3) ^ 0x88888888u);  // u = q + 8 to two's complement
   u32x4_t r;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -195,17 +202,19 @@ struct DirectTokens {
   }
 };
 
-// Up to 16 MT tokens, by rows and through LDS.
-template <class Src, int MT>
+// Up to 4 TQ tokens, by rows and through LDS.  at(t) is a row for every t; where
+// there is no token it is any other one, whose results nobody reads (a matrix
+// row's results depend on that row alone; the same holds for the rows of a tile
+// of 16 that are never written).
+template <class Src, int TQ>
 struct StagedTokens {
-  static constexpr int kPartBytes = MT * 16 * 256;
+  static constexpr int kPartBytes = (TQ + 3) / 4 * 16 * 256;
   static constexpr int kLdsBytes = Src::kParts * kPartBytes;  // of one wave
-  static constexpr int kRows = MT * 4;                        // a load takes four rows
   Src src;
-  const typename Src::Elem* row[kRows];  // row[j]: of token 4 j + lane / 16
+  const typename Src::Elem* row[TQ];  // row[j]: of token 4 j + lane / 16; a load takes four rows
   char* lds;
   struct Loaded {
-    u32x4_t v[kRows][Src::kParts];
+    u32x4_t v[TQ][Src::kParts];
   };
   static __device__ __forceinline__ int piece_at(int r, int place) {
     return (place >> 4) * kPartBytes + r * 256 + (((place & 15) ^ (r & 15)) << 4);
@@ -213,22 +222,18 @@ struct StagedTokens {
   template <class F>
   __device__ __forceinline__ StagedTokens(Src s, F at, char* lds_, int lane) : src(s), lds(lds_) {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) row[j] = at(4 * j + (lane >> 4));
+    for (int j = 0; j < TQ; ++j) row[j] = at(4 * j + (lane >> 4));
   }
   __device__ __forceinline__ void fetch(Loaded& q, int b, bool whole, int lane) const {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
+    for (int j = 0; j < TQ; ++j)
 #pragma unroll
-      for (int i = 0; i < Src::kParts; ++i) {
-        q.v[j][i] = u32x4_t{0, 0, 0, 0};
-        if (row[j] != nullptr) q.v[j][i] = src.piece(row[j], b, i, lane & 15, whole);
-      }
-    }
+      for (int i = 0; i < Src::kParts; ++i) q.v[j][i] = src.piece(row[j], b, i, lane & 15, whole);
   }
   __device__ __forceinline__ void store(const Loaded& q, int lane) const {
     __builtin_amdgcn_wave_barrier();  // the block before has been read
 #pragma unroll
-    for (int j = 0; j < kRows; ++j)
+    for (int j = 0; j < TQ; ++j)
 #pragma unroll
       for (int i = 0; i < Src::kParts; ++i)
         *reinterpret_cast<u32x4_t*>(lds + piece_at(4 * j + (lane >> 4), 16 * i + (lane & 15))) = q.v[j][i];
@@ -250,17 +255,25 @@ constexpr int token_tiles() { return (TQ + 3) / 4; }
 template <int TQ>
 constexpr int token_regs() { return TQ < 4 ? TQ : 4; }
 template <class Src, int TQ>
-using Tokens = std::conditional_t<TQ == 1, DirectTokens<Src>, StagedTokens<Src, token_tiles<TQ>()>>;
+using Tokens = std::conditional_t<TQ == 1, DirectTokens<Src>, StagedTokens<Src, TQ>>;
 
 // ---------------------------------------------------------------- weights
+// STREAM: past the caches, for weights that are read once and are larger than
+// what stays in them.
+template <bool STREAM>
+__device__ __forceinline__ u32x4_t load_codes(const uint8_t* p) {
+  const u32x4_t* q = reinterpret_cast<const u32x4_t*>(p);
+  return STREAM ? __builtin_nontemporal_load(q) : *q;
+}
 template <int BITS>
 struct Block;
 template <>
 struct Block<4> {
   static constexpr int kBytes = 1024;
   u32x4_t c;
+  template <bool STREAM>
   __device__ __forceinline__ void load(const uint8_t* p, int lane) {
-    c = *reinterpret_cast<const u32x4_t*>(p + lane * 16);
+    c = load_codes<STREAM>(p + lane * 16);
   }
   template <bool EXACT>
   __device__ __forceinline__ bf16x8_t step(int s) const {
@@ -271,9 +284,10 @@ template <>
 struct Block<16> {
   static constexpr int kBytes = 4096;
   u32x4_t c[4];
+  template <bool STREAM>
   __device__ __forceinline__ void load(const uint8_t* p, int lane) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) c[s] = *reinterpret_cast<const u32x4_t*>(p + (s * 64 + lane) * 16);
+    for (int s = 0; s < 4; ++s) c[s] = load_codes<STREAM>(p + (s * 64 + lane) * 16);
   }
   template <bool>
   __device__ __forceinline__ bf16x8_t step(int s) const { return __builtin_bit_cast(bf16x8_t, c[s]); }
@@ -306,11 +320,25 @@ struct Scales {
   }
 };
 
+// One block of each of NR tiles.
+template <int BITS, int G, int NR, bool STREAM>
+struct TileBlocks {
+  Block<BITS> w[NR];
+  Scales<G> s[NR];
+  __device__ __forceinline__ void fetch(const Tile (&tile)[NR], int b, int lane) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) w[r].template load<STREAM>(tile[r].codes + static_cast<int64_t>(b) * Block<BITS>::kBytes, lane);
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) s[r].load(tile[r].scales + static_cast<int64_t>(b) * (16 * G), lane);
+    }
+  }
+};
+
 // acc += tokens x weights over blocks [b0, b1) of NR tiles.  TQ: quads of
-// tokens (1: up to 4 tokens, 4 / 8 / 16: up to 16 / 32 / 64); MT = tiles of 16
-// tokens.  G: 4-bit scales per block (1, 2, 4), unused for 16 bits.  nfull:
+// tokens (1, 2 or a multiple of 4); MT = tiles of 16 tokens.  G: 4-bit scales per block (1, 2, 4), unused for 16 bits.  nfull:
 // blocks whose inputs are all below K.
-template <int BITS, int G, int TQ, int NR, class Src>
+template <int BITS, int G, int TQ, int NR, class Src, bool STREAM = false>
 struct Product {
   using X = Tokens<Src, TQ>;
   static constexpr int MT = token_tiles<TQ>();
@@ -327,25 +355,11 @@ struct Product {
       for (int r = 0; r < NR; ++r) acc[m][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
 
-  struct Loaded {
-    typename X::Loaded x;
-    Block<BITS> w[NR];
-    Scales<G> s[NR];
-  };
+  using Weights = TileBlocks<BITS, G, NR, STREAM>;
+  using XLoaded = typename X::Loaded;
 
-  static __device__ __forceinline__ void fetch(Loaded& q, const X& x, const Tile (&tile)[NR], int b, bool whole,
-                                               int lane) {
-    x.fetch(q.x, b, whole, lane);
-#pragma unroll
-    for (int r = 0; r < NR; ++r) q.w[r].load(tile[r].codes + static_cast<int64_t>(b) * Block<BITS>::kBytes, lane);
-    if constexpr (BITS == 4) {
-#pragma unroll
-      for (int r = 0; r < NR; ++r) q.s[r].load(tile[r].scales + static_cast<int64_t>(b) * (16 * G), lane);
-    }
-  }
-
-  __device__ __forceinline__ void use(const Loaded& q, const X& x, int lane) {
-    x.store(q.x, lane);
+  __device__ __forceinline__ void use(const XLoaded& xq, const Weights& w, const X& x, int lane) {
+    x.store(xq, lane);
     const f32x4_t zero{0.f, 0.f, 0.f, 0.f};
     if constexpr (BITS == 16) {
 #pragma unroll
@@ -353,11 +367,11 @@ struct Product {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           bf16x8_t v[P];
-          x.step(q.x, s, m, lane, v);
+          x.step(xq, s, m, lane, v);
 #pragma unroll
           for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int p = P - 1; p >= 0; --p) acc[m][r] = mfma16(v[p], q.w[r].template step<true>(s), acc[m][r]);
+            for (int p = P - 1; p >= 0; --p) acc[m][r] = mfma16(v[p], w.w[r].template step<true>(s), acc[m][r]);
         }
       }
     } else {
@@ -379,29 +393,31 @@ struct Product {
           for (int p = P - 1; p >= 0; --p) t = mfma16(v[p], w, t);
         };
         auto scaled = [&](int m, int r, const f32x4_t& t) {
-          const float sc = q.s[r].at(gr);
+          const float sc = w.s[r].at(gr);
 #pragma unroll
-          for (int i = 0; i < kRegs; ++i) acc[m][r][i] = fmaf(sc, kExact ? t[i] : t[i] + base[m][i], acc[m][r][i]);
+          for (int i = 0; i < kRegs; ++i) acc[m][r][i] = fmaf(sc, t[i], acc[m][r][i]);
         };
-        if constexpr (kSteps * P <= NR) {  // fewer registers: all steps' tokens, then tile by tile
+        if constexpr (!kExact && MT * kSteps * P <= 8) {
+          // all steps' tokens, then tile by tile, so that a tile's sum starts
+          // from the offset's
           bf16x8_t v[MT][kSteps][P];
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-              x.step(q.x, gr * kSteps + i, m, lane, v[m][i]);
+              x.step(xq, gr * kSteps + i, m, lane, v[m][i]);
               offset(m, v[m][i]);
             }
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
             f32x4_t t[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) t[m] = zero;
+            for (int m = 0; m < MT; ++m) t[m] = base[m];
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-              const bf16x8_t w = q.w[r].template step<kExact>(gr * kSteps + i);
+              const bf16x8_t c = w.w[r].template step<kExact>(gr * kSteps + i);
 #pragma unroll
-              for (int m = 0; m < MT; ++m) product(t[m], v[m][i], w);
+              for (int m = 0; m < MT; ++m) product(t[m], v[m][i], c);
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) scaled(m, r, t[m]);
@@ -417,49 +433,53 @@ struct Product {
             bf16x8_t v[MT][P];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              x.step(q.x, gr * kSteps + i, m, lane, v[m]);
+              x.step(xq, gr * kSteps + i, m, lane, v[m]);
               offset(m, v[m]);
             }
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-              const bf16x8_t w = q.w[r].template step<kExact>(gr * kSteps + i);
+              const bf16x8_t c = w.w[r].template step<kExact>(gr * kSteps + i);
 #pragma unroll
-              for (int m = 0; m < MT; ++m) product(t[m][r], v[m], w);
+              for (int m = 0; m < MT; ++m) product(t[m][r], v[m], c);
             }
           }
 #pragma unroll
           for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) scaled(m, r, t[m][r]);
+            for (int m = 0; m < MT; ++m) scaled(m, r, kExact ? t[m][r] : t[m][r] + base[m]);
         }
       }
     }
   }
 
-  // U blocks are fetched together.
+  // The weights of U blocks are on their way together.
   template <int U>
   __device__ __forceinline__ void run(const X& x, const Tile (&tile)[NR], int b0, int b1, int nfull, int lane) {
     int b = b0;
     const int whole_end = b1 < nfull ? b1 : nfull;
     if constexpr (U > 1) {
       for (; b + U <= whole_end; b += U) {
-        Loaded q[U];
+        Weights w[U];
+        XLoaded xq[2];
+        x.fetch(xq[0], b, true, lane);
 #pragma unroll
-        for (int u = 0; u < U; ++u) fetch(q[u], x, tile, b + u, true, lane);
+        for (int u = 0; u < U; ++u) w[u].fetch(tile, b + u, lane);
 #pragma unroll
-        for (int u = 0; u < U; ++u) use(q[u], x, lane);
+        for (int u = 0; u < U; ++u) {
+          if (u + 1 < U) x.fetch(xq[(u + 1) & 1], b + u + 1, true, lane);
+          use(xq[u & 1], w[u], x, lane);
+        }
       }
     }
-    for (; b < whole_end; ++b) {
-      Loaded q;
-      fetch(q, x, tile, b, true, lane);
-      use(q, x, lane);
-    }
-    for (; b < b1; ++b) {
-      Loaded q;
-      fetch(q, x, tile, b, false, lane);
-      use(q, x, lane);
-    }
+    for (; b < whole_end; ++b) one_block(x, tile, b, true, lane);
+    for (; b < b1; ++b) one_block(x, tile, b, false, lane);
+  }
+  __device__ __forceinline__ void one_block(const X& x, const Tile (&tile)[NR], int b, bool whole, int lane) {
+    XLoaded xq;
+    Weights w;
+    x.fetch(xq, b, whole, lane);
+    w.fetch(tile, b, lane);
+    use(xq, w, x, lane);
   }
 
   // The wave's sums to LDS: register j = (r, m, i) of lane l at

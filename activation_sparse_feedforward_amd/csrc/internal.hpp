@@ -188,7 +188,7 @@ constexpr int kMoeBlockTokens = 64;
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 32;
 struct MoeChosen {
-  int32_t expert, n;  // -1: none; pairs
+  int32_t expert, n;  // n: pairs, 0 if there is nothing to do
 };
 struct MoeArgs {
   const void* x;
@@ -202,11 +202,13 @@ struct MoeArgs {
   int64_t ldx, ldy;
   int32_t T, E, k, d, f, bits, group, act, renorm;
   int32_t tiles_f, blocks_d, tiles_d, blocks_f, most_chosen;
+  float inv_k;        // 1 / k
+  int32_t by_expert;  // more than four tokens: row y of the grids is expert y, not the y-th chosen one
   // workspace
   int32_t* live;       // [T x k] ids, or -1 where the weight is 0
   uint16_t* h;         // [planes][T * k][blocks_f * 128] hidden values of each (token, choice) pair
   int64_t h_plane, h_row;
-  MoeChosen* chosen;   // [most_chosen] experts with a token, ascending
+  MoeChosen* chosen;   // [most_chosen] what row y of the grids works on
   int32_t* chosen_pairs;  // [most_chosen][kMoeBlockTokens] their (token, choice) pairs, ascending
   float* z;            // [T * k][d] the pairs' outputs (more than four tokens)
 };

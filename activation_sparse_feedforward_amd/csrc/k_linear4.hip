@@ -13,7 +13,7 @@ namespace {
 // Waves of a workgroup, as registers and LDS (the waves' sums) allow.
 template <class E, int TQ, int NR>
 constexpr int max_waves() {
-  return E::kBytes == 2 ? (NR * token_tiles<TQ>() <= 6 ? 16 : 8) : TQ == 1 || (TQ == 4 && NR <= 3) ? 16 : 8;
+  return E::kBytes == 2 ? (NR * token_tiles<TQ>() <= 4 ? 16 : 8) : TQ <= 2 || (TQ == 4 && NR <= 3) ? 16 : 8;
 }
 
 template <class E, int G, int TQ, int NR>
@@ -29,7 +29,11 @@ __global__ __launch_bounds__((max_waves<E, TQ, NR>() * kWave)) void linear4_kern
   const int T = a.T - t0 < 4 * TQ ? static_cast<int>(a.T - t0) : 4 * TQ;
 
   const typename Prod::X x(
-      Src{a.K}, [&](int t) { return t < T ? static_cast<const Elem*>(a.x) + (t0 + t) * a.ldx : nullptr; },
+      Src{a.K},
+      [&](int t) {
+        if (t >= T && TQ == 1) return static_cast<const Elem*>(nullptr);
+        return static_cast<const Elem*>(a.x) + (t0 + (t < T ? t : 0)) * a.ldx;
+      },
       lds + wave * Prod::X::kLdsBytes, lane);
   Tile tile[NR];
 #pragma unroll
@@ -93,6 +97,7 @@ template <class E, int G>
 hipError_t by_tokens(const LinearArgs& a, hipStream_t s) {
   const int cus = lockstep_resident() > 0 ? lockstep_resident() : 256;
   if (a.T <= 4) return by_rows<E, G, 1, 1, 4>(a, cus, s);
+  if (a.T <= 8) return by_rows<E, G, 2, 1, 4>(a, cus, s);
   if (a.T <= 16) return by_rows<E, G, 4, 1, 4>(a, cus, s);
   if constexpr (E::kBytes == 2) {
     // 64 tokens a workgroup save unpacking the codes twice, once that still

@@ -177,12 +177,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
 }
 
 // ---------------------------------------------------------------- expert lists
-// Waves of a workgroup.  Four workgroups of four waves on a CU are more often at
-// different points of their work than two of eight (64 tokens, 64 experts, 4
-// bits: down 27.6 -> 23.7 us); with few tokens there is one wave of workgroups
-// and more waves have more in flight (1 token: up 7.6 -> 7.1 us).
-template <int TQ>
-constexpr int expert_waves() { return TQ == 1 ? 8 : 4; }
+// Most waves of a workgroup of the up and down kernels (chosen at launch).
+constexpr int kMostWaves = 8;
 
 // Where one wave works out its expert and the expert's pairs.  Every wave does
 // so for itself, without a barrier: the pairs come from the L2 once, and
@@ -202,15 +198,12 @@ __device__ __forceinline__ uint32_t wave_or(uint32_t v) {
   return static_cast<uint32_t>(wave_last(static_cast<int>(v)));
 }
 
-// Finds the `which`-th chosen expert (ascending) and its (token, choice) pairs
-// (ascending) in the list of the router (a.live).  Returns the expert, or -1 if
-// there are not that many; n: its pairs.  kPairsAhead: pairs per lane held at
-// once.
+// The pairs of the router's list (a.live), kPairsAhead for each lane at once.
 template <int kPairsAhead>
-__device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList& l, int lane, int& n) {
-  const int pairs = a.T * a.k;
+struct LivePairs {
   int id[kPairsAhead];
-  auto fetch = [&](int i0) {
+  __device__ __forceinline__ void fetch(const MoeArgs& a, int i0, int lane) {
+    const int pairs = a.T * a.k;
 #pragma unroll
     for (int u = 0; u < kPairsAhead; ++u) {
       const int i = i0 + u * 64 + lane;
@@ -219,7 +212,14 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList
 #pragma unroll
     for (int u = 0; u < kPairsAhead; ++u)
       if (i0 + u * 64 + lane >= pairs) id[u] = -1;
-  };
+  }
+};
+
+// The `which`-th chosen expert (ascending), or -1 if there are not that many.
+template <int kPairsAhead>
+__device__ __forceinline__ int find_expert(const MoeArgs& a, LivePairs<kPairsAhead>& live, int which, WaveList& l,
+                                           int lane) {
+  const int pairs = a.T * a.k;
   int expert = -1, before = 0;  // chosen experts below the 64 looked at
   auto look = [&](int e0, uint64_t has) {
     const int c = __popcll(has);
@@ -232,12 +232,12 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList
   if (a.E <= 64) {
     uint32_t lo = 0, hi = 0;
     for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
-      fetch(i0);
+      if (i0 > 0) live.fetch(a, i0, lane);
 #pragma unroll
       for (int u = 0; u < kPairsAhead; ++u) {
-        const uint32_t bit = id[u] < 0 ? 0u : 1u << (id[u] & 31);
-        lo |= id[u] < 32 ? bit : 0u;
-        hi |= id[u] < 32 ? 0u : bit;
+        const uint32_t bit = live.id[u] < 0 ? 0u : 1u << (live.id[u] & 31);
+        lo |= live.id[u] < 32 ? bit : 0u;
+        hi |= live.id[u] < 32 ? 0u : bit;
       }
     }
     look(0, static_cast<uint64_t>(wave_or(hi)) << 32 | wave_or(lo));
@@ -245,52 +245,57 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, int which, WaveList
     reinterpret_cast<u32x4_t*>(l.taken)[lane] = u32x4_t{0, 0, 0, 0};
     __builtin_amdgcn_wave_barrier();
     for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
-      fetch(i0);
+      if (i0 > 0) live.fetch(a, i0, lane);
 #pragma unroll
       for (int u = 0; u < kPairsAhead; ++u)
-        if (id[u] >= 0) l.taken[id[u]] = 1;
+        if (live.id[u] >= 0) l.taken[live.id[u]] = 1;
     }
     __builtin_amdgcn_wave_barrier();
     for (int e0 = 0; e0 < a.E; e0 += 64) look(e0, __ballot(l.taken[e0 + lane] != 0));
   }
-  if (expert < 0) return -1;
-  n = 0;
+  if (pairs > kPairsAhead * 64) live.fetch(a, 0, lane);
+  return expert;
+}
+
+// The expert's (token, choice) pairs, ascending, into l.pair; returns how many.
+// live: the first pairs.
+template <int kPairsAhead>
+__device__ __forceinline__ int find_pairs(const MoeArgs& a, LivePairs<kPairsAhead>& live, int expert, WaveList& l,
+                                          int lane) {
+  const int pairs = a.T * a.k;
+  int n = 0;
   for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
-    if (pairs > kPairsAhead * 64) fetch(i0);
+    if (i0 > 0) live.fetch(a, i0, lane);
 #pragma unroll
     for (int u = 0; u < kPairsAhead; ++u) {
-      const uint64_t has = __ballot(id[u] == expert);
-      if (id[u] == expert) l.pair[n + __popcll(has & ((1ull << lane) - 1))] = i0 + u * 64 + lane;
+      const uint64_t has = __ballot(live.id[u] == expert);
+      if (live.id[u] == expert) l.pair[n + __popcll(has & ((1ull << lane) - 1))] = i0 + u * 64 + lane;
       n += __popcll(has);
     }
   }
   __builtin_amdgcn_wave_barrier();
-  return expert;
+  return n;
 }
 
-// LDS of the token pieces, and of the waves' sums after them.
-template <class Prod, int kExpertWaves>
-constexpr int expert_lds() {
-  return kExpertWaves * (Prod::kAll * 256 > Prod::X::kLdsBytes ? Prod::kAll * 256 : Prod::X::kLdsBytes);
+// Token of a pair: pair / k, exact since (pair + 1/2) / k is at least 1/64 from
+// every whole number and pair < 2^11.
+__device__ __forceinline__ int64_t token_of(int pair, const MoeArgs& a) {
+  return static_cast<int>((static_cast<float>(pair) + 0.5f) * a.inv_k);
 }
+
+// LDS of one wave: its list, and its token pieces or, after them, its sums.
+template <class Prod>
+constexpr int wave_lds() { return Prod::kAll * 256 > Prod::X::kLdsBytes ? Prod::kAll * 256 : Prod::X::kLdsBytes; }
 
 // ---------------------------------------------------------------- gate and up
-// h = w act(g) u for n pairs of one expert and the neurons of NT tiles from
-// tile ti on.
 template <class E, int BITS, int G, int TQ, int NT>
-__device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, const int* pair, int n, char* lds,
-                                         int lane, int wave) {
-  using Src = std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>;
-  using Elem = typename E::storage;
-  using Prod = Product<BITS, G, TQ, 2 * NT, Src>;
-  constexpr int kExpertWaves = expert_waves<TQ>();
-  constexpr int MT = Prod::MT, kOne = MT * Prod::kRegs;  // registers of one tile
-  const typename Prod::X x(
-      Src{a.d},
-      [&](int i) { return i < n ? static_cast<const Elem*>(a.x) + static_cast<int64_t>(pair[i] / a.k) * a.ldx : nullptr; },
-      lds + wave * Prod::X::kLdsBytes, lane);
-  float* red = reinterpret_cast<float*>(lds);
-  Tile tile[2 * NT];
+using UpProduct = Product<BITS, G, TQ, 2 * NT, std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>, (TQ > 1)>;
+
+template <int NT>
+using Tiles = Tile[NT];
+
+template <int BITS, int G, int NT>
+__device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, int ti, Tiles<2 * NT>& tile) {
 #pragma unroll
   for (int r = 0; r < NT; ++r) {
     const int i = ti + r < a.tiles_f ? ti + r : a.tiles_f - 1;
@@ -298,19 +303,37 @@ __device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, c
     tile[2 * r] = {a.gate_codes + blk * Block<BITS>::kBytes, a.gate_scales + blk * (16 * G)};
     tile[2 * r + 1] = {a.up_codes + blk * Block<BITS>::kBytes, a.up_scales + blk * (16 * G)};
   }
+}
+
+// h = w act(g) u for n <= 4 TQ pairs of one expert and the neurons of NT tiles
+// from tile ti on.  lds: wave_lds per wave.
+template <class E, int BITS, int G, int TQ, int NT>
+__device__ __forceinline__ void up_pairs(const MoeArgs& a, const Tiles<2 * NT>& tile, int ti, const int* pair, int n,
+                                         char* lds, int lane, int wave, int waves) {
+  using Elem = typename E::storage;
+  using Prod = UpProduct<E, BITS, G, TQ, NT>;
+  constexpr int kOne = Prod::kRegs;  // registers of one tile
+  const typename Prod::X x(
+      {a.d},
+      [&](int i) {
+        if (i >= n && TQ == 1) return static_cast<const Elem*>(nullptr);
+        return static_cast<const Elem*>(a.x) + token_of(pair[i < n ? i : 0], a) * a.ldx;
+      },
+      lds + wave * Prod::X::kLdsBytes, lane);
+  float* red = reinterpret_cast<float*>(lds);
   Prod p;
   p.clear();
-  p.template run<TQ == 1 && E::kBytes == 2 ? 2 : 1>(
-      x, tile, a.blocks_d * wave / kExpertWaves, a.blocks_d * (wave + 1) / kExpertWaves, a.d / kBlockK, lane);
+  p.template run<(E::kBytes == 2 && TQ == 1 ? 2 : 1)>(x, tile, a.blocks_d * wave / waves,
+                                                      a.blocks_d * (wave + 1) / waves, a.d / kBlockK, lane);
   if constexpr (Prod::X::kLdsBytes > 0) __syncthreads();  // the token pieces have been read
   p.put(red, wave, lane);
   __syncthreads();
-  for (int o = threadIdx.x; o < NT * kOne * 64; o += kExpertWaves * kWave) {
-    const int r = o / (kOne * 64), j = o / 64 % kOne, l = o & 63;
-    const int i = (j / Prod::kRegs) * 16 + result_token(j % Prod::kRegs, l);
+  for (int o = threadIdx.x; o < NT * kOne * 64; o += waves * kWave) {
+    const int r = o / (kOne * 64), l = o & 63;
+    const int i = result_token(o / 64 % kOne, l);
     if (i >= n) continue;
-    const float g = joined<Prod::kAll>(red, kExpertWaves, o + r * kOne * 64);
-    const float u = joined<Prod::kAll>(red, kExpertWaves, o + (r + 1) * kOne * 64);
+    const float g = joined<Prod::kAll>(red, waves, o + r * kOne * 64);
+    const float u = joined<Prod::kAll>(red, waves, o + (r + 1) * kOne * 64);
     // a NaN gate stays NaN under both activations
     const float act = a.act == 0 ? (g < 0.f ? 0.f : g) : g / (1.f + expf(-g));
     float h = a.weights[pair[i]] * act * u;
@@ -328,77 +351,103 @@ __device__ __forceinline__ void up_pairs(const MoeArgs& a, int expert, int ti, c
   }
 }
 
-template <class E, int BITS, int G, int TQ, int NT>
-__global__ __launch_bounds__(expert_waves<TQ>() * kWave, 4) void moe_up_kernel(MoeArgs a) {
-  constexpr int kExpertWaves = expert_waves<TQ>();
-  __shared__ WaveList lists[kExpertWaves];
-  using Src = std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>;
-  __shared__ __align__(16) char lds[expert_lds<Product<BITS, G, TQ, 2 * NT, Src>, kExpertWaves>()];
+// kFew: up to four tokens.  Where there are at least as many pairs as experts,
+// nearly every expert has a token: row y of the grid is then expert y, which
+// needs no search.
+template <class E, int BITS, int G, bool kFew, int NT>
+__global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_up_kernel(MoeArgs a) {
+  __shared__ WaveList lists[kMostWaves];
+  extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  WaveList& list = lists[wave];
-  int n = 0;
-  const int expert = find_expert<(TQ == 1 ? 2 : 8)>(a, blockIdx.y, list, lane, n);
-  if (TQ > 1 && blockIdx.x == 0 && wave == 0) {  // for the down kernel
-    if (lane == 0) a.chosen[blockIdx.y] = MoeChosen{expert, n};
-    if (lane < n) a.chosen_pairs[blockIdx.y * kMoeBlockTokens + lane] = list.pair[lane];
-  }
-  if (expert < 0) return;  // the whole workgroup
+  const int waves = blockDim.x >> 6;
   const int ti = blockIdx.x * NT;
-  for (int i = 0; i < n; i += 16) {
-    if (i > 0) __syncthreads();
-    up_pairs<E, BITS, G, TQ, NT>(a, expert, ti, list.pair + i, n - i < 16 ? n - i : 16, lds, lane, wave);
+  WaveList& list = lists[wave];
+  LivePairs<(kFew ? 2 : 8)> live;
+  Tiles<2 * NT> tile;
+  if constexpr (kFew) {
+    live.fetch(a, 0, lane);
+    const int expert = find_expert(a, live, blockIdx.y, list, lane);
+    if (expert < 0) return;  // the whole workgroup
+    const int n = find_pairs(a, live, expert, list, lane);
+    up_tiles<BITS, G, NT>(a, expert, ti, tile);
+    up_pairs<E, BITS, G, 1, NT>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
+  } else {
+    live.fetch(a, 0, lane);
+    const int expert = a.by_expert ? static_cast<int>(blockIdx.y) : find_expert(a, live, blockIdx.y, list, lane);
+    const int n = expert < 0 ? 0 : find_pairs(a, live, expert, list, lane);
+    if (blockIdx.x == 0 && wave == 0) {  // for the down kernel
+      if (lane == 0) a.chosen[blockIdx.y] = MoeChosen{expert, n};
+      if (lane < n) a.chosen_pairs[blockIdx.y * kMoeBlockTokens + lane] = list.pair[lane];
+    }
+    if (n == 0) return;
+    up_tiles<BITS, G, NT>(a, expert, ti, tile);
+    if (n <= 8) {
+      up_pairs<E, BITS, G, 2, NT>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
+    } else {
+      for (int i = 0; i < n; i += 16) {
+        if (i > 0) __syncthreads();
+        up_pairs<E, BITS, G, 4, NT>(a, tile, ti, list.pair + i, n - i < 16 ? n - i : 16, lds, lane, wave, waves);
+      }
+    }
   }
 }
 
 // ---------------------------------------------------------------- down
-// z[pair] = W_down_e h[pair] for n pairs of one expert and the outputs of NT
-// tiles from tile ti on.
-template <int BITS, int G, int TQ, int NT, int P>
-__device__ __forceinline__ void down_pairs(const MoeArgs& a, int expert, int ti, const int* pair, int n, char* lds,
-                                           int lane, int wave) {
-  using Src = SourcePlanes<P>;
-  using Prod = Product<BITS, G, TQ, NT, Src>;
-  constexpr int kExpertWaves = expert_waves<TQ>();
-  constexpr int MT = Prod::MT, kOne = MT * Prod::kRegs;
+// The planes that hold h.
+template <class E>
+constexpr int h_planes() { return E::kBytes == 2 ? 2 : 3; }
+template <class E, int BITS, int G, int TQ, int NT>
+using DownProduct = Product<BITS, G, TQ, NT, SourcePlanes<h_planes<E>()>, true>;
+
+// z[pair] = W_down_e h[pair] for n <= 4 TQ pairs of one expert and the outputs
+// of NT tiles from tile ti on.
+template <class E, int BITS, int G, int TQ, int NT>
+__device__ __forceinline__ void down_pairs(const MoeArgs& a, const Tiles<NT>& tile, int ti, const int* pair, int n,
+                                           char* lds, int lane, int wave, int waves) {
+  using Prod = DownProduct<E, BITS, G, TQ, NT>;
+  constexpr int kOne = Prod::kRegs;
   const typename Prod::X x(
-      Src{a.h_plane}, [&](int i) { return i < n ? a.h + static_cast<int64_t>(pair[i]) * a.h_row : nullptr; },
+      {a.h_plane}, [&](int i) { return a.h + static_cast<int64_t>(pair[i < n ? i : 0]) * a.h_row; },
       lds + wave * Prod::X::kLdsBytes, lane);
   float* red = reinterpret_cast<float*>(lds);
-  Tile tile[NT];
+  Prod p;
+  p.clear();
+  p.template run<1>(x, tile, a.blocks_f * wave / waves, a.blocks_f * (wave + 1) / waves, a.blocks_f, lane);
+  __syncthreads();  // the token pieces have been read
+  p.put(red, wave, lane);
+  __syncthreads();
+  for (int o = threadIdx.x; o < NT * kOne * 64; o += waves * kWave) {
+    const int r = o / (kOne * 64), l = o & 63;
+    const int i = result_token(o / 64 % kOne, l);
+    const int out = (ti + r) * kTileRows + (l & 15);
+    if (i < n && out < a.d) a.z[static_cast<int64_t>(pair[i]) * a.d + out] = joined<Prod::kAll>(red, waves, o);
+  }
+}
+
+template <class E, int BITS, int G, int NT>
+__global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_down_kernel(MoeArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int ti = blockIdx.x * NT;
+  const MoeChosen c = a.chosen[blockIdx.y];
+  const int expert = __builtin_amdgcn_readfirstlane(c.expert), n = __builtin_amdgcn_readfirstlane(c.n);
+  if (n == 0) return;
+  Tiles<NT> tile;
 #pragma unroll
   for (int r = 0; r < NT; ++r) {
     const int i = ti + r < a.tiles_d ? ti + r : a.tiles_d - 1;
     const int64_t blk = (static_cast<int64_t>(expert) * a.tiles_d + i) * a.blocks_f;
     tile[r] = {a.down_codes + blk * Block<BITS>::kBytes, a.down_scales + blk * (16 * G)};
   }
-  Prod p;
-  p.clear();
-  p.template run<1>(x, tile, a.blocks_f * wave / kExpertWaves, a.blocks_f * (wave + 1) / kExpertWaves, a.blocks_f, lane);
-  if constexpr (Prod::X::kLdsBytes > 0) __syncthreads();  // the token pieces have been read
-  p.put(red, wave, lane);
-  __syncthreads();
-  for (int o = threadIdx.x; o < NT * kOne * 64; o += kExpertWaves * kWave) {
-    const int r = o / (kOne * 64), j = o / 64 % kOne, l = o & 63;
-    const int i = (j / Prod::kRegs) * 16 + result_token(j % Prod::kRegs, l);
-    const int out = (ti + r) * kTileRows + (l & 15);
-    if (i < n && out < a.d) a.z[static_cast<int64_t>(pair[i]) * a.d + out] = joined<Prod::kAll>(red, kExpertWaves, o);
-  }
-}
-
-template <class E, int BITS, int G, int TQ, int NT>
-__global__ __launch_bounds__(expert_waves<TQ>() * kWave, 4) void moe_down_kernel(MoeArgs a) {
-  constexpr int kExpertWaves = expert_waves<TQ>();
-  constexpr int P = E::kBytes == 2 ? 2 : 3;
-  __shared__ __align__(16) char lds[expert_lds<Product<BITS, G, TQ, NT, SourcePlanes<P>>, kExpertWaves>()];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const MoeChosen c = a.chosen[blockIdx.y];
-  const int expert = c.expert, n = c.n;
-  if (expert < 0) return;
   const int* pair = a.chosen_pairs + blockIdx.y * kMoeBlockTokens;
-  const int ti = blockIdx.x * NT;
-  for (int i = 0; i < n; i += 16) {
-    if (i > 0) __syncthreads();
-    down_pairs<BITS, G, TQ, NT, P>(a, expert, ti, pair + i, n - i < 16 ? n - i : 16, lds, lane, wave);
+  if (n <= 8) {
+    down_pairs<E, BITS, G, 2, NT>(a, tile, ti, pair, n, lds, lane, wave, waves);
+  } else {
+    for (int i = 0; i < n; i += 16) {
+      if (i > 0) __syncthreads();
+      down_pairs<E, BITS, G, 4, NT>(a, tile, ti, pair + i, n - i < 16 ? n - i : 16, lds, lane, wave, waves);
+    }
   }
 }
 
@@ -483,18 +532,37 @@ hipError_t go_route(const MoeArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class E, int BITS, int G, int TQ, int NT>
+// Waves per workgroup: as few as still make kFillWaves waves.  A workgroup's
+// waves wait for each other twice, so what fills the chip with single waves
+// streams best.
+constexpr int64_t kFillWaves = 4096;
+int waves_for(int64_t groups, int blocks) {
+  int w = 1;
+  while (w < kMostWaves && w < blocks && groups * w < kFillWaves) w <<= 1;
+  return w;
+}
+
+template <class E, int BITS, int G, bool kFew, int NT>
 hipError_t go_up(const MoeArgs& a, hipStream_t s) {
   // the tiles that fill the last block of neurons are written too
   const dim3 grid(static_cast<unsigned>(a.blocks_f * (kBlockK / kTileRows) / NT), static_cast<unsigned>(a.most_chosen));
-  moe_up_kernel<E, BITS, G, TQ, NT><<<grid, expert_waves<TQ>() * kWave, 0, s>>>(a);
+  constexpr int kLds = wave_lds<UpProduct<E, BITS, G, kFew ? 1 : 4, NT>>();
+  const int w = waves_for(static_cast<int64_t>(grid.x) * grid.y, a.blocks_d);
+  moe_up_kernel<E, BITS, G, kFew, NT><<<grid, w * kWave, w * kLds, s>>>(a);
   return hipGetLastError();
 }
 
 template <class E, int BITS, int G, int NT>
 hipError_t go_down(const MoeArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.tiles_d + NT - 1) / NT), static_cast<unsigned>(a.most_chosen));
-  moe_down_kernel<E, BITS, G, 4, NT><<<grid, expert_waves<4>() * kWave, 0, s>>>(a);
+  constexpr int kLds = wave_lds<DownProduct<E, BITS, G, 4, NT>>();
+  const int w = waves_for(static_cast<int64_t>(grid.x) * grid.y, a.blocks_f);
+  if constexpr (kMostWaves * kLds > 64 * 1024) {
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_down_kernel<E, BITS, G, NT>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kMostWaves * kLds);
+    if (attr != hipSuccess) return attr;
+  }
+  moe_down_kernel<E, BITS, G, NT><<<grid, w * kWave, w * kLds, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 join(static_cast<unsigned>((a.d + 255) / 256), static_cast<unsigned>(a.T));
@@ -502,42 +570,17 @@ hipError_t go_down(const MoeArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tiles per workgroup: the more, the more of a 4-bit stream is in flight and
-// the less often tokens are fetched, as far as 128 registers go; fewer while
-// that would leave less than two workgroups for a CU.  A tile of bf16 weights
-// is 4 KB a block by itself.
-template <class E, int BITS, int G>
-constexpr int up_tiles() { return BITS == 16 ? 1 : (E::kBytes == 2 ? 4 : 2) / (G == 4 ? 2 : 1); }
-template <class E, int BITS, int G>
-constexpr int down_tiles() { return BITS == 16 ? 2 : E::kBytes == 4 && G == 4 ? 2 : 4; }
-constexpr int64_t kFill = 512;
-
-template <class E, int BITS, int G, int NT>
-hipError_t by_up_tiles(const MoeArgs& a, hipStream_t s) {
-  if constexpr (NT > 1) {
-    if (static_cast<int64_t>(a.tiles_f) * a.most_chosen < NT * kFill) return by_up_tiles<E, BITS, G, NT / 2>(a, s);
-  }
-  return go_up<E, BITS, G, 4, NT>(a, s);
-}
-template <class E, int BITS, int G, int NT>
-hipError_t by_down_tiles(const MoeArgs& a, hipStream_t s) {
-  if constexpr (NT > 1) {
-    if (static_cast<int64_t>(a.tiles_d) * a.most_chosen < NT * kFill) return by_down_tiles<E, BITS, G, NT / 2>(a, s);
-  }
-  return go_down<E, BITS, G, NT>(a, s);
-}
-
 template <class E, int BITS, int G>
 hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
   if (a.T <= 4) {
-    const hipError_t e = go_up<E, BITS, G, 1, 1>(a, s);
+    const hipError_t e = go_up<E, BITS, G, true, 1>(a, s);
     if (e != hipSuccess) return e;
     moe_down_few_kernel<E, BITS, G><<<a.tiles_d, kFewWaves * kWave, 0, s>>>(a);
     return hipGetLastError();
   }
-  const hipError_t e = by_up_tiles<E, BITS, G, up_tiles<E, BITS, G>()>(a, s);
+  const hipError_t e = go_up<E, BITS, G, false, BITS == 16 || E::kBytes == 4 ? 1 : 2>(a, s);
   if (e != hipSuccess) return e;
-  return by_down_tiles<E, BITS, G, down_tiles<E, BITS, G>()>(a, s);
+  return go_down<E, BITS, G, BITS == 16 || E::kBytes == 4 ? 2 : 4>(a, s);
 }
 
 template <class E>

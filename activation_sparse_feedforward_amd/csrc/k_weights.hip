@@ -92,7 +92,7 @@ __device__ __forceinline__ void store_block(const float (&f)[4][8], uint8_t* cod
           const uint32_t u = live ? static_cast<uint32_t>(static_cast<int>(q) + 8) : 8u;
           w |= u << (4 * (i >> 1) + 16 * (i & 1));
         }
-        words[gr * kSteps + s] = w;
+        words[gr * kSteps + s] = __builtin_rotateleft32(w, 3);
       }
     }
     *reinterpret_cast<u32x4_t*>(codes + lane * 16) = words;
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(kPackWaves* kWave) void weights_unpack_kernel(Weigh
   const int64_t blk = (e * a.tiles + tile) * a.blocks + b;
   constexpr int G = scales_per_block<BITS, GROUP>();
   Block<BITS> q;
-  q.load(a.codes + blk * Block<BITS>::kBytes, lane);
+  q.template load<false>(a.codes + blk * Block<BITS>::kBytes, lane);
   Scales<G> sc;
   if constexpr (BITS == 4) sc.load(a.scales + blk * (16 * G), lane);
   if (row >= a.N) return;
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(kPackWaves* kWave) void weights_unpack_kernel(Weigh
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int u = static_cast<int>((q.c[s] >> (4 * (i >> 1) + 16 * (i & 1))) & 15u);
+        const int u = static_cast<int>(__builtin_rotateright32(q.c[s], 3 + 4 * (i >> 1) + 16 * (i & 1)) & 15u);
         f[i] = static_cast<float>(u - 8) * sc.at(s * G / 4);
       }
     }

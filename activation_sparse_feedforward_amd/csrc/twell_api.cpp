@@ -670,6 +670,7 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
   a.ldy = d->ldy;
   a.E = d->experts;
   a.k = d->top_k;
+  a.inv_k = 1.0f / static_cast<float>(d->top_k);
   a.d = d->d_model;
   a.f = d->d_ff;
   a.bits = d->bits;
@@ -696,6 +697,7 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
     a.weights = weights + t0 * d->top_k;
     const int64_t pairs = static_cast<int64_t>(a.T) * d->top_k;
     a.most_chosen = static_cast<int32_t>(pairs < d->experts ? pairs : d->experts);
+    a.by_expert = pairs >= d->experts;
     TWELL_TRY(from_hip(twell::launch_moe(a, d->dtype, s)));
   }
   return TWELL_OK;

@@ -285,8 +285,9 @@ typedef struct {
  * zeros.  In a block, lane l (0..63) holds row l % 16 and inputs 32 s + 8 (l / 16)
  * + 0..7 for s = 0..3:
  *   bits = 16: bf16 [s][l][8]                                        4096 bytes
- *   bits = 4:  32-bit words [l][s], input 2j of the eight in bits 4j..4j+3 and
- *              input 2j+1 in bits 16+4j..16+4j+3, as q + 8            1024 bytes
+ *   bits = 4:  32-bit words [l][s], codes as q + 8: input 2j of the eight in bits
+ *              4j+3 .. 4j+6 and input 2j+1 in bits 4j+19 .. 4j+22, bit numbers
+ *              modulo 32 (the word is rotated left by three)           1024 bytes
  *              and scales bf16 [16 rows][128 / group]. */
 typedef struct {
   void* codes;

@@ -7,6 +7,7 @@ def planes_to_codes(codes: np.ndarray, scales: np.ndarray, E, N, K, group):
     """Codes q and fp32 scales per weight, read from the planes by the documented layout."""
     tiles, blocks = -(-N // 16), -(-K // 128)
     words = codes.view(np.uint32).reshape(E, tiles, blocks, 64, 4)
+    words = (words >> 3) | (words << 29)  # stored rotated left by three
     q = np.zeros((E, tiles * 16, blocks * 128), np.int64)
     lane = np.arange(64)
     for s in range(4):
