@@ -84,12 +84,12 @@ typedef uint32_t u32x4_a4_t __attribute__((ext_vector_type(4), aligned(4)));
 // ---------------------------------------------------------------- token operands
 // The matrix instruction wants 16 tokens at 16 neighbouring lanes, 16 bytes of
 // each: loaded like that, every 16 lanes touch 16 cache lines, which the L1
-// serves one at a time (13 bytes a clock measured, of 64).  More than four
-// tokens therefore come in by rows (16 lanes read 256 consecutive bytes) and
-// go through a piece of LDS that belongs to the wave alone, without a barrier:
-// 16-byte pieces, piece c of row r at place c ^ (r % 16), which spreads both
-// the writes and the reads over the banks.  Up to four tokens are loaded
-// directly (four lines).
+// serves one at a time (13 bytes a clock measured, of 64), and a single token
+// would still take four load instructions of 16 clocks for a block.  Tokens
+// therefore come in by rows (16 lanes read 256 consecutive bytes, one load
+// takes four rows) and go through a piece of LDS that belongs to the wave
+// alone, without a barrier: 16-byte pieces, piece c of row r at place
+// c ^ (r % 16), which spreads both the writes and the reads over the banks.
 //
 // Source: what a row looks like.  A block of 128 inputs is kParts parts of 16
 // pieces of 16 bytes; kPlanes bf16 operands whose sum is the value come out.
@@ -173,42 +173,13 @@ __device__ __forceinline__ int lane_token(int lane) { return ((lane & 3) << 2) |
 // Token of result register i in lane l.
 __device__ __forceinline__ int result_token(int i, int lane) { return 4 * i + (lane >> 4); }
 
-// Up to four tokens, loaded as operands.  at(t): the row of token t, null where
-// there is none: it counts as zeros, so that sums over several operands may
-// leave tokens out.
-template <class Src>
-struct DirectTokens {
-  static constexpr int kLdsBytes = 0;
-  Src src;
-  const typename Src::Elem* row;  // of lane_token(lane)
-  struct Loaded {
-    u32x4_t v[4][Src::kReads];
-  };
-  template <class F>
-  __device__ __forceinline__ DirectTokens(Src s, F at, char*, int lane) : src(s), row(at(lane_token(lane))) {}
-  __device__ __forceinline__ void fetch(Loaded& q, int b, bool whole, int lane) const {
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < Src::kReads; ++i) {
-        const int at = Src::place(s, lane >> 4, i);
-        q.v[s][i] = u32x4_t{0, 0, 0, 0};
-        if (row != nullptr) q.v[s][i] = src.piece(row, b, at >> 4, at & 15, whole);
-      }
-  }
-  __device__ __forceinline__ void store(const Loaded&, int) const {}
-  __device__ __forceinline__ void step(const Loaded& q, int s, int, int, bf16x8_t (&x)[Src::kPlanes]) const {
-    Src::operands(q.v[s], x);
-  }
-};
-
 // Up to 4 TQ tokens, by rows and through LDS.  at(t) is a row for every t; where
 // there is no token it is any other one, whose results nobody reads (a matrix
-// row's results depend on that row alone; the same holds for the rows of a tile
-// of 16 that are never written).
+// row's results depend on that row alone).
 template <class Src, int TQ>
-struct StagedTokens {
-  static constexpr int kPartBytes = (TQ + 3) / 4 * 16 * 256;
+struct Tokens {
+  static constexpr int kRows = 4 * TQ;
+  static constexpr int kPartBytes = kRows * 256;
   static constexpr int kLdsBytes = Src::kParts * kPartBytes;  // of one wave
   Src src;
   const typename Src::Elem* row[TQ];  // row[j]: of token 4 j + lane / 16; a load takes four rows
@@ -220,7 +191,7 @@ struct StagedTokens {
     return (place >> 4) * kPartBytes + r * 256 + (((place & 15) ^ (r & 15)) << 4);
   }
   template <class F>
-  __device__ __forceinline__ StagedTokens(Src s, F at, char* lds_, int lane) : src(s), lds(lds_) {
+  __device__ __forceinline__ Tokens(Src s, F at, char* lds_, int lane) : src(s), lds(lds_) {
 #pragma unroll
     for (int j = 0; j < TQ; ++j) row[j] = at(4 * j + (lane >> 4));
   }
@@ -243,19 +214,17 @@ struct StagedTokens {
     u32x4_t v[Src::kReads];
 #pragma unroll
     for (int i = 0; i < Src::kReads; ++i)
-      v[i] = *reinterpret_cast<const u32x4_t*>(lds + piece_at(m * 16 + lane_token(lane), Src::place(s, lane >> 4, i)));
+      v[i] = *reinterpret_cast<const u32x4_t*>(lds + piece_at((m * 16 + lane_token(lane)) % kRows, Src::place(s, lane >> 4, i)));
     Src::operands(v, x);
   }
 };
 
-// The operand for TQ quads of tokens.
+// Tiles of 16 tokens for TQ quads.
 template <int TQ>
 constexpr int token_tiles() { return (TQ + 3) / 4; }
 // Result registers in use per tile of 16 tokens.
 template <int TQ>
 constexpr int token_regs() { return TQ < 4 ? TQ : 4; }
-template <class Src, int TQ>
-using Tokens = std::conditional_t<TQ == 1, DirectTokens<Src>, StagedTokens<Src, TQ>>;
 
 // ---------------------------------------------------------------- weights
 // STREAM: past the caches, for weights that are read once and are larger than

@@ -30,10 +30,7 @@ __global__ __launch_bounds__((max_waves<E, TQ, NR>() * kWave)) void linear4_kern
 
   const typename Prod::X x(
       Src{a.K},
-      [&](int t) {
-        if (t >= T && TQ == 1) return static_cast<const Elem*>(nullptr);
-        return static_cast<const Elem*>(a.x) + (t0 + (t < T ? t : 0)) * a.ldx;
-      },
+      [&](int t) { return static_cast<const Elem*>(a.x) + (t0 + (t < T ? t : 0)) * a.ldx; },
       lds + wave * Prod::X::kLdsBytes, lane);
   Tile tile[NR];
 #pragma unroll
@@ -48,7 +45,7 @@ __global__ __launch_bounds__((max_waves<E, TQ, NR>() * kWave)) void linear4_kern
   const int b0 = a.blocks * wave / waves, b1 = a.blocks * (wave + 1) / waves;
   p.template run<1>(x, tile, b0, b1, a.K / kBlockK, lane);
   float* red = reinterpret_cast<float*>(lds);
-  if constexpr (Prod::X::kLdsBytes > 0) __syncthreads();  // the pieces have been read
+  __syncthreads();  // the pieces have been read
   p.put(red, wave, lane);
   __syncthreads();
   for (int o = threadIdx.x; o < Prod::kAll * 64; o += blockDim.x) {

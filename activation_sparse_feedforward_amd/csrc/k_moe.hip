@@ -288,8 +288,8 @@ template <class Prod>
 constexpr int wave_lds() { return Prod::kAll * 256 > Prod::X::kLdsBytes ? Prod::kAll * 256 : Prod::X::kLdsBytes; }
 
 // ---------------------------------------------------------------- gate and up
-template <class E, int BITS, int G, int TQ, int NT>
-using UpProduct = Product<BITS, G, TQ, 2 * NT, std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>, (TQ > 1)>;
+template <class E, int BITS, int G, int TQ, int NT, bool STREAM>
+using UpProduct = Product<BITS, G, TQ, 2 * NT, std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>, STREAM>;
 
 template <int NT>
 using Tiles = Tile[NT];
@@ -307,25 +307,22 @@ __device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, int ti, T
 
 // h = w act(g) u for n <= 4 TQ pairs of one expert and the neurons of NT tiles
 // from tile ti on.  lds: wave_lds per wave.
-template <class E, int BITS, int G, int TQ, int NT>
+template <class E, int BITS, int G, int TQ, int NT, bool kFew = false>
 __device__ __forceinline__ void up_pairs(const MoeArgs& a, const Tiles<2 * NT>& tile, int ti, const int* pair, int n,
                                          char* lds, int lane, int wave, int waves) {
   using Elem = typename E::storage;
-  using Prod = UpProduct<E, BITS, G, TQ, NT>;
+  using Prod = UpProduct<E, BITS, G, TQ, NT, !kFew>;
   constexpr int kOne = Prod::kRegs;  // registers of one tile
   const typename Prod::X x(
       {a.d},
-      [&](int i) {
-        if (i >= n && TQ == 1) return static_cast<const Elem*>(nullptr);
-        return static_cast<const Elem*>(a.x) + token_of(pair[i < n ? i : 0], a) * a.ldx;
-      },
+      [&](int i) { return static_cast<const Elem*>(a.x) + token_of(pair[i < n ? i : 0], a) * a.ldx; },
       lds + wave * Prod::X::kLdsBytes, lane);
   float* red = reinterpret_cast<float*>(lds);
   Prod p;
   p.clear();
-  p.template run<(E::kBytes == 2 && TQ == 1 ? 2 : 1)>(x, tile, a.blocks_d * wave / waves,
+  p.template run<(E::kBytes == 2 && kFew ? 2 : 1)>(x, tile, a.blocks_d * wave / waves,
                                                       a.blocks_d * (wave + 1) / waves, a.d / kBlockK, lane);
-  if constexpr (Prod::X::kLdsBytes > 0) __syncthreads();  // the token pieces have been read
+  __syncthreads();  // the token pieces have been read
   p.put(red, wave, lane);
   __syncthreads();
   for (int o = threadIdx.x; o < NT * kOne * 64; o += waves * kWave) {
@@ -370,7 +367,7 @@ __global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_up_kernel(MoeArgs a)
     if (expert < 0) return;  // the whole workgroup
     const int n = find_pairs(a, live, expert, list, lane);
     up_tiles<BITS, G, NT>(a, expert, ti, tile);
-    up_pairs<E, BITS, G, 1, NT>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
+    up_pairs<E, BITS, G, 1, NT, true>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
   } else {
     live.fetch(a, 0, lane);
     const int expert = a.by_expert ? static_cast<int>(blockIdx.y) : find_expert(a, live, blockIdx.y, list, lane);
@@ -381,7 +378,9 @@ __global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_up_kernel(MoeArgs a)
     }
     if (n == 0) return;
     up_tiles<BITS, G, NT>(a, expert, ti, tile);
-    if (n <= 8) {
+    if (n <= 4) {
+      up_pairs<E, BITS, G, 1, NT>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
+    } else if (n <= 8) {
       up_pairs<E, BITS, G, 2, NT>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
     } else {
       for (int i = 0; i < n; i += 16) {
@@ -441,7 +440,9 @@ __global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_down_kernel(MoeArgs 
     tile[r] = {a.down_codes + blk * Block<BITS>::kBytes, a.down_scales + blk * (16 * G)};
   }
   const int* pair = a.chosen_pairs + blockIdx.y * kMoeBlockTokens;
-  if (n <= 8) {
+  if (n <= 4) {
+    down_pairs<E, BITS, G, 1, NT>(a, tile, ti, pair, n, lds, lane, wave, waves);
+  } else if (n <= 8) {
     down_pairs<E, BITS, G, 2, NT>(a, tile, ti, pair, n, lds, lane, wave, waves);
   } else {
     for (int i = 0; i < n; i += 16) {
@@ -479,24 +480,24 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
 }
 
 // Up to four tokens: one workgroup per 16 outputs takes all pairs, its waves
-// splitting (pair, block) among them, and writes y at once.  A pair's hidden
-// values are in its token's row alone, so the sums over the choices form in
-// the result registers.
+// splitting (pair, block) among them, and writes y at once.  Lane group g of a
+// result register belongs to token g, so the sums over a token's choices form
+// in one register.
 constexpr int kFewWaves = 16;
 
 template <class E, int BITS, int G>
 __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs a) {
   constexpr int P = E::kBytes == 2 ? 2 : 3;
-  using Src = SourcePlanes<P>;
-  using Prod = Product<BITS, G, 1, 1, Src>;
-  __shared__ float red[kFewWaves * Prod::kAll * 64];
+  using Prod = Product<BITS, G, 1, 1, SourcePlanes<P>>;
+  static_assert(Prod::kAll == 1);
+  __shared__ __align__(16) char lds[kFewWaves * Prod::X::kLdsBytes];
+  __shared__ float red[kFewWaves * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ti = blockIdx.x;
   const int total = a.T * a.k * a.blocks_f;
   int b = total * wave / kFewWaves;
   const int end = total * (wave + 1) / kFewWaves;
-  Prod p;
-  p.clear();
+  float sum = 0.f;
   while (b < end) {
     const int pair = b / a.blocks_f, b0 = b % a.blocks_f;
     const int b1 = b0 + (end - b) < a.blocks_f ? b0 + (end - b) : a.blocks_f;
@@ -504,19 +505,21 @@ __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs 
     const int expert = a.live[pair];
     if (expert < 0) continue;
     const typename Prod::X x(
-        Src{a.h_plane},
-        [&](int t) { return t == pair / a.k ? a.h + static_cast<int64_t>(pair) * a.h_row : nullptr; },
-        nullptr, lane);
+        {a.h_plane}, [&](int) { return a.h + static_cast<int64_t>(pair) * a.h_row; },
+        lds + wave * Prod::X::kLdsBytes, lane);
     const int64_t blk = (static_cast<int64_t>(expert) * a.tiles_d + ti) * a.blocks_f;
     const Tile tile[1] = {{a.down_codes + blk * Block<BITS>::kBytes, a.down_scales + blk * (16 * G)}};
-    p.template run<(P == 3 ? 1 : 2)>(x, tile, b0, b1, b1, lane);
+    Prod p;
+    p.clear();
+    p.template run<4>(x, tile, b0, b1, b1, lane);
+    if (result_token(0, lane) == pair / a.k) sum += p.acc[0][0][0];
   }
-  p.put(red, wave, lane);
+  red[wave * 64 + lane] = sum;
   __syncthreads();
   if (threadIdx.x >= 64) return;
   const int t = result_token(0, lane), n = ti * kTileRows + (lane & 15);
   if (t < a.T && n < a.d) {
-    const float v = joined<Prod::kAll>(red, kFewWaves, lane);
+    const float v = joined<1>(red, kFewWaves, lane);
     const int64_t at = static_cast<int64_t>(t) * a.ldy + n;
     if constexpr (E::kBytes == 2) static_cast<uint16_t*>(a.y)[at] = bf16_of(v);
     else static_cast<float*>(a.y)[at] = v;
@@ -546,7 +549,7 @@ template <class E, int BITS, int G, bool kFew, int NT>
 hipError_t go_up(const MoeArgs& a, hipStream_t s) {
   // the tiles that fill the last block of neurons are written too
   const dim3 grid(static_cast<unsigned>(a.blocks_f * (kBlockK / kTileRows) / NT), static_cast<unsigned>(a.most_chosen));
-  constexpr int kLds = wave_lds<UpProduct<E, BITS, G, kFew ? 1 : 4, NT>>();
+  constexpr int kLds = wave_lds<UpProduct<E, BITS, G, kFew ? 1 : 4, NT, !kFew>>();
   const int w = waves_for(static_cast<int64_t>(grid.x) * grid.y, a.blocks_d);
   moe_up_kernel<E, BITS, G, kFew, NT><<<grid, w * kWave, w * kLds, s>>>(a);
   return hipGetLastError();
