@@ -15,40 +15,17 @@ constexpr int kPackWaves = 4;
 template <int BITS, int GROUP>
 constexpr int scales_per_block() { return BITS == 4 ? kBlockK / GROUP : 1; }
 
-// Inputs k .. k+7 of one row as fp32, zeros from K on (p: the row).
-template <class E>
-__device__ __forceinline__ void row8(const void* base, int64_t row_off, int k, int K, bool whole, float (&f)[8]) {
-  if constexpr (E::kBytes == 2) {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + row_off + k;
-    if (whole) {
-      const u32x4_t v = *reinterpret_cast<const u32x4_a2_t*>(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(v[i] << 16);
-        f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = k + i < K ? bf16_bits_to_f32(p[i]) : 0.f;
-    }
-  } else {
-    const float* p = static_cast<const float*>(base) + row_off + k;
-    if (whole) {
-      const u32x4_t a = *reinterpret_cast<const u32x4_a4_t*>(p);
-      const u32x4_t b = *reinterpret_cast<const u32x4_a4_t*>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] = __uint_as_float(a[i]);
-        f[4 + i] = __uint_as_float(b[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = k + i < K ? p[i] : 0.f;
-    }
-  }
-}
-
 __device__ __forceinline__ uint32_t umax32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// w / s, correctly rounded, for s with 8 significant bits, inv = 1 / s correctly
+// rounded, and nothing near the ends of the exponent range: the product with
+// inv, corrected once by its exact rest.  (Checked against the division for
+// every mantissa of s and w.)  A third of the division's operations, and 16
+// divisions' worth of them was half of the pack kernel's time.
+__device__ __forceinline__ float divided(float w, float s, float inv) {
+  const float t = w * inv;
+  return fmaf(fmaf(-t, s, w), inv, t);
+}
 
 // Writes one block of 16 rows x 128 inputs; lane's 32 values in f[step][8].
 template <int BITS, int GROUP>
@@ -83,16 +60,31 @@ __device__ __forceinline__ void store_block(const float (&f)[4][8], uint8_t* cod
       const float sf = bf16_bits_to_f32(sc[gr]);
       const bool live = finite && sf > 0.f;
       const float div = live ? sf : 1.f;
+      const float inv = 1.0f / div;
+      // the rests of quotients below 1/4 may be lost without harm: they round to 0
+      const bool plain = div >= 0x1p-100f && div <= 0x1p100f;
+      float q[kSteps][8];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[s][i] = divided(f[gr * kSteps + s][i], div, inv);
+      if (!plain) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[s][i] = f[gr * kSteps + s][i] / div;
+      }
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         uint32_t w = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float q = fminf(fmaxf(rintf(f[gr * kSteps + s][i] / div), -7.f), 7.f);
-          const uint32_t u = live ? static_cast<uint32_t>(static_cast<int>(q) + 8) : 8u;
-          w |= u << (4 * (i >> 1) + 16 * (i & 1));
+          // adding 2^23 + 8 rounds to the nearest even whole number and leaves u = q + 8
+          // in the lowest bits
+          const float c = __builtin_amdgcn_fmed3f(q[s][i], -7.f, 7.f) + 8388616.f;
+          w |= (__float_as_uint(c) & 15u) << (4 * (i >> 1) + 16 * (i & 1));
         }
-        words[gr * kSteps + s] = __builtin_rotateleft32(w, 3);
+        words[gr * kSteps + s] = __builtin_rotateleft32(live ? w : 0x88888888u, 3);
       }
     }
     *reinterpret_cast<u32x4_t*>(codes + lane * 16) = words;
@@ -103,25 +95,41 @@ __device__ __forceinline__ void store_block(const float (&f)[4][8], uint8_t* cod
   }
 }
 
-// w [E][N][K], one wave per block.
+// w [E][N][K], one wave per block.  Like tokens, rows are read by rows and go
+// through LDS: bound by reading w.
 template <class E, int BITS, int GROUP>
 __global__ __launch_bounds__(kPackWaves* kWave) void weights_pack_kernel(WeightsArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kPackWaves + (threadIdx.x >> 6);
+  using Src = std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>;
+  using X = Tokens<Src, 4>;
+  __shared__ __align__(16) char lds[kPackWaves * X::kLdsBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kPackWaves + wave;
   if (id >= static_cast<int64_t>(a.tiles) * a.blocks) return;
   const int tile = static_cast<int>(id / a.blocks), b = static_cast<int>(id % a.blocks);
   const int64_t e = blockIdx.y;
-  const int row = tile * kTileRows + (lane & 15);
-  const int64_t row_off = (e * a.N + row) * a.K;
-  const bool whole = (b + 1) * kBlockK <= a.K;
+  const int row0 = tile * kTileRows, left = a.N - row0;
+  const X x({a.K},
+            [&](int r) {
+              return static_cast<const typename Src::Elem*>(a.w) + (e * a.N + row0 + (r < left ? r : 0)) * a.K;
+            },
+            lds + wave * X::kLdsBytes, lane);
+  typename X::Loaded q;
+  x.fetch(q, b, (b + 1) * kBlockK <= a.K, lane);
+  x.store(q, lane);
+  const int r = lane & 15;
   float f[4][8];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    if (row < a.N) {
-      row8<E>(a.w, row_off, b * kBlockK + 32 * s + 8 * (lane >> 4), a.K, whole, f[s]);
-    } else {
+    u32x4_t v[Src::kReads];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[s][i] = 0.f;
+    for (int i = 0; i < Src::kReads; ++i)
+      v[i] = *reinterpret_cast<const u32x4_t*>(x.lds + X::piece_at(r, Src::place(s, lane >> 4, i)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t u;
+      if constexpr (E::kBytes == 2) u = i & 1 ? v[0][i >> 1] & 0xffff0000u : v[0][i >> 1] << 16;
+      else u = v[i >> 2][i & 3];
+      f[s][i] = __uint_as_float(r < left ? u : 0u);
     }
   }
   const int64_t blk = (e * a.tiles + tile) * a.blocks + b;
@@ -134,14 +142,44 @@ __global__ __launch_bounds__(kPackWaves* kWave) void weights_pack_kernel(Weights
 template <class E, int BITS, int GROUP>
 __global__ __launch_bounds__(kPackWaves* kWave) void weights_pack_t_kernel(WeightsArgs a) {
   __shared__ float tile_f[64][kBlockK + 1];
+  using Elem = typename E::storage;
+  constexpr int kPer = E::kPer16B;      // rows of the result in one load
+  constexpr int kAcross = 64 / kPer;    // lanes along N
+  constexpr int kDown = 64 / kAcross;   // inputs per load
+  constexpr int kLoads = kBlockK / kDown / kPackWaves;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n_groups = (a.tiles + 3) / 4;
   const int tg = static_cast<int>(blockIdx.x % n_groups), b = static_cast<int>(blockIdx.x / n_groups);
   const int64_t e = blockIdx.y;
-  const int n = tg * 64 + lane;
-  for (int i = wave; i < kBlockK; i += kPackWaves) {
-    const int k = b * kBlockK + i;
-    tile_f[lane][i] = (k < a.K && n < a.N) ? load_elem<E>(a.w, (e * a.K + k) * a.N + n) : 0.f;
+  const int in = (lane % kAcross) * kPer, n = tg * 64 + in;
+  const Elem* w = static_cast<const Elem*>(a.w) + e * a.K * a.N;
+  if (tg * 64 + 64 <= a.N && (b + 1) * kBlockK <= a.K) {
+    u32x4_t v[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int64_t k = b * kBlockK + (j * kPackWaves + wave) * kDown + lane / kAcross;
+      if constexpr (E::kBytes == 2) v[j] = *reinterpret_cast<const u32x4_a2_t*>(w + k * a.N + n);
+      else v[j] = *reinterpret_cast<const u32x4_a4_t*>(w + k * a.N + n);
+    }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = (j * kPackWaves + wave) * kDown + lane / kAcross;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        uint32_t u;
+        if constexpr (E::kBytes == 2) u = c & 1 ? v[j][c >> 1] & 0xffff0000u : v[j][c >> 1] << 16;
+        else u = v[j][c];
+        tile_f[in + c][i] = __uint_as_float(u);
+      }
+    }
+  } else {
+    const int m = tg * 64 + lane;
+#pragma unroll
+    for (int j = 0; j < kBlockK / kPackWaves; ++j) {  // no branch: all loads at once
+      const int i = j * kPackWaves + wave, k = b * kBlockK + i;
+      const float v = load_elem<E>(w, static_cast<int64_t>(k < a.K ? k : a.K - 1) * a.N + (m < a.N ? m : a.N - 1));
+      tile_f[lane][i] = (k < a.K) & (m < a.N) ? v : 0.f;
+    }
   }
   __syncthreads();
   const int tile = tg * 4 + wave;
@@ -156,65 +194,73 @@ __global__ __launch_bounds__(kPackWaves* kWave) void weights_pack_t_kernel(Weigh
   store_block<BITS, GROUP>(f, a.codes + blk * Block<BITS>::kBytes, a.scales + blk * (16 * G), lane);
 }
 
-// The values the planes stand for, into w [E][N][K]; one wave per block.
+// The values the planes stand for, into w [E][N][K]; one wave per block, by rows
+// through LDS.  Bound by writing w.
 template <class E, int BITS, int GROUP>
 __global__ __launch_bounds__(kPackWaves* kWave) void weights_unpack_kernel(WeightsArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kPackWaves + (threadIdx.x >> 6);
+  using Elem = typename E::storage;
+  constexpr int kPieces = kBlockK / E::kPer16B;  // of 16 bytes in a row of the block
+  constexpr int kWaveBytes = 16 * kPieces * 16;
+  __shared__ __align__(16) char lds[kPackWaves * kWaveBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kPackWaves + wave;
   if (id >= static_cast<int64_t>(a.tiles) * a.blocks) return;
   const int tile = static_cast<int>(id / a.blocks), b = static_cast<int>(id % a.blocks);
   const int64_t e = blockIdx.y;
-  const int row = tile * kTileRows + (lane & 15);
   const int64_t blk = (e * a.tiles + tile) * a.blocks + b;
   constexpr int G = scales_per_block<BITS, GROUP>();
   Block<BITS> q;
   q.template load<false>(a.codes + blk * Block<BITS>::kBytes, lane);
   Scales<G> sc;
   if constexpr (BITS == 4) sc.load(a.scales + blk * (16 * G), lane);
-  if (row >= a.N) return;
-  const int64_t row_off = (e * a.N + row) * a.K;
+  char* mine = lds + wave * kWaveBytes;
+  auto piece_at = [&](int r, int c) { return mine + r * kPieces * 16 + ((c ^ r) << 4); };
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    float f[8];
+    const int r = lane & 15, g = lane >> 4;
     if constexpr (BITS == 16) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = bf16_bits_to_f32(i & 1 ? q.c[s][i >> 1] >> 16 : q.c[s][i >> 1] & 0xffffu);
+      *reinterpret_cast<u32x4_t*>(piece_at(r, 4 * s + g)) = q.c[s];
     } else {
+      float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int u = static_cast<int>(__builtin_rotateright32(q.c[s], 3 + 4 * (i >> 1) + 16 * (i & 1)) & 15u);
         f[i] = static_cast<float>(u - 8) * sc.at(s * G / 4);
       }
-    }
-    const int k = b * kBlockK + 32 * s + 8 * (lane >> 4);
-    const bool whole = k + 8 <= a.K;
-    if constexpr (E::kBytes == 4) {
-      float* p = static_cast<float*>(a.out) + row_off + k;
-      if (whole) {
-        u32x4_t lo, hi;
+      if constexpr (E::kBytes == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lo[i] = __float_as_uint(f[i]);
-          hi[i] = __float_as_uint(f[4 + i]);
+        for (int h = 0; h < 2; ++h) {
+          u32x4_t v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(f[4 * h + i]);
+          *reinterpret_cast<u32x4_t*>(piece_at(r, 8 * s + 2 * g + h)) = v;
         }
-        *reinterpret_cast<u32x4_a4_t*>(p) = lo;
-        *reinterpret_cast<u32x4_a4_t*>(p + 4) = hi;
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (k + i < a.K) p[i] = f[i];
-      }
-    } else {
-      uint16_t* p = static_cast<uint16_t*>(a.out) + row_off + k;
-      if (whole) {
         u32x4_t v;
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = bf16_of(f[2 * j]) | (static_cast<uint32_t>(bf16_of(f[2 * j + 1])) << 16);
-        *reinterpret_cast<u32x4_a2_t*>(p) = v;
-      } else {
+        *reinterpret_cast<u32x4_t*>(piece_at(r, 4 * s + g)) = v;
+      }
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  const int row0 = tile * kTileRows;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (k + i < a.K) p[i] = bf16_of(f[i]);
+  for (int j = 0; j < kPieces / 4; ++j) {  // 64 pieces are 64 / kPieces rows
+    const int r = (j * 64 + lane) / kPieces, c = lane % kPieces;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(piece_at(r, c));
+    const int k = b * kBlockK + c * E::kPer16B;
+    if (row0 + r >= a.N) continue;
+    Elem* p = static_cast<Elem*>(a.out) + (e * a.N + row0 + r) * a.K + k;
+    if (k + E::kPer16B <= a.K) {
+      if constexpr (E::kBytes == 2) *reinterpret_cast<u32x4_a2_t*>(p) = v;
+      else *reinterpret_cast<u32x4_a4_t*>(p) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < E::kPer16B; ++i) {
+        if (k + i >= a.K) break;
+        if constexpr (E::kBytes == 2) p[i] = static_cast<uint16_t>(v[i >> 1] >> (16 * (i & 1)));
+        else p[i] = __uint_as_float(v[i]);
       }
     }
   }
