@@ -1,6 +1,6 @@
 // Laying out weights for the few-token products (few_token.hpp), and reading
 // them back.  4 bits: each group of 32, 64 or 128 consecutive inputs of a row
-// has one scale s = bf16(max|w| / 7), the quotient in fp32; codes are
+// has one scale s = bf16(max|w| * r), r = 1/7 in fp32; codes are
 // q = rne(w / s) clamped to -7 .. 7 and stored as q + 8.  A group that holds an
 // infinity or a NaN gets a NaN scale, so that every value of it reads back as
 // NaN instead of as something plausible.
@@ -56,7 +56,7 @@ __device__ __forceinline__ void store_block(const float (&f)[4][8], uint8_t* cod
       m = umax32(m, __shfl_xor(m, 16));
       m = umax32(m, __shfl_xor(m, 32));
       const bool finite = m < 0x7f800000u;
-      sc[gr] = finite ? bf16_of(__uint_as_float(m) / 7.0f) : static_cast<uint16_t>(0x7fc0);
+      sc[gr] = finite ? bf16_of(__uint_as_float(m) * (1.0f / 7.0f)) : static_cast<uint16_t>(0x7fc0);
       const float sf = bf16_bits_to_f32(sc[gr]);
       const bool live = finite && sf > 0.f;
       const float div = live ? sf : 1.f;

@@ -306,9 +306,10 @@ twell_status twell_weights_sizes(const twell_wdesc* d, twell_wsizes_t* out);
  * [experts][cols][rows] (w_down as the layer above keeps it, one row per
  * neuron, is the transposed form of its d_model x d_ff matrix); contiguous,
  * bf16, or fp32 when bits = 4.
- * bits = 4: scale s = bf16(max|w| / 7) of the group (fp32 quotient), code
- * q = w / s rounded to nearest even and clamped to -7 .. 7 (0 where s = 0).  A group that
- * holds an infinity or a NaN gets a NaN scale: all its values become NaN. */
+ * bits = 4: scale s = bf16(max|w| * r) of the group, r = 1/7 in fp32; code q =
+ * w / s in fp32, rounded to nearest even and clamped to -7 .. 7 (0 where s = 0).
+ * A group that holds an infinity or a NaN gets a NaN scale: all its values
+ * become NaN. */
 twell_status twell_weights_pack(const twell_wdesc* d, const void* w, int32_t w_dtype, int32_t transposed,
                                 twell_wplanes out, void* stream);
 

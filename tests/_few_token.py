@@ -38,7 +38,7 @@ def quantise(w: np.ndarray, group: int) -> np.ndarray:
         p = w[..., a:a + group]
         bad = ~np.isfinite(p).all(-1, keepdims=True)
         m = np.abs(np.where(np.isfinite(p), p, 0)).max(-1, keepdims=True)
-        s = bf16_round(m / np.float32(7))
+        s = bf16_round(m * np.float32(1 / 7))
         live = (s > 0) & ~bad
         with np.errstate(all="ignore"):
             q = np.clip(np.rint((p / np.where(live, s, np.float32(1))).astype(np.float32)), -7, 7)
