@@ -340,9 +340,13 @@ def twell_dense_ffn_fwd(desc: Desc, x, w_gate_t, w_up_t, w_down, y, ws, stream=N
 
 
 # ----------------------------------------------------------------------------- serving a few tokens
+# A call here takes a few microseconds of GPU time, so its host cost sets the
+# pace: the C structs of a descriptor are kept on it, and the checks below are
+# one condition each, with the reason worked out only when it fails.
 ACTIVATIONS = {"relu": 0, "silu": 1}
 _TORCH = {"bf16": torch.bfloat16, "fp32": torch.float32}
 _CODE = {torch.bfloat16: TWELL_BF16, torch.float32: TWELL_FP32}
+_CODE_DTYPE, _SCALE_DTYPE = torch.uint8, torch.bfloat16
 
 
 @dataclass(frozen=True)
@@ -354,6 +358,17 @@ class WDesc:
     cols: int
     bits: int
     group: int = 0
+
+    @functools.cached_property
+    def _ref(self):
+        return ctypes.byref(CWDesc(int(self.experts), int(self.rows), int(self.cols), int(self.bits), int(self.group)))
+
+    @functools.cached_property
+    def plane_bytes(self) -> tuple:
+        """Bytes of the planes (codes, scales)."""
+        out = CWSizes()
+        _check("twell_weights_sizes", library().twell_weights_sizes(self._ref, ctypes.byref(out)))
+        return int(out.codes), int(out.scales)
 
 
 class Weights(NamedTuple):
@@ -376,19 +391,38 @@ class MoeDesc:
     act: str = "silu"  # "relu" | "silu"
     renorm: bool = True
 
-    @property
+    @functools.cached_property
     def torch_dtype(self) -> torch.dtype:
         return _TORCH[self.dtype]
 
-    @property
+    @functools.cached_property
     def in_desc(self) -> WDesc:
         """Of the gate and the up projections: d_model -> d_ff."""
         return WDesc(self.experts, self.d_ff, self.d_model, self.bits, self.group)
 
-    @property
+    @functools.cached_property
     def out_desc(self) -> WDesc:
         """Of the down projections: d_ff -> d_model."""
         return WDesc(self.experts, self.d_model, self.d_ff, self.bits, self.group)
+
+    def _strided(self, ldx: int, ldy: int):
+        if self.act not in ACTIVATIONS or self.dtype not in _TORCH:
+            raise ValueError(f"act {self.act!r}, dtype {self.dtype!r}: expected one of {tuple(ACTIVATIONS)} and "
+                             f"{tuple(_TORCH)}")
+        return ctypes.byref(CMoeDesc(
+            int(self.T), int(ldx), int(ldy), int(self.d_model), int(self.d_ff), int(self.experts), int(self.top_k),
+            _CODE[self.torch_dtype], int(self.bits), int(self.group), ACTIVATIONS[self.act], int(bool(self.renorm))))
+
+    @functools.cached_property
+    def _ref(self):  # contiguous rows
+        return self._strided(self.d_model, self.d_model)
+
+    @functools.cached_property
+    def ws_bytes(self) -> int:
+        """Bytes of twell_moe_fwd's workspace."""
+        out = ctypes.c_size_t()
+        _check("twell_moe_sizes", library().twell_moe_sizes(self._ref, ctypes.byref(out)))
+        return int(out.value)
 
 
 class MoeWeights(NamedTuple):
@@ -403,40 +437,18 @@ class MoeOut(NamedTuple):
     weights: torch.Tensor  # fp32 [T, top_k]
 
 
-@functools.lru_cache(maxsize=256)
-def _cwdesc(desc: WDesc) -> CWDesc:
-    return CWDesc(int(desc.experts), int(desc.rows), int(desc.cols), int(desc.bits), int(desc.group))
-
-
-@functools.lru_cache(maxsize=256)
 def _weights_sizes(desc: WDesc) -> tuple:
-    out = CWSizes()
-    _check("twell_weights_sizes", library().twell_weights_sizes(ctypes.byref(_cwdesc(desc)), ctypes.byref(out)))
-    return int(out.codes), int(out.scales)
+    return desc.plane_bytes
 
 
-@functools.lru_cache(maxsize=256)
-def _cmoedesc(desc: MoeDesc, ldx: int, ldy: int) -> CMoeDesc:
-    if desc.act not in ACTIVATIONS or desc.dtype not in _TORCH:
-        raise ValueError(f"act {desc.act!r}, dtype {desc.dtype!r}: expected one of {tuple(ACTIVATIONS)} and "
-                         f"{tuple(_TORCH)}")
-    return CMoeDesc(int(desc.T), int(ldx), int(ldy), int(desc.d_model), int(desc.d_ff), int(desc.experts),
-                    int(desc.top_k), TWELL_BF16 if desc.dtype == "bf16" else TWELL_FP32, int(desc.bits),
-                    int(desc.group), ACTIVATIONS[desc.act], int(bool(desc.renorm)))
-
-
-@functools.lru_cache(maxsize=256)
 def moe_ws_bytes(desc: MoeDesc) -> int:
-    out = ctypes.c_size_t()
-    _check("twell_moe_sizes", library().twell_moe_sizes(
-        ctypes.byref(_cmoedesc(desc, desc.d_model, desc.d_model)), ctypes.byref(out)))
-    return int(out.value)
+    return desc.ws_bytes
 
 
 def alloc_weights(desc: WDesc, device="cuda") -> Weights:
-    codes, scales = _weights_sizes(desc)
-    return Weights(torch.empty(codes, dtype=torch.uint8, device=device),
-                   torch.empty(scales // 2, dtype=torch.bfloat16, device=device))
+    codes, scales = desc.plane_bytes
+    return Weights(torch.empty(codes, dtype=_CODE_DTYPE, device=device),
+                   torch.empty(scales // 2, dtype=_SCALE_DTYPE, device=device))
 
 
 def alloc_moe_weights(desc: MoeDesc, device="cuda") -> MoeWeights:
@@ -451,13 +463,22 @@ def alloc_moe_out(desc: MoeDesc, device="cuda") -> MoeOut:
 
 
 def alloc_moe_ws(desc: MoeDesc, device="cuda") -> torch.Tensor:
-    return torch.empty(moe_ws_bytes(desc), dtype=torch.uint8, device=device)
+    return torch.empty(desc.ws_bytes, dtype=torch.uint8, device=device)
+
+
+def _fit(t, name: str, nbytes: int, dtype: torch.dtype) -> int:
+    """Pointer of a contiguous GPU tensor of the dtype with at least nbytes."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.nbytes >= nbytes and t.is_contiguous():
+        return t.data_ptr()
+    if t is None:
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    return _ptr(t, name, nbytes, dtype)  # says what is wrong
 
 
 def _planes(desc: WDesc, w: Weights, name: str) -> CPlanes:
-    codes, scales = _weights_sizes(desc)
-    return CPlanes(_ptr(w.codes, name + ".codes", codes, torch.uint8),
-                   _ptr(w.scales, name + ".scales", scales, torch.bfloat16) if scales else 0)
+    codes, scales = desc.plane_bytes
+    return CPlanes(_fit(w.codes, name + ".codes", codes, _CODE_DTYPE),
+                   _fit(w.scales, name + ".scales", scales, _SCALE_DTYPE) if scales else 0)
 
 
 def _rows(t: torch.Tensor, name: str, n: int, width: int, dtype: torch.dtype) -> tuple:
@@ -466,10 +487,12 @@ def _rows(t: torch.Tensor, name: str, n: int, width: int, dtype: torch.dtype) ->
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a GPU tensor (got {t.device})")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
+    if t.shape != (n, width):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n, width)}")
+    if t.is_contiguous():
+        return t.data_ptr(), width
     s0, s1 = t.stride()
     if width > 1 and s1 != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
@@ -478,54 +501,75 @@ def _rows(t: torch.Tensor, name: str, n: int, width: int, dtype: torch.dtype) ->
     return t.data_ptr(), s0 if n > 1 else width
 
 
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """The stream's handle; by default the one current on t's device."""
+    if stream is None:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
+
+
+# The handle alone: building a Stream object costs more than the other checks of a call together.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _any_dtype(t, name: str) -> int:
+    code = _CODE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    return code
+
+
 def twell_weights_pack(desc: WDesc, w, planes: Weights, transposed: bool = False, stream=None):
     """Lay out w [experts, rows, cols] ([experts, cols, rows] if transposed; bf16, or fp32 for 4 bits) into planes."""
-    if not isinstance(w, torch.Tensor):
-        raise TypeError("w: expected a torch.Tensor")
-    if w.dtype not in _CODE:
-        raise ValueError(f"w: dtype {w.dtype}, expected torch.bfloat16 or torch.float32")
-    n = desc.experts * desc.rows * desc.cols
-    _check("twell_weights_pack", library().twell_weights_pack(
-        ctypes.byref(_cwdesc(desc)), _ptr(w, "w", n * w.element_size()), _CODE[w.dtype], int(bool(transposed)),
-        _planes(desc, planes, "planes"), _stream(stream)))
+    code = _any_dtype(w, "w")
+    n = desc.experts * desc.rows * desc.cols * w.element_size()
+    st = library().twell_weights_pack(desc._ref, _fit(w, "w", n, w.dtype), code, 1 if transposed else 0,
+                                      _planes(desc, planes, "planes"), _stream_of(w, stream))
+    if st:
+        _check("twell_weights_pack", st)
 
 
 def twell_weights_unpack(desc: WDesc, planes: Weights, w, stream=None):
     """Write the values that planes stand for to w [experts, rows, cols] (bf16, or fp32 for 4 bits)."""
-    if not isinstance(w, torch.Tensor):
-        raise TypeError("w: expected a torch.Tensor")
-    if w.dtype not in _CODE:
-        raise ValueError(f"w: dtype {w.dtype}, expected torch.bfloat16 or torch.float32")
-    n = desc.experts * desc.rows * desc.cols
-    _check("twell_weights_unpack", library().twell_weights_unpack(
-        ctypes.byref(_cwdesc(desc)), _planes(desc, planes, "planes"), _ptr(w, "w", n * w.element_size()),
-        _CODE[w.dtype], _stream(stream)))
+    code = _any_dtype(w, "w")
+    n = desc.experts * desc.rows * desc.cols * w.element_size()
+    st = library().twell_weights_unpack(desc._ref, _planes(desc, planes, "planes"), _fit(w, "w", n, w.dtype), code,
+                                        _stream_of(w, stream))
+    if st:
+        _check("twell_weights_unpack", st)
 
 
 def twell_linear_fwd(desc: WDesc, planes: Weights, x, y, stream=None):
     """y [T, rows] = x [T, cols] times one matrix of 4-bit weights; x and y in bf16 or fp32, rows may be strided."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _CODE or x.dim() != 2:
-        raise ValueError("x: expected a 2-d torch.bfloat16 or torch.float32 tensor")
-    T = x.shape[0]
-    px, ldx = _rows(x, "x", T, desc.cols, x.dtype)
-    py, ldy = _rows(y, "y", T, desc.rows, x.dtype)
-    _check("twell_linear_fwd", library().twell_linear_fwd(
-        ctypes.byref(_cwdesc(desc)), _planes(desc, planes, "planes"), T, _CODE[x.dtype], px, ldx, py, ldy,
-        _stream(stream)))
+    code = _any_dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected {('T', desc.cols)}")
+    T, dtype = x.shape[0], x.dtype
+    px, ldx = _rows(x, "x", T, desc.cols, dtype)
+    py, ldy = _rows(y, "y", T, desc.rows, dtype)
+    st = library().twell_linear_fwd(desc._ref, _planes(desc, planes, "planes"), T, code, px, ldx, py, ldy,
+                                    _stream_of(x, stream))
+    if st:
+        _check("twell_linear_fwd", st)
 
 
 def twell_moe_fwd(desc: MoeDesc, x, w_router, weights: MoeWeights, out: MoeOut, ws, router_bias=None, stream=None):
     """Router, chosen experts and their weighted sum for desc.T tokens (see include/twell.h).  x and out.y may have
     strided rows; ws holds moe_ws_bytes(desc) bytes."""
-    dt = desc.torch_dtype
-    px, ldx = _rows(x, "x", desc.T, desc.d_model, dt)
-    py, ldy = _rows(out.y, "out.y", desc.T, desc.d_model, dt)
+    dt, d, T = desc.torch_dtype, desc.d_model, desc.T
+    px, ldx = _rows(x, "x", T, d, dt)
+    py, ldy = _rows(out.y, "out.y", T, d, dt)
     din, dout = desc.in_desc, desc.out_desc
-    pairs = desc.T * desc.top_k * 4
-    _check("twell_moe_fwd", library().twell_moe_fwd(
-        ctypes.byref(_cmoedesc(desc, ldx, ldy)), px,
-        _ptr(w_router, "w_router", desc.experts * desc.d_model * (2 if desc.dtype == "bf16" else 4), dt),
-        _ptr(router_bias, "router_bias", desc.experts * 4, torch.float32), _planes(din, weights.gate, "gate"),
-        _planes(din, weights.up, "up"), _planes(dout, weights.down, "down"), py,
-        _ptr(out.ids, "out.ids", pairs, torch.int32), _ptr(out.weights, "out.weights", pairs, torch.float32),
-        _ptr(ws, "ws", moe_ws_bytes(desc)), ctypes.c_size_t(ws.nbytes if ws is not None else 0), _stream(stream)))
+    pairs, need = T * desc.top_k * 4, desc.ws_bytes
+    st = library().twell_moe_fwd(
+        desc._ref if ldx == d and ldy == d else desc._strided(ldx, ldy), px,
+        _fit(w_router, "w_router", desc.experts * d * dt.itemsize, dt),
+        _fit(router_bias, "router_bias", desc.experts * 4, torch.float32) if router_bias is not None else None,
+        _planes(din, weights.gate, "gate"), _planes(din, weights.up, "up"), _planes(dout, weights.down, "down"), py,
+        _fit(out.ids, "out.ids", pairs, torch.int32), _fit(out.weights, "out.weights", pairs, torch.float32),
+        _fit(ws, "ws", need, torch.uint8), need, _stream_of(x, stream))
+    if st:
+        _check("twell_moe_fwd", st)
