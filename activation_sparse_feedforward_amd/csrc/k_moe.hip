@@ -6,10 +6,10 @@
 // (1) moe_route_kernel: one workgroup per token, logits in fp32, selection by
 // one wave.  (2) moe_up_kernel: one workgroup per (chosen expert, NT tiles of
 // 16 neurons); it gathers the expert's tokens, computes gate and up together
-// and writes h = w * act(g) * u.  (3) Up to four tokens: moe_down_few_kernel,
-// one workgroup per 16 outputs for all choices.  More: moe_down_kernel, one
-// workgroup per (chosen expert, NT tiles of 16 outputs), writes every pair's
-// part and moe_join_kernel adds them up in the order of the choices.
+// and writes h = w * act(g) * u.  (3) moe_down_kernel: one workgroup per
+// (chosen expert, NT tiles of 16 outputs), writes every pair's part, and
+// (4) moe_join_kernel adds them up in the order of the choices; one or two
+// tokens with little to read take moe_down_few_kernel instead of both.
 // Nothing depends on timing.  Only chosen experts' weights are read, each once
 // per 16 of its tokens.  Bound by reading them.
 #include "few_token.hpp"
@@ -348,6 +348,13 @@ __device__ __forceinline__ void up_pairs(const MoeArgs& a, const Tiles<2 * NT>& 
   }
 }
 
+// The row's expert and pairs for the down kernel.
+__device__ __forceinline__ void hand_on(const MoeArgs& a, int expert, int n, const WaveList& list, int lane, int wave) {
+  if (blockIdx.x != 0 || wave != 0) return;
+  if (lane == 0) a.chosen[blockIdx.y] = MoeChosen{expert, n};
+  if (lane < n) a.chosen_pairs[blockIdx.y * kMoeBlockTokens + lane] = list.pair[lane];
+}
+
 // kFew: up to four tokens.  Where there are at least as many pairs as experts,
 // nearly every expert has a token: row y of the grid is then expert y, which
 // needs no search.
@@ -364,18 +371,16 @@ __global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_up_kernel(MoeArgs a)
   if constexpr (kFew) {
     live.fetch(a, 0, lane);
     const int expert = find_expert(a, live, blockIdx.y, list, lane);
-    if (expert < 0) return;  // the whole workgroup
-    const int n = find_pairs(a, live, expert, list, lane);
+    const int n = expert < 0 ? 0 : find_pairs(a, live, expert, list, lane);
+    hand_on(a, expert, n, list, lane, wave);
+    if (n == 0) return;  // the whole workgroup
     up_tiles<BITS, G, NT>(a, expert, ti, tile);
     up_pairs<E, BITS, G, 1, NT, true>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
   } else {
     live.fetch(a, 0, lane);
     const int expert = a.by_expert ? static_cast<int>(blockIdx.y) : find_expert(a, live, blockIdx.y, list, lane);
     const int n = expert < 0 ? 0 : find_pairs(a, live, expert, list, lane);
-    if (blockIdx.x == 0 && wave == 0) {  // for the down kernel
-      if (lane == 0) a.chosen[blockIdx.y] = MoeChosen{expert, n};
-      if (lane < n) a.chosen_pairs[blockIdx.y * kMoeBlockTokens + lane] = list.pair[lane];
-    }
+    hand_on(a, expert, n, list, lane, wave);
     if (n == 0) return;
     up_tiles<BITS, G, NT>(a, expert, ti, tile);
     if (n <= 4) {
@@ -479,10 +484,10 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
   else static_cast<float*>(a.y)[at] = v;
 }
 
-// Up to four tokens: one workgroup per 16 outputs takes all pairs, its waves
-// splitting (pair, block) among them, and writes y at once.  Lane group g of a
-// result register belongs to token g, so the sums over a token's choices form
-// in one register.
+// One or two tokens and little to read: one workgroup per 16 outputs takes all
+// pairs, its waves splitting (pair, block) among them, and writes y at once.
+// Lane group g of a result register belongs to token g, so the sums over a
+// token's choices form in one register.
 constexpr int kFewWaves = 16;
 
 template <class E, int BITS, int G>
@@ -573,16 +578,23 @@ hipError_t go_down(const MoeArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Tokens, and bytes of the down projections of their pairs, up to which the one
+// kernel for few tokens is the faster (a whole call, both ways: 1 token, 2 of 8
+// bf16 experts, 16 MB 16.9 against 21.0 us; 1 token, 8 of 64, 32 MB 31.8 against
+// 28.7; 4 tokens, 8 of 64 in 4 bits, 32 MB 35.6 against 31.6).
+constexpr int kFewTokens = 2;
+constexpr int64_t kFewBytes = int64_t(24) << 20;
+
 template <class E, int BITS, int G>
 hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
-  if (a.T <= 4) {
-    const hipError_t e = go_up<E, BITS, G, true, 1>(a, s);
-    if (e != hipSuccess) return e;
+  const hipError_t e = a.T <= 4 ? go_up<E, BITS, G, true, 1>(a, s)
+                                : go_up<E, BITS, G, false, BITS == 16 || E::kBytes == 4 ? 1 : 2>(a, s);
+  if (e != hipSuccess) return e;
+  if (a.T <= kFewTokens &&
+      static_cast<int64_t>(a.T) * a.k * a.tiles_d * a.blocks_f * Block<BITS>::kBytes <= kFewBytes) {
     moe_down_few_kernel<E, BITS, G><<<a.tiles_d, kFewWaves * kWave, 0, s>>>(a);
     return hipGetLastError();
   }
-  const hipError_t e = go_up<E, BITS, G, false, BITS == 16 || E::kBytes == 4 ? 1 : 2>(a, s);
-  if (e != hipSuccess) return e;
   return go_down<E, BITS, G, BITS == 16 || E::kBytes == 4 ? 2 : 4>(a, s);
 }
 
