@@ -205,6 +205,8 @@ struct MoeArgs {
   float inv_k;        // 1 / k
   int32_t by_expert;  // more than four tokens: row y of the grids is expert y, not the y-th chosen one
   // workspace
+  int32_t own_logits;  // up to four tokens: the up kernel computes the logits (set by the launcher)
+  float* logits;       // [min(T, 4)][E]
   int32_t* live;       // [T x k] ids, or -1 where the weight is 0
   uint16_t* h;         // [planes][T * k][blocks_f * 128] hidden values of each (token, choice) pair
   int64_t h_plane, h_row;

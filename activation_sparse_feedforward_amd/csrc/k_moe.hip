@@ -4,7 +4,7 @@
 //   y[t]   = sum_i w_i  W_down_e ( act(W_gate_e x) * (W_up_e x) ),   e = ids[t,i]
 //
 // (1) moe_route_kernel: one workgroup per token, logits in fp32, selection by
-// one wave.  (2) moe_up_kernel: one workgroup per (chosen expert, NT tiles of
+// one wave (up to four tokens: moe_logits_kernel, or nothing).  (2) moe_up_kernel: one workgroup per (chosen expert, NT tiles of
 // 16 neurons); it gathers the expert's tokens, computes gate and up together
 // and writes h = w * act(g) * u.  (3) moe_down_kernel: one workgroup per
 // (chosen expert, NT tiles of 16 outputs), writes every pair's part, and
@@ -17,6 +17,9 @@
 
 namespace twell {
 namespace {
+
+// Most waves of a workgroup of the up and down kernels (chosen at launch).
+constexpr int kMostWaves = 8;
 
 // ---------------------------------------------------------------- router
 constexpr int kRouteWaves = 16;
@@ -73,67 +76,73 @@ struct Eight {
 };
 
 // s[j] += x . r[j] over inputs [k0, k0 + 512 U), eight per lane and 512; all
-// loads ahead of all sums, since one workgroup has a CU's share of the
-// bandwidth to itself and is bound by how much it has in flight.
-template <class E, int U>
-__device__ __forceinline__ void route_dots(const typename E::storage* x, const typename E::storage* const (&r)[kRouteAhead],
-                                           int k, float (&s)[kRouteAhead]) {
-  Eight<E> xv[U], rv[U][kRouteAhead];
+// loads ahead of all sums, since what bounds a wave is how much it has in flight.
+template <class E, int U, int J>
+__device__ __forceinline__ void route_dots(const typename E::storage* x, const typename E::storage* const (&r)[J], int k,
+                                           float (&s)[J]) {
+  Eight<E> xv[U], rv[U][J];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     xv[u].load(x + k + 512 * u);
 #pragma unroll
-    for (int j = 0; j < kRouteAhead; ++j) rv[u][j].load(r[j] + k + 512 * u);
+    for (int j = 0; j < J; ++j) rv[u][j].load(r[j] + k + 512 * u);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int j = 0; j < kRouteAhead; ++j) s[j] = xv[u].dot(rv[u][j], s[j]);
+    for (int j = 0; j < J; ++j) s[j] = xv[u].dot(rv[u][j], s[j]);
 }
 
-// kRegs * 64 >= E.
-template <class E, int kRegs>
-__global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a) {
-  __shared__ float logit[kRegs * 64];
+// Logits of token t and experts [e0, e0 + J), in every lane; of experts that do
+// not exist: the last one's.
+template <class E, int J>
+__device__ __forceinline__ void route_logits(const MoeArgs& a, int64_t t, int e0, int lane, float (&s)[J]) {
   using Elem = typename E::storage;
   constexpr int U = E::kBytes == 2 ? 4 : 2;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = blockIdx.x;
   const Elem* x = static_cast<const Elem*>(a.x) + t * a.ldx;
-  for (int e0 = wave * kRouteAhead; e0 < a.E; e0 += kRouteWaves * kRouteAhead) {
-    const Elem* r[kRouteAhead];
+  const Elem* r[J];
 #pragma unroll
-    for (int j = 0; j < kRouteAhead; ++j)
-      r[j] = static_cast<const Elem*>(a.router) + static_cast<int64_t>(e0 + j < a.E ? e0 + j : a.E - 1) * a.d;
-    float s[kRouteAhead] = {};
-    int k0 = 0;
-    for (; k0 + 512 * U <= a.d; k0 += 512 * U) route_dots<E, U>(x, r, k0 + lane * 8, s);
-    for (; k0 + 512 <= a.d; k0 += 512) route_dots<E, 1>(x, r, k0 + lane * 8, s);
-    const int k = k0 + lane * 8;
-    if (k + 8 <= a.d) {
-      route_dots<E, 1>(x, r, k, s);
-    } else {
-      for (int i = k; i < a.d; ++i) {
-        const float xv = load_elem<E>(x, i);
+  for (int j = 0; j < J; ++j) {
+    r[j] = static_cast<const Elem*>(a.router) + static_cast<int64_t>(e0 + j < a.E ? e0 + j : a.E - 1) * a.d;
+    s[j] = 0.f;
+  }
+  int k0 = 0;
+  for (; k0 + 512 * U <= a.d; k0 += 512 * U) route_dots<E, U>(x, r, k0 + lane * 8, s);
+  for (; k0 + 512 <= a.d; k0 += 512) route_dots<E, 1>(x, r, k0 + lane * 8, s);
+  const int k = k0 + lane * 8;
+  if (k + 8 <= a.d) {
+    route_dots<E, 1>(x, r, k, s);
+  } else {
+    for (int i = k; i < a.d; ++i) {
+      const float xv = load_elem<E>(x, i);
 #pragma unroll
-        for (int j = 0; j < kRouteAhead; ++j) s[j] = fmaf(xv, load_elem<E>(r[j], i), s[j]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kRouteAhead; ++j) {
-      const float l = wave_sum(s[j]);
-      if (lane == 0 && e0 + j < a.E) logit[e0 + j] = a.bias ? l + a.bias[e0 + j] : l;
+      for (int j = 0; j < J; ++j) s[j] = fmaf(xv, load_elem<E>(r[j], i), s[j]);
     }
   }
-  __syncthreads();
-  if (wave != 0) return;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    s[j] = wave_sum(s[j]);
+    if (a.bias) s[j] += a.bias[e0 + j < a.E ? e0 + j : a.E - 1];
+  }
+}
 
-  // expert e = 64 r + lane is in key[r]
+// A token's choices from its logits, by one wave: lane i < top_k has choice i.
+struct Choice {
+  int id;
+  float weight;
+  // a choice of weight 0 is no choice; a NaN weight is one
+  __device__ __forceinline__ int live() const { return weight == 0.f ? -1 : id; }
+};
+template <int kRegs>  // kRegs * 64 >= E
+__device__ __forceinline__ Choice choose(const MoeArgs& a, const float* logit, int lane) {
+  float l[kRegs];  // expert e = 64 r + lane is in l[r] and key[r]
   uint32_t key[kRegs];
   uint32_t top = 0;
 #pragma unroll
+  for (int r = 0; r < kRegs; ++r) l[r] = r * 64 + lane < a.E ? logit[r * 64 + lane] : 0.f;
+#pragma unroll
   for (int r = 0; r < kRegs; ++r) {
-    key[r] = r * 64 + lane < a.E ? order_key(logit[r * 64 + lane]) : 0u;
+    key[r] = r * 64 + lane < a.E ? order_key(l[r]) : 0u;
     top = key[r] > top ? key[r] : top;
   }
   const float most = key_value(wave_umax(top));
@@ -141,10 +150,10 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
   float sum = 0.f;
 #pragma unroll
   for (int r = 0; r < kRegs; ++r)
-    if (r * 64 + lane < a.E) sum += expf(logit[r * 64 + lane] - most);
+    if (r * 64 + lane < a.E) sum += expf(l[r] - most);
   sum = wave_sum(sum);
 
-  uint32_t mine_key = 0;  // lane i keeps choice i
+  uint32_t mine_key = 0;
   int mine_id = 0;
   for (int i = 0; i < a.k; ++i) {
     uint32_t m = 0;
@@ -156,9 +165,9 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
     for (int r = 0; r < kRegs; ++r) {
       const uint64_t has = __ballot(key[r] == m);
       if (id < 0 && has != 0) {
-        const int l = __builtin_ctzll(has);
-        id = r * 64 + l;
-        if (lane == l) key[r] = 0;
+        const int at = __builtin_ctzll(has);
+        id = r * 64 + at;
+        if (lane == at) key[r] = 0;
       }
     }
     if (lane == i) {
@@ -168,18 +177,87 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
   }
   float mine = lane < a.k && !none ? expf(key_value(mine_key) - most) / sum : 0.f;
   if (a.renorm && !none) mine /= wave_sum(mine);
-  if (lane < a.k) {
-    a.ids[t * a.k + lane] = mine_id;
-    a.weights[t * a.k + lane] = mine;
-    // a choice of weight 0 is no choice; a NaN weight is one
-    a.live[t * a.k + lane] = mine == 0.f ? -1 : mine_id;
+  return {mine_id, mine};
+}
+__device__ __forceinline__ Choice choose(const MoeArgs& a, const float* logit, int lane) {
+  if (a.E <= 64) return choose<1>(a, logit, lane);
+  if (a.E <= 256) return choose<4>(a, logit, lane);
+  return choose<kMoeMaxExperts / 64>(a, logit, lane);
+}
+
+__device__ __forceinline__ void tell_choice(const MoeArgs& a, int64_t t, const Choice& c, int lane) {
+  if (lane >= a.k) return;
+  a.ids[t * a.k + lane] = c.id;
+  a.weights[t * a.k + lane] = c.weight;
+  a.live[t * a.k + lane] = c.live();
+}
+
+// More than four tokens: a workgroup per token.
+template <class E>
+__global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a) {
+  __shared__ float logit[kMoeMaxExperts];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = blockIdx.x;
+  for (int e0 = wave * kRouteAhead; e0 < a.E; e0 += kRouteWaves * kRouteAhead) {
+    float s[kRouteAhead];
+    route_logits<E, kRouteAhead>(a, t, e0, lane, s);
+#pragma unroll
+    for (int j = 0; j < kRouteAhead; ++j)
+      if (lane == 0 && e0 + j < a.E) logit[e0 + j] = s[j];
   }
+  __syncthreads();
+  if (wave == 0) tell_choice(a, t, choose(a, logit, lane), lane);
+}
+
+// Up to four tokens: a wave per logit spreads the router over the chip (one
+// workgroup alone takes 5.8 us for 256 KB); the up kernel's workgroups choose
+// for themselves.
+constexpr int kLogitWaves = 4;
+template <class E>
+__global__ __launch_bounds__(kLogitWaves* kWave) void moe_logits_kernel(MoeArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = blockIdx.x * kLogitWaves + wave, t = blockIdx.y;
+  if (e >= a.E) return;
+  float s[1];
+  route_logits<E, 1>(a, t, e, lane, s);
+  if (lane == 0) a.logits[t * a.E + e] = s[0];
+}
+
+// What a workgroup of the up kernel works out for itself for up to four tokens:
+// the choices, and where that is a matter of one or two logits a wave the logits
+// too (1 token, 2 of 8 experts, d 1024: 15.3 us for a call against 16.6; 4 of 16,
+// d 2048: 11.6 against 12.2; 4 of 32: 12.9 against 12.4; 64 logits on 4 waves:
+// 14.0 against 9.9).
+constexpr int kOwnPerWave = 2;
+constexpr int64_t kOwnBytes = 64 << 10;
+constexpr int kOwnLogits = kOwnPerWave * kMostWaves;
+struct FewChoices {
+  int live[4 * kMoeMaxTopK];
+  float weight[4 * kMoeMaxTopK];
+  float logit[kOwnLogits];
+};
+template <class E>
+__device__ __forceinline__ void few_choose(const MoeArgs& a, FewChoices& c, int lane, int wave, int waves) {
+  if (a.own_logits) {
+    for (int i = wave; i < a.T * a.E; i += waves) {
+      float s[1];
+      route_logits<E, 1>(a, i / a.E, i % a.E, lane, s);
+      if (lane == 0) c.logit[i] = s[0];
+    }
+    __syncthreads();
+  }
+  for (int t = wave; t < a.T; t += waves) {
+    const Choice mine = a.own_logits ? choose(a, c.logit + t * a.E, lane) : choose(a, a.logits + t * a.E, lane);
+    if (lane < a.k) {
+      c.live[t * a.k + lane] = mine.live();
+      c.weight[t * a.k + lane] = mine.weight;
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0) tell_choice(a, t, mine, lane);
+  }
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------- expert lists
-// Most waves of a workgroup of the up and down kernels (chosen at launch).
-constexpr int kMostWaves = 8;
-
 // Where one wave works out its expert and the expert's pairs.  Every wave does
 // so for itself, without a barrier: the pairs come from the L2 once, and
 // what follows are LDS and lane operations of a few hundred cycles.
@@ -198,21 +276,21 @@ __device__ __forceinline__ uint32_t wave_or(uint32_t v) {
   return static_cast<uint32_t>(wave_last(static_cast<int>(v)));
 }
 
-// The pairs of the router's list (a.live), kPairsAhead for each lane at once.
+// Pairs of a list of choices, kPairsAhead for each lane at once.
 template <int kPairsAhead>
 struct LivePairs {
   int id[kPairsAhead];
-  __device__ __forceinline__ void fetch(const MoeArgs& a, int i0, int lane) {
-    const int pairs = a.T * a.k;
+  __device__ __forceinline__ void fetch(const int* live, int pairs, int i0, int lane) {
 #pragma unroll
     for (int u = 0; u < kPairsAhead; ++u) {
       const int i = i0 + u * 64 + lane;
-      id[u] = a.live[i < pairs ? i : pairs - 1];  // all loads at once: no branch
+      id[u] = live[i < pairs ? i : pairs - 1];  // all loads at once: no branch
     }
 #pragma unroll
     for (int u = 0; u < kPairsAhead; ++u)
       if (i0 + u * 64 + lane >= pairs) id[u] = -1;
   }
+  __device__ __forceinline__ void fetch(const MoeArgs& a, int i0, int lane) { fetch(a.live, a.T * a.k, i0, lane); }
 };
 
 // The `which`-th chosen expert (ascending), or -1 if there are not that many.
@@ -283,6 +361,12 @@ __device__ __forceinline__ int64_t token_of(int pair, const MoeArgs& a) {
   return static_cast<int>((static_cast<float>(pair) + 0.5f) * a.inv_k);
 }
 
+// Waves a SIMD that the registers leave room for.  fp32 data with 16-bit weights
+// needs more than 128 (64 tokens, 16 experts of 1500 x 700: 62 us against 75 with
+// spills); 4-bit weights gain about as much as they lose by it.
+template <class E, int BITS>
+constexpr int least_waves() { return E::kBytes == 4 && BITS == 16 ? 3 : 4; }
+
 // LDS of one wave: its list, and its token pieces or, after them, its sums.
 template <class Prod>
 constexpr int wave_lds() { return Prod::kAll * 256 > Prod::X::kLdsBytes ? Prod::kAll * 256 : Prod::X::kLdsBytes; }
@@ -309,7 +393,7 @@ __device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, int ti, T
 // from tile ti on.  lds: wave_lds per wave.
 template <class E, int BITS, int G, int TQ, int NT, bool kFew = false>
 __device__ __forceinline__ void up_pairs(const MoeArgs& a, const Tiles<2 * NT>& tile, int ti, const int* pair, int n,
-                                         char* lds, int lane, int wave, int waves) {
+                                         const float* weights, char* lds, int lane, int wave, int waves) {
   using Elem = typename E::storage;
   using Prod = UpProduct<E, BITS, G, TQ, NT, !kFew>;
   constexpr int kOne = Prod::kRegs;  // registers of one tile
@@ -333,7 +417,7 @@ __device__ __forceinline__ void up_pairs(const MoeArgs& a, const Tiles<2 * NT>& 
     const float u = joined<Prod::kAll>(red, waves, o + (r + 1) * kOne * 64);
     // a NaN gate stays NaN under both activations
     const float act = a.act == 0 ? (g < 0.f ? 0.f : g) : g / (1.f + expf(-g));
-    float h = a.weights[pair[i]] * act * u;
+    float h = weights[pair[i]] * act * u;
     if (ti + r >= a.tiles_f) h = 0.f;  // neurons that fill the last block of 128
     // the down projection reads h as bf16 values whose sum is h: two of them
     // keep 16 bits, so that only the output's own rounding is seen in bf16;
@@ -359,7 +443,7 @@ __device__ __forceinline__ void hand_on(const MoeArgs& a, int expert, int n, con
 // nearly every expert has a token: row y of the grid is then expert y, which
 // needs no search.
 template <class E, int BITS, int G, bool kFew, int NT>
-__global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kMostWaves* kWave, (least_waves<E, BITS>())) void moe_up_kernel(MoeArgs a) {
   __shared__ WaveList lists[kMostWaves];
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -369,13 +453,15 @@ __global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_up_kernel(MoeArgs a)
   LivePairs<(kFew ? 2 : 8)> live;
   Tiles<2 * NT> tile;
   if constexpr (kFew) {
-    live.fetch(a, 0, lane);
+    __shared__ FewChoices choices;
+    few_choose<E>(a, choices, lane, wave, waves);
+    live.fetch(choices.live, a.T * a.k, 0, lane);
     const int expert = find_expert(a, live, blockIdx.y, list, lane);
     const int n = expert < 0 ? 0 : find_pairs(a, live, expert, list, lane);
     hand_on(a, expert, n, list, lane, wave);
     if (n == 0) return;  // the whole workgroup
     up_tiles<BITS, G, NT>(a, expert, ti, tile);
-    up_pairs<E, BITS, G, 1, NT, true>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
+    up_pairs<E, BITS, G, 1, NT, true>(a, tile, ti, list.pair, n, choices.weight, lds, lane, wave, waves);
   } else {
     live.fetch(a, 0, lane);
     const int expert = a.by_expert ? static_cast<int>(blockIdx.y) : find_expert(a, live, blockIdx.y, list, lane);
@@ -384,13 +470,14 @@ __global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_up_kernel(MoeArgs a)
     if (n == 0) return;
     up_tiles<BITS, G, NT>(a, expert, ti, tile);
     if (n <= 4) {
-      up_pairs<E, BITS, G, 1, NT>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
+      up_pairs<E, BITS, G, 1, NT>(a, tile, ti, list.pair, n, a.weights, lds, lane, wave, waves);
     } else if (n <= 8) {
-      up_pairs<E, BITS, G, 2, NT>(a, tile, ti, list.pair, n, lds, lane, wave, waves);
+      up_pairs<E, BITS, G, 2, NT>(a, tile, ti, list.pair, n, a.weights, lds, lane, wave, waves);
     } else {
       for (int i = 0; i < n; i += 16) {
         if (i > 0) __syncthreads();
-        up_pairs<E, BITS, G, 4, NT>(a, tile, ti, list.pair + i, n - i < 16 ? n - i : 16, lds, lane, wave, waves);
+        up_pairs<E, BITS, G, 4, NT>(a, tile, ti, list.pair + i, n - i < 16 ? n - i : 16, a.weights, lds, lane, wave,
+                                    waves);
       }
     }
   }
@@ -429,7 +516,7 @@ __device__ __forceinline__ void down_pairs(const MoeArgs& a, const Tiles<NT>& ti
 }
 
 template <class E, int BITS, int G, int NT>
-__global__ __launch_bounds__(kMostWaves* kWave, 4) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kMostWaves* kWave, (least_waves<E, BITS>())) void moe_down_kernel(MoeArgs a) {
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
@@ -533,10 +620,12 @@ __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs 
 
 template <class E>
 hipError_t go_route(const MoeArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.T)), block(kRouteWaves * kWave);
-  if (a.E <= 64) moe_route_kernel<E, 1><<<grid, block, 0, s>>>(a);
-  else if (a.E <= 256) moe_route_kernel<E, 4><<<grid, block, 0, s>>>(a);
-  else moe_route_kernel<E, kMoeMaxExperts / 64><<<grid, block, 0, s>>>(a);
+  if (a.T > 4) {
+    moe_route_kernel<E><<<static_cast<unsigned>(a.T), kRouteWaves * kWave, 0, s>>>(a);
+  } else if (!a.own_logits) {
+    const dim3 grid(static_cast<unsigned>((a.E + kLogitWaves - 1) / kLogitWaves), static_cast<unsigned>(a.T));
+    moe_logits_kernel<E><<<grid, kLogitWaves * kWave, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
@@ -551,11 +640,14 @@ int waves_for(int64_t groups, int blocks) {
 }
 
 template <class E, int BITS, int G, bool kFew, int NT>
-hipError_t go_up(const MoeArgs& a, hipStream_t s) {
+hipError_t go_choices_up(MoeArgs a, hipStream_t s) {
   // the tiles that fill the last block of neurons are written too
   const dim3 grid(static_cast<unsigned>(a.blocks_f * (kBlockK / kTileRows) / NT), static_cast<unsigned>(a.most_chosen));
   constexpr int kLds = wave_lds<UpProduct<E, BITS, G, kFew ? 1 : 4, NT, !kFew>>();
   const int w = waves_for(static_cast<int64_t>(grid.x) * grid.y, a.blocks_d);
+  a.own_logits = kFew && a.T * a.E <= kOwnPerWave * w && static_cast<int64_t>(a.T) * a.E * a.d * E::kBytes <= kOwnBytes;
+  const hipError_t e = go_route<E>(a, s);
+  if (e != hipSuccess) return e;
   moe_up_kernel<E, BITS, G, kFew, NT><<<grid, w * kWave, w * kLds, s>>>(a);
   return hipGetLastError();
 }
@@ -587,8 +679,8 @@ constexpr int64_t kFewBytes = int64_t(24) << 20;
 
 template <class E, int BITS, int G>
 hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
-  const hipError_t e = a.T <= 4 ? go_up<E, BITS, G, true, 1>(a, s)
-                                : go_up<E, BITS, G, false, BITS == 16 || E::kBytes == 4 ? 1 : 2>(a, s);
+  const hipError_t e = a.T <= 4 ? go_choices_up<E, BITS, G, true, 1>(a, s)
+                                : go_choices_up<E, BITS, G, false, BITS == 16 || E::kBytes == 4 ? 1 : 2>(a, s);
   if (e != hipSuccess) return e;
   if (a.T <= kFewTokens &&
       static_cast<int64_t>(a.T) * a.k * a.tiles_d * a.blocks_f * Block<BITS>::kBytes <= kFewBytes) {
@@ -600,8 +692,6 @@ hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
 
 template <class E>
 hipError_t by_weights(const MoeArgs& a, hipStream_t s) {
-  const hipError_t e = go_route<E>(a, s);
-  if (e != hipSuccess) return e;
   if (a.bits == 16) return by_tokens<E, 16, 1>(a, s);
   if (a.group == 32) return by_tokens<E, 4, 4>(a, s);
   if (a.group == 64) return by_tokens<E, 4, 2>(a, s);

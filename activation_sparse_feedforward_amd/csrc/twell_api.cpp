@@ -197,7 +197,7 @@ twell_status check_moe(const twell_moe_desc* d) {
 // tokens' (token, choice) pairs, the pairs' outputs, the choices that count, and
 // the chosen experts with their pairs.
 struct MoeWs {
-  size_t h, z, live, chosen, chosen_pairs, total;
+  size_t h, z, logits, live, chosen, chosen_pairs, total;
   int64_t h_plane, h_row;
   int32_t block_tokens;
 };
@@ -210,6 +210,8 @@ MoeWs moe_ws(const twell_moe_desc* d) {
   size_t o = 0;
   w.h = o;        o += align256(static_cast<size_t>(w.h_plane) * 2 * (d->dtype == TWELL_BF16 ? 2 : 3));
   w.z = o;        o += align256(static_cast<size_t>(pairs) * static_cast<size_t>(d->d_model) * 4);
+  const size_t few = static_cast<size_t>(w.block_tokens < 4 ? w.block_tokens : 4);
+  w.logits = o;   o += align256(few * static_cast<size_t>(d->experts) * 4);
   w.live = o;     o += align256(static_cast<size_t>(pairs) * 4);
   const size_t chosen = static_cast<size_t>(pairs < d->experts ? pairs : d->experts);
   w.chosen = o;       o += align256(chosen * sizeof(twell::MoeChosen));
@@ -685,6 +687,7 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
   a.h_plane = w.h_plane;
   a.h_row = w.h_row;
   a.z = reinterpret_cast<float*>(wsb + w.z);
+  a.logits = reinterpret_cast<float*>(wsb + w.logits);
   a.live = reinterpret_cast<int32_t*>(wsb + w.live);
   a.chosen = reinterpret_cast<twell::MoeChosen*>(wsb + w.chosen);
   a.chosen_pairs = reinterpret_cast<int32_t*>(wsb + w.chosen_pairs);
