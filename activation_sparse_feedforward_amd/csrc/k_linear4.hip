@@ -1,9 +1,18 @@
 // y = x W^T for a few tokens with 4-bit weights (layout and arithmetic:
 // few_token.hpp).
 //
-// One workgroup per NR tiles of 16 weight rows; its waves split the inputs
-// and their sums are joined through LDS in wave order.  Bound by reading the
-// codes: 0.5 byte per weight against one shift and one and-or per two weights.
+//   y[t,n] = sum_g s[n,g] sum_{k in g} x[t,k] q[n,k]
+//
+// One workgroup per NR tiles of 16 weight rows and 4 TQ tokens; its waves split
+// the inputs and their sums are joined through LDS in wave order, so that one
+// launch does it all and a short product still has every CU reading.  Up to 16
+// tokens it is bound by reading the codes (bf16 data; 0.5 byte and one rotation
+// and one and-or for two weights): 11008 x 4096 takes 6.7 us for one token (3.5
+// TB/s) and 7.3 for 16, 4096 x 1024 2.6 us, of which the launch itself is 1.6.
+// Beyond that by getting the tokens to the matrix core, through the L1 and LDS
+// once per NR tiles: 128 tokens of 2048 x 8192 12 us (0.36 PFLOP/s), of 16384 x
+// 2048 21 us (0.41).  fp32 data costs three matrix instructions and 2.5 times the
+// unpacking: 7 tokens of 5001 x 1999 6.1 us.
 #include "few_token.hpp"
 #include "internal.hpp"
 
@@ -79,27 +88,43 @@ hipError_t go(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The fewest tiles per workgroup that leave no more than one workgroup for a
-// CU, so that all run at once.
-template <class E, int G, int TQ, int NR, int kMost>
+// Tiles per workgroup, NR in [kLeast, kMost]: the workgroups go round the CUs
+// one after another, and one costs NR tiles and its tokens, about a tile's time.
+// (100 tokens of 8192 x 8192: 28.7 us with four tiles in one round against 44.6
+// with three in two; one token of 20480 x 2048: 7.2 with three in two rounds
+// against 8.0 with four in two.)
+template <class E, int G, int TQ, int kLeast, int kMost>
 hipError_t by_rows(const LinearArgs& a, int cus, hipStream_t s) {
   const int64_t groups = (a.T + 4 * TQ - 1) / (4 * TQ);
-  if constexpr (NR < kMost) {
-    if ((a.tiles + NR - 1) / NR * groups > cus) return by_rows<E, G, TQ, NR + 1, kMost>(a, cus, s);
+  int best = kMost;
+  int64_t least = INT64_MAX;
+  for (int nr = kMost; nr >= kLeast; --nr) {
+    const int64_t cost = ((a.tiles + nr - 1) / nr * groups + cus - 1) / cus * (nr + 1);
+    if (cost < least) {
+      least = cost;
+      best = nr;
+    }
   }
-  return go<E, G, TQ, NR>(a, s);
+  if constexpr (kLeast <= 1) if (best == 1) return go<E, G, TQ, 1>(a, s);
+  if constexpr (kLeast <= 2 && kMost >= 2) if (best == 2) return go<E, G, TQ, 2>(a, s);
+  if constexpr (kLeast <= 3 && kMost >= 3) if (best == 3) return go<E, G, TQ, 3>(a, s);
+  return go<E, G, TQ, kMost>(a, s);
 }
 
 template <class E, int G>
 hipError_t by_tokens(const LinearArgs& a, hipStream_t s) {
   const int cus = lockstep_resident() > 0 ? lockstep_resident() : 256;
-  if (a.T <= 4) return by_rows<E, G, 1, 1, 4>(a, cus, s);
-  if (a.T <= 8) return by_rows<E, G, 2, 1, 4>(a, cus, s);
-  if (a.T <= 16) return by_rows<E, G, 4, 1, 4>(a, cus, s);
+  // As many tokens as there are at once (their weights are unpacked once), but
+  // fewer where that leaves CUs without work: 50 tokens of 700 x 6000 take 7.8 us
+  // by fours against 12.6 by 32, 16 of 2048 x 8192 5.2 by eights against 6.2.
+  auto fills = [&](int tokens) { return static_cast<int64_t>(a.tiles) * ((a.T + tokens - 1) / tokens) <= cus; };
+  if (a.T <= 4 || fills(4)) return by_rows<E, G, 1, 1, 4>(a, cus, s);
+  if (a.T <= 8 || fills(8)) return by_rows<E, G, 2, 1, 4>(a, cus, s);
+  if (a.T <= 16 || fills(16)) return by_rows<E, G, 4, 1, 4>(a, cus, s);
   if constexpr (E::kBytes == 2) {
     // 64 tokens a workgroup save unpacking the codes twice, once that still
     // leaves a workgroup for every CU
-    if (a.T > 32 && (a.tiles + 2) / 3 * ((a.T + 63) / 64) >= cus) return go<E, G, 16, 3>(a, s);
+    if (a.T > 32 && (a.tiles + 2) / 3 * ((a.T + 63) / 64) >= cus) return by_rows<E, G, 16, 3, 4>(a, cus, s);
     return by_rows<E, G, 8, 1, 4>(a, cus, s);
   }
   return by_rows<E, G, 8, 1, 2>(a, cus, s);

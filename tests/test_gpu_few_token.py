@@ -149,6 +149,21 @@ def test_linear(T_, N, K, group, dtype):
     _close(y, ref, dtype)
 
 
+@pytest.mark.parametrize("T_", [3, 7, 13, 29, 61, 100])
+@pytest.mark.parametrize("N", [4090, 4100, 8200, 12288, 12300])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_linear_many_rows(T_, N, group, dtype):
+    """Rows for every CU: the most tokens a workgroup takes, and one to four tiles of rows each."""
+    say(f"[gpu case] linear many rows T={T_} N={N} group={group} {dtype}")
+    wd, pl, x, ref = _linear_case(T_, N, 203, group, dtype)
+    y = guarded((T_, N), DT[dtype])
+    T.twell_linear_fwd(wd, pl, x, y)
+    torch.cuda.synchronize()
+    check_guards(*pl, y)
+    _close(y, ref, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("T_", [1, 3, 20])
 def test_linear_strided_rows_at_odd_addresses(T_, dtype):
