@@ -116,7 +116,7 @@ hipError_t by_tokens(const LinearArgs& a, hipStream_t s) {
   const int cus = lockstep_resident() > 0 ? lockstep_resident() : 256;
   // As many tokens as there are at once (their weights are unpacked once), but
   // fewer where that leaves CUs without work: 50 tokens of 700 x 6000 take 7.8 us
-  // by fours against 12.6 by 32, 16 of 2048 x 8192 5.2 by eights against 6.2.
+  // by sixteens against 12.6 by 32, 16 of 2048 x 8192 5.2 by eights against 6.2.
   auto fills = [&](int tokens) { return static_cast<int64_t>(a.tiles) * ((a.T + tokens - 1) / tokens) <= cus; };
   if (a.T <= 4 || fills(4)) return by_rows<E, G, 1, 1, 4>(a, cus, s);
   if (a.T <= 8 || fills(8)) return by_rows<E, G, 2, 1, 4>(a, cus, s);

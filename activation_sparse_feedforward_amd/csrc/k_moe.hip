@@ -677,17 +677,36 @@ hipError_t go_down(const MoeArgs& a, hipStream_t s) {
 constexpr int kFewTokens = 2;
 constexpr int64_t kFewBytes = int64_t(24) << 20;
 
+// Whether NT of `tiles` tiles a workgroup leave work for most CUs: more tiles
+// share the tokens' way through LDS, fewer give more CUs something to read (64
+// tokens, 2 of 4 experts of 512 x 512 in 4 bits: 18.7 us with one and one tile
+// against 25.9 with two and four; 12 tokens, 6 of 40 experts of 700 x 300: 23.1
+// against 19.3).
+bool fills(const MoeArgs& a, int tiles, int NT) {
+  const int cus = lockstep_resident() > 0 ? lockstep_resident() : 256;
+  return static_cast<int64_t>((tiles + NT - 1) / NT) * a.most_chosen * 4 >= int64_t(3) * cus;
+}
+
 template <class E, int BITS, int G>
 hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
-  const hipError_t e = a.T <= 4 ? go_choices_up<E, BITS, G, true, 1>(a, s)
-                                : go_choices_up<E, BITS, G, false, BITS == 16 || E::kBytes == 4 ? 1 : 2>(a, s);
+  constexpr bool kSlim = BITS == 4 && E::kBytes == 2;  // room for twice the tiles in registers
+  hipError_t e;
+  if (a.T <= 4) {
+    e = go_choices_up<E, BITS, G, true, 1>(a, s);
+  } else if (kSlim && fills(a, a.blocks_f * (kBlockK / kTileRows), 2)) {
+    e = go_choices_up<E, BITS, G, false, kSlim ? 2 : 1>(a, s);
+  } else {
+    e = go_choices_up<E, BITS, G, false, 1>(a, s);
+  }
   if (e != hipSuccess) return e;
   if (a.T <= kFewTokens &&
       static_cast<int64_t>(a.T) * a.k * a.tiles_d * a.blocks_f * Block<BITS>::kBytes <= kFewBytes) {
     moe_down_few_kernel<E, BITS, G><<<a.tiles_d, kFewWaves * kWave, 0, s>>>(a);
     return hipGetLastError();
   }
-  return go_down<E, BITS, G, BITS == 16 || E::kBytes == 4 ? 2 : 4>(a, s);
+  if (kSlim && fills(a, a.tiles_d, 4)) return go_down<E, BITS, G, kSlim ? 4 : 2>(a, s);
+  if (fills(a, a.tiles_d, 2)) return go_down<E, BITS, G, 2>(a, s);
+  return go_down<E, BITS, G, 1>(a, s);
 }
 
 template <class E>

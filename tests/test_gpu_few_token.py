@@ -295,6 +295,33 @@ def test_moe_larger_widths(T_, bits, group):
     _moe_check(md, *_moe_case(md))
 
 
+@pytest.mark.parametrize("T_", [5, 20, 64])
+@pytest.mark.parametrize("bits,group", [(16, 0), (4, 32), (4, 64), (4, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_moe_work_for_every_cu(T_, bits, group, dtype):
+    """Many experts: the most tiles a workgroup takes, some of them beyond the last."""
+    md = T.MoeDesc(T_, 300, 200, 40, 8, dtype, bits, group, "silu", True)
+    say(f"[gpu case] moe many T={T_} bits={bits} group={group} {dtype}")
+    _moe_check(md, *_moe_case(md))
+
+
+@pytest.mark.parametrize("T_,E,k,d", [(1, 16, 4, 600), (2, 5, 2, 601), (4, 4, 4, 520), (3, 1024, 32, 40), (4, 256, 3, 130),
+                                      (1, 17, 3, 1030)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_moe_router_of_a_few_tokens(T_, E, k, d, dtype):
+    """Small routers and large ones, with experts taken out by the bias and a token that is not finite."""
+    say(f"[gpu case] moe router T={T_} E={E} k={k} d={d} {dtype}")
+    md = T.MoeDesc(T_, d, 70, E, k, dtype, 4, 64, "relu", False)
+    x, router, w, mats = _moe_case(md)
+    bias = _randn(_gen(E), E)
+    bias[::3] = float("-inf")
+    _moe_check(md, x, router, w, mats, bias)
+    x[T_ - 1, d - 1] = float("nan")
+    out = _moe_check(md, x, router, w, mats, bias)
+    assert torch.isnan(out.y[T_ - 1]).all()
+    assert not torch.isnan(out.y[:T_ - 1]).any()
+
+
 @pytest.mark.parametrize("T_", [2, 40])
 def test_moe_masked_experts_ties_and_empty_rows(T_):
     md = T.MoeDesc(T_, 96, 40, 12, 4, "fp32", 4, 32, "silu", True)
