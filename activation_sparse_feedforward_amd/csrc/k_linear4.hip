@@ -22,7 +22,7 @@ namespace {
 // Waves of a workgroup, as registers and LDS (the waves' sums) allow.
 template <class E, int TQ, int NR>
 constexpr int max_waves() {
-  return E::kBytes == 2 ? (NR * token_tiles<TQ>() <= 4 ? 16 : 8) : TQ <= 2 || (TQ == 4 && NR <= 3) ? 16 : 8;
+  return E::kBytes == 2 ? (TQ < 8 && NR * token_tiles<TQ>() <= 4 ? 16 : 8) : TQ <= 2 || (TQ == 4 && NR <= 3) ? 16 : 8;
 }
 
 template <class E, int G, int TQ, int NR>
