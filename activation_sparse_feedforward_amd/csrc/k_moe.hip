@@ -4,12 +4,13 @@
 //   y[t]   = sum_i w_i  W_down_e ( act(W_gate_e x) * (W_up_e x) ),   e = ids[t,i]
 //
 // (1) moe_route_kernel: one workgroup per token, logits in fp32, selection by
-// one wave (up to four tokens: moe_logits_kernel, or nothing).  (2) moe_up_kernel: one workgroup per (chosen expert, NT tiles of
-// 16 neurons); it gathers the expert's tokens, computes gate and up together
-// and writes h = w * act(g) * u.  (3) moe_down_kernel: one workgroup per
+// one wave (up to four tokens: moe_logits_kernel, or nothing).  (2)
+// moe_up_kernel: one workgroup per (chosen expert, NT tiles of 16 neurons); it
+// gathers the expert's tokens, computes gate and up together and writes h =
+// w * act(g) * u.  (3) moe_down_kernel: one workgroup per
 // (chosen expert, NT tiles of 16 outputs), writes every pair's part, and
-// (4) moe_join_kernel adds them up in the order of the choices; one or two
-// tokens with little to read take moe_down_few_kernel instead of both.
+// (4) moe_join_kernel adds them up in the order of the choices; few tokens with
+// little to read take moe_down_few_kernel instead of both.
 // Nothing depends on timing.  Only chosen experts' weights are read, each once
 // per 16 of its tokens.  Bound by reading them.
 #include "few_token.hpp"
@@ -571,25 +572,26 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
   else static_cast<float*>(a.y)[at] = v;
 }
 
-// One or two tokens and little to read: one workgroup per 16 outputs takes all
-// pairs, its waves splitting (pair, block) among them, and writes y at once.
-// Lane group g of a result register belongs to token g, so the sums over a
-// token's choices form in one register.
+// Few tokens and little to read: one workgroup per 16 outputs takes all pairs,
+// its waves splitting (pair, block) among them, and writes y at once.  A pair's
+// h is every row of the matrix operand, so that all lane groups hold its result;
+// group t % 4 adds it to the sum of token t, so a token's choices come together
+// in one register.  TQ: quads of tokens.
 constexpr int kFewWaves = 16;
 
-template <class E, int BITS, int G>
+template <class E, int BITS, int G, int TQ>
 __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs a) {
   constexpr int P = E::kBytes == 2 ? 2 : 3;
   using Prod = Product<BITS, G, 1, 1, SourcePlanes<P>>;
   static_assert(Prod::kAll == 1);
   __shared__ __align__(16) char lds[kFewWaves * Prod::X::kLdsBytes];
-  __shared__ float red[kFewWaves * 64];
+  __shared__ float red[kFewWaves * TQ * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ti = blockIdx.x;
   const int total = a.T * a.k * a.blocks_f;
   int b = total * wave / kFewWaves;
   const int end = total * (wave + 1) / kFewWaves;
-  float sum = 0.f;
+  float sum[TQ] = {};
   while (b < end) {
     const int pair = b / a.blocks_f, b0 = b % a.blocks_f;
     const int b1 = b0 + (end - b) < a.blocks_f ? b0 + (end - b) : a.blocks_f;
@@ -604,14 +606,18 @@ __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs 
     Prod p;
     p.clear();
     p.template run<4>(x, tile, b0, b1, b1, lane);
-    if (result_token(0, lane) == pair / a.k) sum += p.acc[0][0][0];
+    const int t = pair / a.k;
+#pragma unroll
+    for (int q = 0; q < TQ; ++q)
+      if (result_token(q, lane) == t) sum[q] += p.acc[0][0][0];
   }
-  red[wave * 64 + lane] = sum;
+#pragma unroll
+  for (int q = 0; q < TQ; ++q) red[(wave * TQ + q) * 64 + lane] = sum[q];
   __syncthreads();
-  if (threadIdx.x >= 64) return;
-  const int t = result_token(0, lane), n = ti * kTileRows + (lane & 15);
+  if (wave >= TQ) return;
+  const int t = result_token(wave, lane), n = ti * kTileRows + (lane & 15);
   if (t < a.T && n < a.d) {
-    const float v = joined<1>(red, kFewWaves, lane);
+    const float v = joined<TQ>(red, kFewWaves, threadIdx.x);
     const int64_t at = static_cast<int64_t>(t) * a.ldy + n;
     if constexpr (E::kBytes == 2) static_cast<uint16_t*>(a.y)[at] = bf16_of(v);
     else static_cast<float*>(a.y)[at] = v;
@@ -670,12 +676,20 @@ hipError_t go_down(const MoeArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tokens, and bytes of the down projections of their pairs, up to which the one
-// kernel for few tokens is the faster (a whole call, both ways: 1 token, 2 of 8
-// bf16 experts, 16 MB 16.9 against 21.0 us; 1 token, 8 of 64, 32 MB 31.8 against
-// 28.7; 4 tokens, 8 of 64 in 4 bits, 32 MB 35.6 against 31.6).
-constexpr int kFewTokens = 2;
-constexpr int64_t kFewBytes = int64_t(24) << 20;
+// Up to so many (pair, block)s for a workgroup, and bytes in all, the one kernel
+// for few tokens is the faster: it reads an expert's weights once per pair, on as
+// many CUs as there are tiles of outputs, but saves a launch and the way of the
+// parts through memory.  Whole calls, this one against the other: 1 token, 2 of 8
+// bf16 experts of 1024 x 4096 (64 blocks, 16 MB) 15.4 against 19.5 us; 8 tokens, 1
+// of 4 in 4 bits, 512 x 512 (32) 10.7 against 11.7; 16 tokens, 1 of 8, 1024 x 512
+// (64) 13.1 against 13.1, in fp32 18.0 against 16.4; 5 tokens, 3 of 7, 1001 x 707
+// (90) 15.3 against 13.8; 1 token, 8 of 64 bf16 experts of 2048 x 1024 (64, 32 MB)
+// 31.8 against 28.7.
+template <class E>
+bool one_down(const MoeArgs& a, int block_bytes) {
+  const int64_t blocks = static_cast<int64_t>(a.T) * a.k * a.blocks_f;
+  return a.T <= 16 && blocks <= (E::kBytes == 2 ? 64 : 32) && blocks * a.tiles_d * block_bytes <= int64_t(24) << 20;
+}
 
 // Whether NT of `tiles` tiles a workgroup leave work for most CUs: more tiles
 // share the tokens' way through LDS, fewer give more CUs something to read (64
@@ -699,9 +713,9 @@ hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
     e = go_choices_up<E, BITS, G, false, 1>(a, s);
   }
   if (e != hipSuccess) return e;
-  if (a.T <= kFewTokens &&
-      static_cast<int64_t>(a.T) * a.k * a.tiles_d * a.blocks_f * Block<BITS>::kBytes <= kFewBytes) {
-    moe_down_few_kernel<E, BITS, G><<<a.tiles_d, kFewWaves * kWave, 0, s>>>(a);
+  if (one_down<E>(a, Block<BITS>::kBytes)) {
+    if (a.T <= 4) moe_down_few_kernel<E, BITS, G, 1><<<a.tiles_d, kFewWaves * kWave, 0, s>>>(a);
+    else moe_down_few_kernel<E, BITS, G, 4><<<a.tiles_d, kFewWaves * kWave, 0, s>>>(a);
     return hipGetLastError();
   }
   if (kSlim && fills(a, a.tiles_d, 4)) return go_down<E, BITS, G, kSlim ? 4 : 2>(a, s);
