@@ -10,9 +10,9 @@
 // and one and-or for two weights): 11008 x 4096 takes 6.7 us for one token (3.5
 // TB/s) and 7.3 for 16, 4096 x 1024 2.6 us, of which the launch itself is 1.6.
 // Beyond that by getting the tokens to the matrix core, through the L1 and LDS
-// once per NR tiles: 128 tokens of 2048 x 8192 12 us (0.36 PFLOP/s), of 16384 x
+// once per NR tiles: 128 tokens of 2048 x 8192 11.5 us (0.37 PFLOP/s), of 16384 x
 // 2048 21 us (0.41).  fp32 data costs three matrix instructions and 2.5 times the
-// unpacking: 7 tokens of 5001 x 1999 6.1 us.
+// unpacking: 7 tokens of 5001 x 1999 5.7 us.
 #include "few_token.hpp"
 #include "internal.hpp"
 
