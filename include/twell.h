@@ -320,10 +320,12 @@ twell_status twell_weights_unpack(const twell_wdesc* d, twell_wplanes in, void* 
 /* y[t, n] = sum_k x[t, k] q[n, k] s[n, k / group]: the product of T tokens with
  * one matrix of 4-bit weights (experts = 1, bits = 4), fp32 sums.
  *   x [T x cols], y [T x rows] in dtype, rows ldx / ldy apart.
- * Made for few tokens: the weights are read once per 32 tokens.  T = 0 is a
- * no-op.  Codes are multiplied as q + 24 and the 24 taken off again inside the
- * sum, so an infinite input gives NaN, and inputs beyond about 1e36 may
- * overflow.  Deterministic. */
+ * Made for few tokens: the weights are read once per 4 to 64 of them, by how
+ * many there are and how many workgroups that makes.  T = 0 is a no-op.
+ * bf16 data: codes are multiplied as q + 24 and the 24 taken off again inside
+ * the sum, so inputs beyond about 1e36 may overflow; fp32 data is cut into three
+ * bf16 parts and multiplied with q.  Either way an infinite or NaN input makes
+ * its own token's outputs NaN, and no other token's.  Deterministic. */
 twell_status twell_linear_fwd(const twell_wdesc* d, twell_wplanes w, int64_t T, int32_t dtype, const void* x,
                               int64_t ldx, void* y, int64_t ldy, void* stream);
 
@@ -364,9 +366,10 @@ twell_status twell_moe_sizes(const twell_moe_desc* d, size_t* ws);
  * row whose logits are all -inf has weights 0 and y = 0.  A NaN logit makes its
  * token's weights and y NaN, no other token's.
  * Hidden values are kept to 16 bits of mantissa (bf16 data) or 24 (fp32); sums
- * are fp32.  Deterministic.  ws: twell_moe_sizes() bytes; nothing in it needs
- * to start at zero.  Made for few tokens: experts' weights are read once per
- * 64 tokens.  T = 0 is a no-op. */
+ * are fp32.  With infinite inputs, and with hidden values that overflow, the
+ * token's y is NaN.  Deterministic.  ws: twell_moe_sizes() bytes; nothing in it
+ * needs to start at zero.  Made for few tokens: 64 of them at a time, an expert's
+ * weights once per 16 of its tokens.  T = 0 is a no-op. */
 twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w_router, const float* router_bias,
                            twell_wplanes gate, twell_wplanes up, twell_wplanes down, void* y, int32_t* ids,
                            float* weights, void* ws, size_t ws_bytes, void* stream);
