@@ -84,8 +84,7 @@ hipError_t go(const LinearArgs& a, hipStream_t s) {
   int waves = kWaves;
   while (waves > 1 && waves > a.blocks) waves >>= 1;
   const dim3 grid((a.tiles + NR - 1) / NR, static_cast<unsigned>((a.T + 4 * TQ - 1) / (4 * TQ)));
-  linear4_kernel<E, G, TQ, NR><<<grid, waves * kWave, waves * kPerWave, s>>>(a);
-  return hipGetLastError();
+  return launch(linear4_kernel<E, G, TQ, NR>, grid, waves * kWave, waves * kPerWave, s, a);
 }
 
 // Tiles per workgroup, NR in [kLeast, kMost]: the workgroups go round the CUs
@@ -113,7 +112,7 @@ hipError_t by_rows(const LinearArgs& a, int cus, hipStream_t s) {
 
 template <class E, int G>
 hipError_t by_tokens(const LinearArgs& a, hipStream_t s) {
-  const int cus = lockstep_resident() > 0 ? lockstep_resident() : 256;
+  const int resident = lockstep_resident(), cus = resident > 0 ? resident : 256;
   // As many tokens as there are at once (their weights are unpacked once), but
   // fewer where that leaves CUs without work: 50 tokens of 700 x 6000 take 7.8 us
   // by sixteens against 12.6 by 32, 16 of 2048 x 8192 5.2 by eights against 6.2.

@@ -636,13 +636,10 @@ __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs 
 
 template <class E>
 hipError_t go_route(const MoeArgs& a, hipStream_t s) {
-  if (a.T > 4) {
-    moe_route_kernel<E><<<static_cast<unsigned>(a.T), kRouteWaves * kWave, 0, s>>>(a);
-  } else if (!a.own_logits) {
-    const dim3 grid(static_cast<unsigned>((a.E + kLogitWaves - 1) / kLogitWaves), static_cast<unsigned>(a.T));
-    moe_logits_kernel<E><<<grid, kLogitWaves * kWave, 0, s>>>(a);
-  }
-  return hipGetLastError();
+  if (a.T > 4) return launch(moe_route_kernel<E>, dim3(static_cast<unsigned>(a.T)), kRouteWaves * kWave, 0, s, a);
+  if (a.own_logits) return hipSuccess;
+  const dim3 grid(static_cast<unsigned>((a.E + kLogitWaves - 1) / kLogitWaves), static_cast<unsigned>(a.T));
+  return launch(moe_logits_kernel<E>, grid, kLogitWaves * kWave, 0, s, a);
 }
 
 // Waves per workgroup: as few as still make kFillWaves waves.  A workgroup's
@@ -664,8 +661,7 @@ hipError_t go_choices_up(MoeArgs a, hipStream_t s) {
   a.own_logits = kFew && a.T * a.E <= kOwnPerWave * w && static_cast<int64_t>(a.T) * a.E * a.d * E::kBytes <= kOwnBytes;
   const hipError_t e = go_route<E>(a, s);
   if (e != hipSuccess) return e;
-  moe_up_kernel<E, BITS, G, kFew, NT><<<grid, w * kWave, w * kLds, s>>>(a);
-  return hipGetLastError();
+  return launch(moe_up_kernel<E, BITS, G, kFew, NT>, grid, w * kWave, w * kLds, s, a);
 }
 
 template <class E, int BITS, int G, int NT>
@@ -678,12 +674,10 @@ hipError_t go_down(const MoeArgs& a, hipStream_t s) {
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, kMostWaves * kLds);
     if (attr != hipSuccess) return attr;
   }
-  moe_down_kernel<E, BITS, G, NT><<<grid, w * kWave, w * kLds, s>>>(a);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = launch(moe_down_kernel<E, BITS, G, NT>, grid, w * kWave, w * kLds, s, a);
   if (e != hipSuccess) return e;
   const dim3 join(static_cast<unsigned>((a.d + 255) / 256), static_cast<unsigned>(a.T));
-  moe_join_kernel<E><<<join, 256, 0, s>>>(a);
-  return hipGetLastError();
+  return launch(moe_join_kernel<E>, join, 256, 0, s, a);
 }
 
 // Up to so many (pair, block)s for a workgroup, and bytes in all, the one kernel
@@ -707,7 +701,7 @@ bool one_down(const MoeArgs& a, int block_bytes) {
 // against 25.9 with two and four; 12 tokens, 6 of 40 experts of 700 x 300: 23.1
 // against 19.3).
 bool fills(const MoeArgs& a, int tiles, int NT) {
-  const int cus = lockstep_resident() > 0 ? lockstep_resident() : 256;
+  const int resident = lockstep_resident(), cus = resident > 0 ? resident : 256;
   return static_cast<int64_t>((tiles + NT - 1) / NT) * a.most_chosen * 4 >= int64_t(3) * cus;
 }
 
@@ -724,9 +718,8 @@ hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
   }
   if (e != hipSuccess) return e;
   if (one_down<E>(a, Block<BITS>::kBytes)) {
-    if (a.T <= 4) moe_down_few_kernel<E, BITS, G, 1><<<a.tiles_d, kFewWaves * kWave, 0, s>>>(a);
-    else moe_down_few_kernel<E, BITS, G, 4><<<a.tiles_d, kFewWaves * kWave, 0, s>>>(a);
-    return hipGetLastError();
+    return launch(a.T <= 4 ? moe_down_few_kernel<E, BITS, G, 1> : moe_down_few_kernel<E, BITS, G, 4>, dim3(a.tiles_d),
+                  kFewWaves * kWave, 0, s, a);
   }
   if (kSlim && fills(a, a.tiles_d, 4)) return go_down<E, BITS, G, kSlim ? 4 : 2>(a, s);
   if (fills(a, a.tiles_d, 2)) return go_down<E, BITS, G, 2>(a, s);

@@ -270,36 +270,27 @@ __global__ __launch_bounds__(kPackWaves* kWave) void weights_unpack_kernel(Weigh
   }
 }
 
-// Calls fn with the kernel instance of (element type, bits, group).
+// Launches the instance of K for (element type, bits, group).
 template <template <class, int, int> class K>
-void dispatch(const WeightsArgs& a, int dtype, dim3 grid, hipStream_t s) {
-  const dim3 block(kPackWaves * kWave);
+hipError_t dispatch(const WeightsArgs& a, int dtype, dim3 grid, hipStream_t s) {
+  auto go = [&](void (*kernel)(WeightsArgs)) { return launch(kernel, grid, kPackWaves * kWave, 0, s, a); };
   const bool f32 = dtype == 0;
-  if (a.bits == 16) {
-    K<EBf16, 16, 128>::go(a, grid, block, s);
-  } else if (a.group == 32) {
-    f32 ? K<EF32, 4, 32>::go(a, grid, block, s) : K<EBf16, 4, 32>::go(a, grid, block, s);
-  } else if (a.group == 64) {
-    f32 ? K<EF32, 4, 64>::go(a, grid, block, s) : K<EBf16, 4, 64>::go(a, grid, block, s);
-  } else {
-    f32 ? K<EF32, 4, 128>::go(a, grid, block, s) : K<EBf16, 4, 128>::go(a, grid, block, s);
-  }
+  if (a.bits == 16) return go(K<EBf16, 16, 128>::kernel());
+  if (a.group == 32) return go(f32 ? K<EF32, 4, 32>::kernel() : K<EBf16, 4, 32>::kernel());
+  if (a.group == 64) return go(f32 ? K<EF32, 4, 64>::kernel() : K<EBf16, 4, 64>::kernel());
+  return go(f32 ? K<EF32, 4, 128>::kernel() : K<EBf16, 4, 128>::kernel());
 }
 template <class E, int B, int G>
-struct GoPack {
-  static void go(const WeightsArgs& a, dim3 g, dim3 b, hipStream_t s) { weights_pack_kernel<E, B, G><<<g, b, 0, s>>>(a); }
+struct Pack {
+  static auto kernel() { return &weights_pack_kernel<E, B, G>; }
 };
 template <class E, int B, int G>
-struct GoPackT {
-  static void go(const WeightsArgs& a, dim3 g, dim3 b, hipStream_t s) {
-    weights_pack_t_kernel<E, B, G><<<g, b, 0, s>>>(a);
-  }
+struct PackT {
+  static auto kernel() { return &weights_pack_t_kernel<E, B, G>; }
 };
 template <class E, int B, int G>
-struct GoUnpack {
-  static void go(const WeightsArgs& a, dim3 g, dim3 b, hipStream_t s) {
-    weights_unpack_kernel<E, B, G><<<g, b, 0, s>>>(a);
-  }
+struct Unpack {
+  static auto kernel() { return &weights_unpack_kernel<E, B, G>; }
 };
 
 dim3 block_grid(const WeightsArgs& a) {
@@ -310,18 +301,13 @@ dim3 block_grid(const WeightsArgs& a) {
 }  // namespace
 
 hipError_t launch_weights_pack(const WeightsArgs& a, int dtype, bool transposed, hipStream_t s) {
-  if (transposed) {
-    const int64_t n = static_cast<int64_t>((a.tiles + 3) / 4) * a.blocks;
-    dispatch<GoPackT>(a, dtype, dim3(static_cast<unsigned>(n), static_cast<unsigned>(a.experts)), s);
-  } else {
-    dispatch<GoPack>(a, dtype, block_grid(a), s);
-  }
-  return hipGetLastError();
+  if (!transposed) return dispatch<Pack>(a, dtype, block_grid(a), s);
+  const int64_t n = static_cast<int64_t>((a.tiles + 3) / 4) * a.blocks;
+  return dispatch<PackT>(a, dtype, dim3(static_cast<unsigned>(n), static_cast<unsigned>(a.experts)), s);
 }
 
 hipError_t launch_weights_unpack(const WeightsArgs& a, int dtype, hipStream_t s) {
-  dispatch<GoUnpack>(a, dtype, block_grid(a), s);
-  return hipGetLastError();
+  return dispatch<Unpack>(a, dtype, block_grid(a), s);
 }
 
 }  // namespace twell

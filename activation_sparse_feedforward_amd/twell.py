@@ -477,12 +477,19 @@ def _fit(t, name: str, nbytes: int, dtype: torch.dtype) -> int:
 
 def _planes(desc: WDesc, w: Weights, name: str) -> CPlanes:
     codes, scales = desc.plane_bytes
+    c, s = w.codes, w.scales
+    if (scales and isinstance(c, torch.Tensor) and c.is_cuda and c.dtype is _CODE_DTYPE and c.nbytes >= codes
+            and c.is_contiguous() and isinstance(s, torch.Tensor) and s.is_cuda and s.dtype is _SCALE_DTYPE
+            and s.nbytes >= scales and s.is_contiguous()):  # _fit of both, without the calls
+        return CPlanes(c.data_ptr(), s.data_ptr())
     return CPlanes(_fit(w.codes, name + ".codes", codes, _CODE_DTYPE),
                    _fit(w.scales, name + ".scales", scales, _SCALE_DTYPE) if scales else 0)
 
 
 def _rows(t: torch.Tensor, name: str, n: int, width: int, dtype: torch.dtype) -> tuple:
     """Pointer and row stride of n rows of ``width`` elements, each row contiguous."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.shape == (n, width):
+        return t.data_ptr(), width
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -491,8 +498,6 @@ def _rows(t: torch.Tensor, name: str, n: int, width: int, dtype: torch.dtype) ->
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != (n, width):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n, width)}")
-    if t.is_contiguous():
-        return t.data_ptr(), width
     s0, s1 = t.stride()
     if width > 1 and s1 != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
@@ -545,13 +550,14 @@ def twell_weights_unpack(desc: WDesc, planes: Weights, w, stream=None):
 def twell_linear_fwd(desc: WDesc, planes: Weights, x, y, stream=None):
     """y [T, rows] = x [T, cols] times one matrix of 4-bit weights; x and y in bf16 or fp32, rows may be strided."""
     code = _any_dtype(x, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected {('T', desc.cols)}")
-    T, dtype = x.shape[0], x.dtype
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2:
+        raise ValueError(f"x: shape {tuple(shape)}, expected {('T', desc.cols)}")
+    T = shape[0]
     px, ldx = _rows(x, "x", T, desc.cols, dtype)
     py, ldy = _rows(y, "y", T, desc.rows, dtype)
     st = library().twell_linear_fwd(desc._ref, _planes(desc, planes, "planes"), T, code, px, ldx, py, ldy,
-                                    _stream_of(x, stream))
+                                    _raw_stream(x.get_device()) if stream is None else _stream(stream))
     if st:
         _check("twell_linear_fwd", st)
 
