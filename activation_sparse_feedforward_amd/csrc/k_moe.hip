@@ -700,18 +700,18 @@ bool one_down(const MoeArgs& a, int block_bytes) {
 // tokens, 2 of 4 experts of 512 x 512 in 4 bits: 18.7 us with one and one tile
 // against 25.9 with two and four; 12 tokens, 6 of 40 experts of 700 x 300: 23.1
 // against 19.3).
-bool fills(const MoeArgs& a, int tiles, int NT) {
-  const int resident = lockstep_resident(), cus = resident > 0 ? resident : 256;
+bool fills(const MoeArgs& a, int cus, int tiles, int NT) {
   return static_cast<int64_t>((tiles + NT - 1) / NT) * a.most_chosen * 4 >= int64_t(3) * cus;
 }
 
 template <class E, int BITS, int G>
 hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
   constexpr bool kSlim = BITS == 4 && E::kBytes == 2;  // room for twice the tiles in registers
+  const int resident = lockstep_resident(), cus = resident > 0 ? resident : 256;
   hipError_t e;
   if (a.T <= 4) {
     e = go_choices_up<E, BITS, G, true, 1>(a, s);
-  } else if (kSlim && fills(a, a.blocks_f * (kBlockK / kTileRows), 2)) {
+  } else if (kSlim && fills(a, cus, a.blocks_f * (kBlockK / kTileRows), 2)) {
     e = go_choices_up<E, BITS, G, false, kSlim ? 2 : 1>(a, s);
   } else {
     e = go_choices_up<E, BITS, G, false, 1>(a, s);
@@ -721,8 +721,8 @@ hipError_t by_tokens(const MoeArgs& a, hipStream_t s) {
     return launch(a.T <= 4 ? moe_down_few_kernel<E, BITS, G, 1> : moe_down_few_kernel<E, BITS, G, 4>, dim3(a.tiles_d),
                   kFewWaves * kWave, 0, s, a);
   }
-  if (kSlim && fills(a, a.tiles_d, 4)) return go_down<E, BITS, G, kSlim ? 4 : 2>(a, s);
-  if (fills(a, a.tiles_d, 2)) return go_down<E, BITS, G, 2>(a, s);
+  if (kSlim && fills(a, cus, a.tiles_d, 4)) return go_down<E, BITS, G, kSlim ? 4 : 2>(a, s);
+  if (fills(a, cus, a.tiles_d, 2)) return go_down<E, BITS, G, 2>(a, s);
   return go_down<E, BITS, G, 1>(a, s);
 }
 

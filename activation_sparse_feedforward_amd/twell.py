@@ -418,6 +418,12 @@ class MoeDesc:
         return self._strided(self.d_model, self.d_model)
 
     @functools.cached_property
+    def _call(self) -> tuple:
+        """What every call asks for: bytes of the router, the choices and the workspace among it."""
+        return (self.torch_dtype, self.T, self.d_model, self._ref, self.in_desc, self.out_desc,
+                self.experts * self.d_model * self.torch_dtype.itemsize, self.T * self.top_k * 4, self.ws_bytes)
+
+    @functools.cached_property
     def ws_bytes(self) -> int:
         """Bytes of twell_moe_fwd's workspace."""
         out = ctypes.c_size_t()
@@ -565,17 +571,16 @@ def twell_linear_fwd(desc: WDesc, planes: Weights, x, y, stream=None):
 def twell_moe_fwd(desc: MoeDesc, x, w_router, weights: MoeWeights, out: MoeOut, ws, router_bias=None, stream=None):
     """Router, chosen experts and their weighted sum for desc.T tokens (see include/twell.h).  x and out.y may have
     strided rows; ws holds moe_ws_bytes(desc) bytes."""
-    dt, d, T = desc.torch_dtype, desc.d_model, desc.T
+    dt, T, d, ref, din, dout, router, pairs, need = desc._call
     px, ldx = _rows(x, "x", T, d, dt)
-    py, ldy = _rows(out.y, "out.y", T, d, dt)
-    din, dout = desc.in_desc, desc.out_desc
-    pairs, need = T * desc.top_k * 4, desc.ws_bytes
+    y, ids, wts = out
+    py, ldy = _rows(y, "out.y", T, d, dt)
+    gate, up, down = weights
     st = library().twell_moe_fwd(
-        desc._ref if ldx == d and ldy == d else desc._strided(ldx, ldy), px,
-        _fit(w_router, "w_router", desc.experts * d * dt.itemsize, dt),
+        ref if ldx == d and ldy == d else desc._strided(ldx, ldy), px, _fit(w_router, "w_router", router, dt),
         _fit(router_bias, "router_bias", desc.experts * 4, torch.float32) if router_bias is not None else None,
-        _planes(din, weights.gate, "gate"), _planes(din, weights.up, "up"), _planes(dout, weights.down, "down"), py,
-        _fit(out.ids, "out.ids", pairs, torch.int32), _fit(out.weights, "out.weights", pairs, torch.float32),
-        _fit(ws, "ws", need, torch.uint8), need, _stream_of(x, stream))
+        _planes(din, gate, "gate"), _planes(din, up, "up"), _planes(dout, down, "down"), py,
+        _fit(ids, "out.ids", pairs, torch.int32), _fit(wts, "out.weights", pairs, torch.float32),
+        _fit(ws, "ws", need, torch.uint8), need, _raw_stream(x.get_device()) if stream is None else _stream(stream))
     if st:
         _check("twell_moe_fwd", st)
