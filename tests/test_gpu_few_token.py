@@ -322,6 +322,36 @@ def test_moe_router_of_a_few_tokens(T_, E, k, d, dtype):
     assert not torch.isnan(out.y[:T_ - 1]).any()
 
 
+@pytest.mark.parametrize("T_", [2, 20])
+def test_moe_planes_beyond_4_gib(T_):
+    """The last expert's weights begin 4.3 GiB into each plane."""
+    say(f"[gpu case] moe planes beyond 4 GiB T={T_}")
+    md = T.MoeDesc(T_, 4096, 4096, 140, 2, "bf16", 16, 0, "silu", True)
+    g = _gen(5)
+    x = _randn(g, T_, 4096).bfloat16()
+    router = _randn(g, 140, 4096, scale=4096 ** -0.5).bfloat16()
+    bias = torch.full((140,), float("-inf"), device="cuda")
+    bias[[1, 139]] = 0.0
+    w, kept = T.alloc_moe_weights(md), []
+    for desc, planes, transposed in ((md.in_desc, w.gate, False), (md.in_desc, w.up, False), (md.out_desc, w.down, True)):
+        full = torch.randn(140, 4096, 4096, generator=g, device="cuda", dtype=torch.bfloat16) / 64
+        T.twell_weights_pack(desc, full, planes, transposed=transposed)
+        kept.append(full[[1, 139]].double())
+        del full
+    out = T.alloc_moe_out(md)
+    T.twell_moe_fwd(md, x, router, w, out, T.alloc_moe_ws(md), router_bias=bias)
+    x64 = host64(x)
+    ids, wts = R.route(x64, host64(router), bias.cpu().numpy(), 2, True)
+    assert np.array_equal(out.ids.cpu().numpy(), ids)
+    xg, ref = x.double(), torch.zeros(T_, 4096, dtype=torch.float64, device="cuda")
+    for i, e in enumerate((1, 139)):
+        gate, up, down = (k[i] for k in kept)
+        a = xg @ gate.T
+        y = (a / (1 + torch.exp(-a)) * (xg @ up.T)) @ down
+        ref += y * torch.from_numpy((wts * (ids == e)).sum(1)).cuda()[:, None]
+    _close(out.y, ref.cpu().numpy(), "bf16", extra=4e-6 + 2.0 ** -17)
+
+
 @pytest.mark.parametrize("T_", [2, 40])
 def test_moe_masked_experts_ties_and_empty_rows(T_):
     md = T.MoeDesc(T_, 96, 40, 12, 4, "fp32", 4, 32, "silu", True)
