@@ -370,11 +370,13 @@ __device__ __forceinline__ int64_t token_of(int pair, const MoeArgs& a) {
   return static_cast<int>((static_cast<float>(pair) + 0.5f) * a.inv_k);
 }
 
-// Waves a SIMD that the registers leave room for.  fp32 data with 16-bit weights
-// needs more than 128 (64 tokens, 16 experts of 1500 x 700: 62 us against 75 with
-// spills); 4-bit weights gain about as much as they lose by it.
-template <class E, int BITS>
-constexpr int least_waves() { return E::kBytes == 4 && BITS == 16 ? 3 : 4; }
+// Waves a SIMD that the registers are to leave room for: four, but three where
+// four spill and that shows, which is with fp32 data and 16-bit weights (64 tokens,
+// 4 of 16 experts of 1500 x 700: 62 us against 75) and in the down kernel with
+// fp32 data (the same in 4 bits: 56 us against 63; the up kernel gains and loses
+// by it).
+template <class E, int BITS, bool DOWN>
+constexpr int least_waves() { return E::kBytes == 4 && (BITS == 16 || DOWN) ? 3 : 4; }
 
 // LDS of one wave: its list, and its token pieces or, after them, its sums.
 template <class Prod>
@@ -453,7 +455,7 @@ __device__ __forceinline__ void hand_on(const MoeArgs& a, int expert, int n, con
 // Where there are at least as many pairs as experts, nearly every expert has a
 // token: row y of the grid is then expert y, which needs no search.
 template <class E, int BITS, int G, bool kFew, int NT>
-__global__ __launch_bounds__(kMostWaves* kWave, (least_waves<E, BITS>())) void moe_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kMostWaves* kWave, (least_waves<E, BITS, false>())) void moe_up_kernel(MoeArgs a) {
   __shared__ WaveList lists[kMostWaves];
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -526,7 +528,7 @@ __device__ __forceinline__ void down_pairs(const MoeArgs& a, const Tiles<NT>& ti
 }
 
 template <class E, int BITS, int G, int NT>
-__global__ __launch_bounds__(kMostWaves* kWave, (least_waves<E, BITS>())) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kMostWaves* kWave, (least_waves<E, BITS, true>())) void moe_down_kernel(MoeArgs a) {
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
