@@ -42,6 +42,16 @@ __device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// Where lanes of a wave hand values to each other through LDS: what was written (or
+// read) before is done before anything after it, in the compiler's order too, which
+// the barrier alone does not ask for.  No workgroup barrier, and no instruction: a
+// wave's LDS operations come in order.
+__device__ __forceinline__ void lds_handoff() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // fp32 -> bf16 bits, round to nearest even, NaN stays NaN.
 __device__ __forceinline__ uint16_t bf16_of(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
 
@@ -246,7 +256,7 @@ struct Tokens {
       for (int i = 0; i < Src::kParts; ++i) q.v[j][i] = src.piece(row[j], b, i, lane & 15, whole);
   }
   __device__ __forceinline__ void store(const Loaded& q, int lane) const {
-    __builtin_amdgcn_wave_barrier();  // the block before has been read
+    lds_handoff();  // the block before has been read
 #pragma unroll
     for (int j = 0; j < TQ; ++j)
 #pragma unroll
@@ -263,7 +273,7 @@ struct Tokens {
           *reinterpret_cast<u32x4_t*>(lds + piece_at(r, 16 * i + c)) = q.v[j][i];
         }
       }
-    __builtin_amdgcn_wave_barrier();
+    lds_handoff();
   }
   __device__ __forceinline__ void step(const Loaded&, int s, int m, int lane, bf16x8_t (&x)[Src::kPlanes]) const {
     const int r = (m * 16 + lane_token(lane)) % kRows, g = lane >> 4;

@@ -330,14 +330,14 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, LivePairs<kPairsAhe
     look(0, static_cast<uint64_t>(wave_or(hi)) << 32 | wave_or(lo));
   } else {
     reinterpret_cast<u32x4_t*>(l.taken)[lane] = u32x4_t{0, 0, 0, 0};
-    __builtin_amdgcn_wave_barrier();
+    lds_handoff();
     for (int i0 = 0; i0 < pairs; i0 += kPairsAhead * 64) {
       if (i0 > 0) live.fetch(a, i0, lane);
 #pragma unroll
       for (int u = 0; u < kPairsAhead; ++u)
         if (live.id[u] >= 0) l.taken[live.id[u]] = 1;
     }
-    __builtin_amdgcn_wave_barrier();
+    lds_handoff();
     for (int e0 = 0; e0 < a.E; e0 += 64) look(e0, __ballot(l.taken[e0 + lane] != 0));
   }
   if (pairs > kPairsAhead * 64) live.fetch(a, 0, lane);
@@ -360,7 +360,7 @@ __device__ __forceinline__ int find_pairs(const MoeArgs& a, LivePairs<kPairsAhea
       n += __popcll(has);
     }
   }
-  __builtin_amdgcn_wave_barrier();
+  lds_handoff();
   return n;
 }
 

@@ -247,7 +247,7 @@ __global__ __launch_bounds__(kPackWaves* kWave) void weights_unpack_kernel(Weigh
       }
     }
   }
-  __builtin_amdgcn_wave_barrier();
+  lds_handoff();
   const int row0 = tile * kTileRows;
 #pragma unroll
   for (int j = 0; j < kPieces / 4; ++j) {  // 64 pieces are 64 / kPieces rows

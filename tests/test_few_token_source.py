@@ -1,0 +1,23 @@
+"""CPU checks of the few-token kernels' sources for what no result shows."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "activation_sparse_feedforward_amd", "csrc")
+SOURCES = ("few_token.hpp", "k_linear4.hip", "k_moe.hip", "k_weights.hip")
+
+
+def _code(name):
+    """A source without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_lanes_hand_over_through_lds_between_fences(name):
+    """A wave barrier orders no memory: it stands between a release and an acquire fence wherever it is used."""
+    fenced = re.compile(r'__builtin_amdgcn_fence\(__ATOMIC_RELEASE, "wavefront"\);\s*'
+                        r'__builtin_amdgcn_wave_barrier\(\);\s*'
+                        r'__builtin_amdgcn_fence\(__ATOMIC_ACQUIRE, "wavefront"\);')
+    assert "__builtin_amdgcn_wave_barrier" not in fenced.sub("", _code(name))
