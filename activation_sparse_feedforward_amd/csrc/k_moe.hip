@@ -270,7 +270,7 @@ __device__ __forceinline__ void few_choose(const MoeArgs& a, FewChoices& c, int 
 // Where one wave works out its expert and the expert's pairs.  Every wave does
 // so for itself, without a barrier: the pairs come from the L2 once, and
 // what follows are LDS and lane operations of a few hundred cycles.
-struct WaveList {
+struct alignas(16) WaveList {
   uint8_t taken[kMoeMaxExperts];  // more than 64 experts
   int pair[kMoeBlockTokens];
 };

@@ -21,3 +21,14 @@ def test_lanes_hand_over_through_lds_between_fences(name):
                         r'__builtin_amdgcn_wave_barrier\(\);\s*'
                         r'__builtin_amdgcn_fence\(__ATOMIC_ACQUIRE, "wavefront"\);')
     assert "__builtin_amdgcn_wave_barrier" not in fenced.sub("", _code(name))
+
+
+def test_what_is_stored_to_in_16_bytes_is_aligned_to_16():
+    """LDS that 16-byte vectors go to says so itself; the compiler's placing of variables is not relied on."""
+    code = _code("k_moe.hip")
+    assert "reinterpret_cast<u32x4_t*>(l.taken)" in code
+    assert re.search(r"struct alignas\(16\) WaveList \{\s*uint8_t taken\[", code)
+    for name in SOURCES:
+        for line in _code(name).splitlines():
+            if re.search(r"__shared__.*\bchar lds\[", line):
+                assert "__align__(16)" in line, (name, line)
