@@ -22,6 +22,8 @@
 // four tokens need one register, and one FMA per group of weights.
 #pragma once
 
+#include <atomic>
+
 #include "common.hpp"
 
 namespace twell {
@@ -33,6 +35,25 @@ template <class Args>
 hipError_t launch(void (*kernel)(Args), dim3 grid, unsigned threads, size_t lds, hipStream_t s, Args a) {
   void* args[] = {&a};
   return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, lds, s);
+}
+
+// The same for a kernel that is handed LDS at launch, kMost bytes at the most.  More
+// than 64 KB together with what the kernel declares itself has to be asked for, which
+// the first launch does (a process drives one GPU).  A refusal goes to the caller, and
+// the next call asks again.
+template <auto kKernel, size_t kMost, class Args>
+hipError_t launch_lds(dim3 grid, unsigned threads, size_t lds, hipStream_t s, const Args& a) {
+  static std::atomic<bool> allowed{false};
+  if (!allowed.load(std::memory_order_relaxed)) {
+    const void* kernel = reinterpret_cast<const void*>(kKernel);
+    hipFuncAttributes f{};
+    hipError_t e = hipFuncGetAttributes(&f, kernel);
+    if (e == hipSuccess && f.sharedSizeBytes + kMost > 64 * 1024)
+      e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
+    if (e != hipSuccess) return e;
+    allowed.store(true, std::memory_order_relaxed);
+  }
+  return launch(kKernel, grid, threads, lds, s, a);
 }
 
 constexpr int kTileRows = 16;

@@ -76,15 +76,10 @@ hipError_t go(const LinearArgs& a, hipStream_t s) {
   using Prod = Product<4, G, TQ, NR, std::conditional_t<E::kBytes == 2, SourceBf16, SourceF32>>;
   constexpr int kPerWave = Prod::kAll * 256 > Prod::X::kLdsBytes ? Prod::kAll * 256 : Prod::X::kLdsBytes;
   constexpr int kWaves = max_waves<E, TQ, NR>();
-  if constexpr (kWaves * kPerWave > 64 * 1024) {
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear4_kernel<E, G, TQ, NR>),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kWaves * kPerWave);
-    if (attr != hipSuccess) return attr;
-  }
   int waves = kWaves;
   while (waves > 1 && waves > a.blocks) waves >>= 1;
   const dim3 grid((a.tiles + NR - 1) / NR, static_cast<unsigned>((a.T + 4 * TQ - 1) / (4 * TQ)));
-  return launch(linear4_kernel<E, G, TQ, NR>, grid, waves * kWave, waves * kPerWave, s, a);
+  return launch_lds<&linear4_kernel<E, G, TQ, NR>, kWaves * kPerWave>(grid, waves * kWave, waves * kPerWave, s, a);
 }
 
 // Tiles per workgroup, NR in [kLeast, kMost]: the workgroups go round the CUs

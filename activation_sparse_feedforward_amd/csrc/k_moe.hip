@@ -663,7 +663,7 @@ hipError_t go_choices_up(MoeArgs a, hipStream_t s) {
   a.own_logits = kFew && a.T * a.E <= kOwnPerWave * w && static_cast<int64_t>(a.T) * a.E * a.d * E::kBytes <= kOwnBytes;
   const hipError_t e = go_route<E>(a, s);
   if (e != hipSuccess) return e;
-  return launch(moe_up_kernel<E, BITS, G, kFew, NT>, grid, w * kWave, w * kLds, s, a);
+  return launch_lds<&moe_up_kernel<E, BITS, G, kFew, NT>, kMostWaves * kLds>(grid, w * kWave, w * kLds, s, a);
 }
 
 template <class E, int BITS, int G, int NT>
@@ -671,12 +671,7 @@ hipError_t go_down(const MoeArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.tiles_d + NT - 1) / NT), static_cast<unsigned>(a.most_chosen));
   constexpr int kLds = wave_lds<DownProduct<E, BITS, G, 4, NT>>();
   const int w = waves_for(static_cast<int64_t>(grid.x) * grid.y, a.blocks_f);
-  if constexpr (kMostWaves * kLds > 64 * 1024) {
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_down_kernel<E, BITS, G, NT>),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kMostWaves * kLds);
-    if (attr != hipSuccess) return attr;
-  }
-  const hipError_t e = launch(moe_down_kernel<E, BITS, G, NT>, grid, w * kWave, w * kLds, s, a);
+  const hipError_t e = launch_lds<&moe_down_kernel<E, BITS, G, NT>, kMostWaves * kLds>(grid, w * kWave, w * kLds, s, a);
   if (e != hipSuccess) return e;
   const dim3 join(static_cast<unsigned>((a.d + 255) / 256), static_cast<unsigned>(a.T));
   return launch(moe_join_kernel<E>, join, 256, 0, s, a);

@@ -32,3 +32,17 @@ def test_what_is_stored_to_in_16_bytes_is_aligned_to_16():
         for line in _code(name).splitlines():
             if re.search(r"__shared__.*\bchar lds\[", line):
                 assert "__align__(16)" in line, (name, line)
+
+
+@pytest.mark.parametrize("name", [n for n in SOURCES if n.endswith(".hip")])
+def test_kernels_handed_lds_at_launch_ask_for_it(name):
+    """More than 64 KB of LDS, the kernel's own included, is asked for in one place that every such launch goes through:
+    launch() itself is for kernels that are handed none."""
+    code = _code(name)
+    assert "hipFuncSetAttribute" not in code and "<<<" not in code
+    handed = re.findall(r"void (\w+_kernel)\(\w+ a\) \{(?:(?!\n\}).)*?extern __shared__", code, re.S)
+    assert handed == {"k_linear4.hip": ["linear4_kernel"], "k_moe.hip": ["moe_up_kernel", "moe_down_kernel"],
+                      "k_weights.hip": []}[name]
+    for kernel in handed:
+        assert re.search(rf"launch_lds<&{kernel}<", code)
+        assert not re.search(rf"launch\({kernel}<", code)
