@@ -76,43 +76,23 @@ __device__ __forceinline__ void lds_handoff() {
 // fp32 -> bf16 bits, round to nearest even, NaN stays NaN.
 __device__ __forceinline__ uint16_t bf16_of(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
 
-// A constant in a vector register: v_and_or_b32 takes no literals and one scalar.
-__device__ __forceinline__ uint32_t vector_constant(uint32_t c) {
-  uint32_t v;
-  asm("v_mov_b32 %0, %1" : "=v"(v) : "s"(c));
-  return v;
-}
-
-// Eight 4-bit codes as bf16 values 16 + u: u belongs into mantissa bits 3 .. 6 of
-// 16.0 (bit pattern 0x4180), where the first pair is already; the other pairs
-// cost one rotation, every pair one and-or.  The offset 16 + 8 is taken off
-// again by a product with -24 (offset_operand).  For bf16 data: its sums are
-// rounded to 8 bits in the end.
+// Eight 4-bit codes as bf16 values q / 16, exact; the 16 is made good once, on the
+// sums (Product::run).  16 + u with the offset 24 taken off by a product with -24 is
+// half the work (7 operations instead of 15; 11008 x 4096 in 6.8 us instead of 7.5 for
+// one token, 64 tokens through an expert layer in 62 instead of 66), but a sum then
+// holds 24 times every input: beside an input of 1e4 nothing is left of 0.01 times a
+// code where the large one's code is 0, and 128 inputs of 2e35 overflow whose products
+// do not.
 __device__ __forceinline__ bf16x8_t codes_operand(uint32_t w) {
-  const uint32_t mask = vector_constant(0x00780078u), base = vector_constant(0x41804180u);
-  u32x4_t r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = (__builtin_rotateright32(w, 4 * j) & mask) | base;
-  return __builtin_bit_cast(bf16x8_t, r);
-}
-__device__ __forceinline__ bf16x8_t offset_operand() {
-  const u32x4_t r{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};  // -24
-  return __builtin_bit_cast(bf16x8_t, r);
-}
-
-// Eight 4-bit codes as bf16 values q.  2.5 operations per code instead of one,
-// for fp32 data: the matrix core cuts its sums off at the size of the largest
-// term, and with the offset's terms around 5 times the codes' that showed as
-// an error of 1.1e-6 of the result's norm (64 x 4096 weights, groups of 32),
-// one-sided; fp32 products of the plain kind have 3e-7.
-__device__ __forceinline__ bf16x8_t exact_codes_operand(uint32_t w) {
-  const int v = static_cast<int>(__builtin_rotateright32(w, 3) ^ 0x88888888u);  // u = q + 8 to two's complement
+  const uint32_t v = __builtin_rotateright32(w, 3) ^ 0x88888888u;  // u = q + 8 to two's complement
+  uint32_t h = v >> 4;
+  asm("" : "+v"(h));  // a word of its own: a conversion picks its byte for nothing, but not its nibble
   u32x4_t r;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float lo = static_cast<float>((v << (28 - 4 * j)) >> 28);
-    const float hi = static_cast<float>((v << (12 - 4 * j)) >> 28);
-    r[j] = (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xffff0000u);
+    const uint32_t n = (j & 1 ? h : v) >> (8 * (j >> 1));
+    const float lo = __builtin_amdgcn_cvt_off_f32_i4(n), hi = __builtin_amdgcn_cvt_off_f32_i4(n >> 16);
+    r[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
   }
   return __builtin_bit_cast(bf16x8_t, r);
 }
@@ -337,10 +317,7 @@ struct Block<4> {
   __device__ __forceinline__ void load(const uint8_t* p, int lane) {
     c = load_codes<STREAM>(p + lane * 16);
   }
-  template <bool EXACT>
-  __device__ __forceinline__ bf16x8_t step(int s) const {
-    return EXACT ? exact_codes_operand(c[s]) : codes_operand(c[s]);
-  }
+  __device__ __forceinline__ bf16x8_t step(int s) const { return codes_operand(c[s]); }
 };
 template <>
 struct Block<16> {
@@ -351,7 +328,6 @@ struct Block<16> {
 #pragma unroll
     for (int s = 0; s < 4; ++s) c[s] = load_codes<STREAM>(p + (s * 64 + lane) * 16);
   }
-  template <bool>
   __device__ __forceinline__ bf16x8_t step(int s) const { return __builtin_bit_cast(bf16x8_t, c[s]); }
 };
 
@@ -407,7 +383,6 @@ struct Product {
   static constexpr int P = Src::kPlanes;
   static constexpr int kRegs = token_regs<TQ>();
   static constexpr int kAll = NR * MT * kRegs;  // result registers
-  static constexpr bool kExact = P == 3;        // fp32 data: codes without the offset
   f32x4_t acc[MT][NR];
 
   __device__ __forceinline__ void clear() {
@@ -433,82 +408,39 @@ struct Product {
 #pragma unroll
           for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int p = P - 1; p >= 0; --p) acc[m][r] = mfma16(v[p], w.w[r].template step<true>(s), acc[m][r]);
+            for (int p = P - 1; p >= 0; --p) acc[m][r] = mfma16(v[p], w.w[r].step(s), acc[m][r]);
         }
       }
     } else {
       constexpr int kSteps = 4 / G;  // steps that share a scale
-      const bf16x8_t off = offset_operand();
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
-        f32x4_t base[MT];
+        f32x4_t t[MT][NR];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) base[m] = zero;
-        auto offset = [&](int m, const bf16x8_t(&v)[P]) {
-          if constexpr (!kExact) {
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int p = P - 1; p >= 0; --p) base[m] = mfma16(v[p], off, base[m]);
-          }
-        };
-        auto product = [&](f32x4_t& t, const bf16x8_t(&v)[P], bf16x8_t w) {
+          for (int r = 0; r < NR; ++r) t[m][r] = zero;
 #pragma unroll
-          for (int p = P - 1; p >= 0; --p) t = mfma16(v[p], w, t);
-        };
-        auto scaled = [&](int m, int r, const f32x4_t& t) {
-          const float sc = w.s[r].at(gr);
+        for (int i = 0; i < kSteps; ++i) {
+          bf16x8_t v[MT][P];
 #pragma unroll
-          for (int i = 0; i < kRegs; ++i) acc[m][r][i] = fmaf(sc, t[i], acc[m][r][i]);
-        };
-        if constexpr (!kExact && MT * kSteps * P <= 8) {
-          // all steps' tokens, then tile by tile, so that a tile's sum starts
-          // from the offset's
-          bf16x8_t v[MT][kSteps][P];
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-              x.step(xq, gr * kSteps + i, m, lane, v[m][i]);
-              offset(m, v[m][i]);
-            }
+          for (int m = 0; m < MT; ++m) x.step(xq, gr * kSteps + i, m, lane, v[m]);
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            f32x4_t t[MT];
+            const bf16x8_t c = w.w[r].step(gr * kSteps + i);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) t[m] = base[m];
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-              const bf16x8_t c = w.w[r].template step<kExact>(gr * kSteps + i);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) product(t[m], v[m][i], c);
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) scaled(m, r, t[m]);
+              for (int p = P - 1; p >= 0; --p) t[m][r] = mfma16(v[m][p], c, t[m][r]);
           }
-        } else {  // step by step, all tiles
-          f32x4_t t[MT][NR];
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float sc = w.s[r].at(gr);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int r = 0; r < NR; ++r) t[m][r] = zero;
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i) {
-            bf16x8_t v[MT][P];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              x.step(xq, gr * kSteps + i, m, lane, v[m]);
-              offset(m, v[m]);
-            }
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              const bf16x8_t c = w.w[r].template step<kExact>(gr * kSteps + i);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) product(t[m][r], v[m], c);
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) scaled(m, r, kExact ? t[m][r] : t[m][r] + base[m]);
+            for (int i = 0; i < kRegs; ++i) acc[m][r][i] = fmaf(sc, t[m][r][i], acc[m][r][i]);
         }
       }
     }
@@ -535,6 +467,12 @@ struct Product {
     }
     for (; b < whole_end; ++b) one_block(x, tile, b, true, lane);
     for (; b < b1; ++b) one_block(x, tile, b, false, lane);
+    if constexpr (BITS == 4) {  // codes_operand
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) acc[m][r] *= 16.f;
+    }
   }
   __device__ __forceinline__ void one_block(const X& x, const Tile (&tile)[NR], int b, bool whole, int lane) {
     XLoaded xq;

@@ -6,13 +6,12 @@
 // One workgroup per NR tiles of 16 weight rows and 4 TQ tokens; its waves split
 // the inputs and their sums are joined through LDS in wave order, so that one
 // launch does it all and a short product still has every CU reading.  Up to 16
-// tokens it is bound by reading the codes (bf16 data; 0.5 byte and one rotation
-// and one and-or for two weights): 11008 x 4096 takes 6.7 us for one token (3.5
-// TB/s) and 7.3 for 16, 4096 x 1024 2.6 us, of which the launch itself is 1.6.
-// Beyond that by getting the tokens to the matrix core, through the L1 and LDS
-// once per NR tiles: 128 tokens of 2048 x 8192 11.5 us (0.37 PFLOP/s), of 16384 x
-// 2048 21 us (0.41).  fp32 data costs three matrix instructions and 2.5 times the
-// unpacking: 7 tokens of 5001 x 1999 5.7 us.
+// tokens it is bound by reading the codes and unpacking them (0.5 byte and two
+// operations a weight): 11008 x 4096 takes 7.5 us for one token (3.1 TB/s) and 8.1
+// for 16, 4096 x 1024 2.7 us, of which the launch itself is 1.6.  Beyond that by
+// getting the tokens to the matrix core, through the L1 and LDS once per NR tiles:
+// 128 tokens of 2048 x 8192 12.7 us (0.34 PFLOP/s), of 16384 x 2048 21.7 us (0.40).
+// fp32 data costs three matrix instructions for one: 7 tokens of 5001 x 1999 5.2 us.
 #include "few_token.hpp"
 #include "internal.hpp"
 
@@ -23,6 +22,13 @@ namespace {
 template <class E, int TQ, int NR>
 constexpr int max_waves() {
   return E::kBytes == 2 ? (TQ < 8 && NR * token_tiles<TQ>() <= 4 ? 16 : 8) : TQ <= 2 || (TQ == 4 && NR <= 3) ? 16 : 8;
+}
+
+__device__ __forceinline__ bool holds_infinity(const uint16_t* x, int K) {
+#pragma unroll 1
+  for (int k = 0; k < K; ++k)
+    if ((x[k] & 0x7fff) == 0x7f80) return true;
+  return false;
 }
 
 template <class E, int G, int TQ, int NR>
@@ -58,15 +64,22 @@ __global__ __launch_bounds__((max_waves<E, TQ, NR>() * kWave)) void linear4_kern
   p.put(red, wave, lane);
   __syncthreads();
   for (int o = threadIdx.x; o < Prod::kAll * 64; o += blockDim.x) {
-    const float v = joined<Prod::kAll>(red, waves, o);
+    float v = joined<Prod::kAll>(red, waves, o);
     const int j = o >> 6, l = o & 63;
     const int i = j % Prod::kRegs, m = (j / Prod::kRegs) % MT, r = j / (Prod::kRegs * MT);
     const int t = m * 16 + result_token(i, l);
     const int n = (blockIdx.x * NR + r) * kTileRows + (l & 15);
     if (t < T && n < a.N) {
       Elem* y = static_cast<Elem*>(a.y) + (t0 + t) * a.ldy + n;
-      if constexpr (E::kBytes == 2) *y = bf16_of(v);
-      else *y = v;
+      if constexpr (E::kBytes == 2) {
+        // An infinite input makes its token's outputs NaN.  Codes of 0 and the cut of
+        // fp32 data do that by themselves; an infinite sum of bf16 data is asked
+        // whether it comes from one or from finite inputs.
+        if (fabsf(v) == INFINITY && holds_infinity(static_cast<const Elem*>(a.x) + (t0 + t) * a.ldx, a.K)) v = NAN;
+        *y = bf16_of(v);
+      } else {
+        *y = v;
+      }
     }
   }
 }

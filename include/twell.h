@@ -322,10 +322,11 @@ twell_status twell_weights_unpack(const twell_wdesc* d, twell_wplanes in, void* 
  *   x [T x cols], y [T x rows] in dtype, rows ldx / ldy apart.
  * Made for few tokens: the weights are read once per 4 to 64 of them, by how
  * many there are and how many workgroups that makes.  T = 0 is a no-op.
- * bf16 data: codes are multiplied as q + 24 and the 24 taken off again inside
- * the sum, so inputs beyond about 1e36 may overflow; fp32 data is cut into three
- * bf16 parts and multiplied with q.  Either way an infinite or NaN input makes
- * its own token's outputs NaN, and no other token's.  Deterministic. */
+ * Products x q are exact (fp32 data is cut into three bf16 parts for them, whose
+ * last bits end at 2^-133: inputs below 2^-109 have fewer than 24), so an input
+ * takes nothing from a row whose code for it is 0, and a group's sum of x q is
+ * finite where it is in fp32.  An infinite or NaN input makes its own token's
+ * outputs NaN, and no other token's.  Deterministic. */
 twell_status twell_linear_fwd(const twell_wdesc* d, twell_wplanes w, int64_t T, int32_t dtype, const void* x,
                               int64_t ldx, void* y, int64_t ldy, void* stream);
 
