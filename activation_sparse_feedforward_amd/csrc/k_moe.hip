@@ -590,6 +590,10 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
 // group t % 4 adds it to the sum of token t, so a token's choices come together
 // in one register.  TQ: quads of tokens.
 constexpr int kFewWaves = 16;
+// (pair, block)s that it takes at the most (one_down), of which each wave has its
+// share on the way at once.
+template <class E>
+constexpr int few_blocks() { return E::kBytes == 2 ? 64 : 32; }
 
 template <class E, int BITS, int G, int TQ>
 __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs a) {
@@ -617,7 +621,7 @@ __global__ __launch_bounds__(kFewWaves* kWave) void moe_down_few_kernel(MoeArgs 
     const Tile tile[1] = {{a.down_codes + blk * Block<BITS>::kBytes, a.down_scales + blk * (16 * G)}};
     Prod p;
     p.clear();
-    p.template run<4>(x, tile, b0, b1, b1, lane);
+    p.template run<few_blocks<E>() / kFewWaves>(x, tile, b0, b1, b1, lane);
     const int t = pair / a.k;
 #pragma unroll
     for (int q = 0; q < TQ; ++q)
@@ -689,7 +693,7 @@ hipError_t go_down(const MoeArgs& a, hipStream_t s) {
 template <class E>
 bool one_down(const MoeArgs& a, int block_bytes) {
   const int64_t blocks = static_cast<int64_t>(a.T) * a.k * a.blocks_f;
-  return a.T <= 16 && blocks <= (E::kBytes == 2 ? 64 : 32) && blocks * a.tiles_d * block_bytes <= int64_t(24) << 20;
+  return a.T <= 16 && blocks <= few_blocks<E>() && blocks * a.tiles_d * block_bytes <= int64_t(24) << 20;
 }
 
 // Whether NT of `tiles` tiles a workgroup leave work for most CUs: more tiles

@@ -46,3 +46,12 @@ def test_kernels_handed_lds_at_launch_ask_for_it(name):
     for kernel in handed:
         assert re.search(rf"launch_lds<&{kernel}<", code)
         assert not re.search(rf"launch\({kernel}<", code)
+
+
+def test_down_kernel_for_few_tokens_fetches_no_further_ahead_than_a_wave_has_blocks():
+    """The launcher's limit on (pair, block)s, over the kernel's waves, is what a wave fetches at once: a longer body
+    would be code that no call reaches."""
+    code = _code("k_moe.hip")
+    assert re.search(r"blocks <= few_blocks<E>\(\)", code)
+    kernel = code[code.index("void moe_down_few_kernel"):code.index("hipError_t go_route")]
+    assert re.findall(r"template run<(.*)>\(x,", kernel) == ["few_blocks<E>() / kFewWaves"]
