@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
@@ -481,6 +482,16 @@ def _fit(t, name: str, nbytes: int, dtype: torch.dtype) -> int:
     return _ptr(t, name, nbytes, dtype)  # says what is wrong
 
 
+def _shaped(t, name: str, shape: tuple) -> None:
+    """Refuses a tensor that holds something else than ``shape``: another number of elements, or other axes behind the
+    first.  A flat one says nothing of axes, and leading axes of 1 may be left out."""
+    if not isinstance(t, torch.Tensor) or t.shape == shape:
+        return
+    inner = shape[1:]
+    if t.numel() != math.prod(shape) or (inner and t.dim() > 1 and t.shape[-len(inner):] != inner):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+
+
 def _planes(desc: WDesc, w: Weights, name: str) -> CPlanes:
     codes, scales = desc.plane_bytes
     c, s = w.codes, w.scales
@@ -534,8 +545,10 @@ def _any_dtype(t, name: str) -> int:
 
 
 def twell_weights_pack(desc: WDesc, w, planes: Weights, transposed: bool = False, stream=None):
-    """Lay out w [experts, rows, cols] ([experts, cols, rows] if transposed; bf16, or fp32 for 4 bits) into planes."""
+    """Lay out w [experts, rows, cols] ([experts, cols, rows] if transposed; bf16, or fp32 for 4 bits) into planes.
+    A flat w is taken in that order; any other shape is refused."""
     code = _any_dtype(w, "w")
+    _shaped(w, "w", (desc.experts, desc.cols, desc.rows) if transposed else (desc.experts, desc.rows, desc.cols))
     n = desc.experts * desc.rows * desc.cols * w.element_size()
     st = library().twell_weights_pack(desc._ref, _fit(w, "w", n, w.dtype), code, 1 if transposed else 0,
                                       _planes(desc, planes, "planes"), _stream_of(w, stream))
@@ -544,8 +557,9 @@ def twell_weights_pack(desc: WDesc, w, planes: Weights, transposed: bool = False
 
 
 def twell_weights_unpack(desc: WDesc, planes: Weights, w, stream=None):
-    """Write the values that planes stand for to w [experts, rows, cols] (bf16, or fp32 for 4 bits)."""
+    """Write the values that planes stand for to w [experts, rows, cols] (bf16, or fp32 for 4 bits; flat will do)."""
     code = _any_dtype(w, "w")
+    _shaped(w, "w", (desc.experts, desc.rows, desc.cols))
     n = desc.experts * desc.rows * desc.cols * w.element_size()
     st = library().twell_weights_unpack(desc._ref, _planes(desc, planes, "planes"), _fit(w, "w", n, w.dtype), code,
                                         _stream_of(w, stream))
@@ -576,6 +590,9 @@ def twell_moe_fwd(desc: MoeDesc, x, w_router, weights: MoeWeights, out: MoeOut, 
     y, ids, wts = out
     py, ldy = _rows(y, "out.y", T, d, dt)
     gate, up, down = weights
+    _shaped(w_router, "w_router", (desc.experts, d))
+    if router_bias is not None:
+        _shaped(router_bias, "router_bias", (desc.experts,))
     st = library().twell_moe_fwd(
         ref if ldx == d and ldy == d else desc._strided(ldx, ldy), px, _fit(w_router, "w_router", router, dt),
         _fit(router_bias, "router_bias", desc.experts * 4, torch.float32) if router_bias is not None else None,
