@@ -350,6 +350,14 @@ _CODE = {torch.bfloat16: TWELL_BF16, torch.float32: TWELL_FP32}
 _CODE_DTYPE, _SCALE_DTYPE = torch.uint8, torch.bfloat16
 
 
+def _c_ints(width: int, /, **numbers) -> dict:
+    """The numbers as C takes them; ctypes alone would wrap the ones that do not fit."""
+    for name, v in numbers.items():
+        if not -(1 << (width - 1)) <= int(v) < 1 << (width - 1):
+            raise ValueError(f"{name}: {v} does not fit {width} bits")
+    return {name: int(v) for name, v in numbers.items()}
+
+
 @dataclass(frozen=True)
 class WDesc:
     """``experts`` matrices of ``rows`` outputs x ``cols`` inputs, held in 4 bits with a scale for every ``group``
@@ -362,7 +370,8 @@ class WDesc:
 
     @functools.cached_property
     def _ref(self):
-        return ctypes.byref(CWDesc(int(self.experts), int(self.rows), int(self.cols), int(self.bits), int(self.group)))
+        return ctypes.byref(CWDesc(**_c_ints(32, experts=self.experts, rows=self.rows, cols=self.cols, bits=self.bits,
+                                             group=self.group)))
 
     @functools.cached_property
     def plane_bytes(self) -> tuple:
@@ -411,8 +420,10 @@ class MoeDesc:
             raise ValueError(f"act {self.act!r}, dtype {self.dtype!r}: expected one of {tuple(ACTIVATIONS)} and "
                              f"{tuple(_TORCH)}")
         return ctypes.byref(CMoeDesc(
-            int(self.T), int(ldx), int(ldy), int(self.d_model), int(self.d_ff), int(self.experts), int(self.top_k),
-            _CODE[self.torch_dtype], int(self.bits), int(self.group), ACTIVATIONS[self.act], int(bool(self.renorm))))
+            **_c_ints(64, T=self.T, ldx=ldx, ldy=ldy),
+            **_c_ints(32, d_model=self.d_model, d_ff=self.d_ff, experts=self.experts, top_k=self.top_k, bits=self.bits,
+                      group=self.group),
+            dtype=_CODE[self.torch_dtype], act=ACTIVATIONS[self.act], renorm=int(bool(self.renorm))))
 
     @functools.cached_property
     def _ref(self):  # contiguous rows

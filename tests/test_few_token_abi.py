@@ -165,3 +165,26 @@ def test_binding_refuses_host_tensors_and_bad_shapes():
         T.moe_ws_bytes(T.MoeDesc(1, 128, 64, 8, 2, "bf16", 4, 64, act="tanh"))
     with pytest.raises(T.TwellError):
         T.moe_ws_bytes(T.MoeDesc(1, 128, 64, 8, 9, "bf16", 4, 64))
+
+
+@pytest.mark.parametrize("make", [
+    lambda big: T.WDesc(1, 64, 128, 4, big + 64), lambda big: T.WDesc(1, big + 64, 128, 4, 64),
+    lambda big: T.WDesc(big + 1, 64, 128, 16), lambda big: T.WDesc(1, 64, big + 128, 16, 0),
+    lambda big: T.WDesc(1, 64, 128, big + 16),
+])
+def test_numbers_beyond_32_bits_do_not_wrap(make):
+    for big in (1 << 32, -(1 << 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            make(big).plane_bytes
+        with pytest.raises(ValueError, match="32 bits"):
+            T.alloc_weights(make(big), device="cpu")
+
+
+@pytest.mark.parametrize("name", ["d_model", "d_ff", "experts", "top_k", "bits", "group"])
+def test_moe_numbers_beyond_32_bits_do_not_wrap(name):
+    good = dict(T=1, d_model=128, d_ff=64, experts=8, top_k=2, dtype="bf16", bits=4, group=64)
+    T.moe_ws_bytes(T.MoeDesc(**good))
+    with pytest.raises(ValueError, match="32 bits"):
+        T.moe_ws_bytes(T.MoeDesc(**{**good, name: good[name] + (1 << 32)}))
+    with pytest.raises(ValueError, match="64 bits"):
+        T.moe_ws_bytes(T.MoeDesc(**{**good, "T": 1 << 64}))
