@@ -13,7 +13,7 @@ import ctypes
 import functools
 import math
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 from typing import NamedTuple, Optional
 
 import torch
@@ -358,8 +358,15 @@ def _c_ints(width: int, /, **numbers) -> dict:
     return {name: int(v) for name, v in numbers.items()}
 
 
+class _Keeping:
+    """A descriptor that keeps C structs between calls: copies and pickles hold its fields alone."""
+
+    def __reduce__(self):
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
+
+
 @dataclass(frozen=True)
-class WDesc:
+class WDesc(_Keeping):
     """``experts`` matrices of ``rows`` outputs x ``cols`` inputs, held in 4 bits with a scale for every ``group``
     inputs of a row (32, 64 or 128), or in bf16 (``bits`` 16, ``group`` 0)."""
     experts: int
@@ -388,7 +395,7 @@ class Weights(NamedTuple):
 
 
 @dataclass(frozen=True)
-class MoeDesc:
+class MoeDesc(_Keeping):
     """A mixture-of-experts layer for T tokens; ``bits`` and ``group`` are those of the experts' weights."""
     T: int
     d_model: int

@@ -1,7 +1,10 @@
 """CPU tests of the few-token entry points: sizes, and bad arguments mapped to
 status codes before any HIP call."""
+import copy
 import ctypes
+import dataclasses
 import os
+import pickle
 
 import pytest
 import torch
@@ -188,3 +191,16 @@ def test_moe_numbers_beyond_32_bits_do_not_wrap(name):
         T.moe_ws_bytes(T.MoeDesc(**{**good, name: good[name] + (1 << 32)}))
     with pytest.raises(ValueError, match="64 bits"):
         T.moe_ws_bytes(T.MoeDesc(**{**good, "T": 1 << 64}))
+
+
+@pytest.mark.parametrize("desc", [T.WDesc(2, 64, 128, 4, 64), T.MoeDesc(3, 128, 64, 8, 2, "bf16", 4, 64)])
+def test_descriptors_are_copied_and_sent_after_their_first_use_as_before(desc):
+    """What a descriptor keeps of its C structs is its own affair: a model or a worker's arguments that hold one can be
+    copied and pickled."""
+    used = desc.plane_bytes if isinstance(desc, T.WDesc) else desc._call
+    for again in (copy.copy(desc), copy.deepcopy(desc), pickle.loads(pickle.dumps(desc)), dataclasses.replace(desc)):
+        assert again == desc and type(again) is type(desc) and hash(again) == hash(desc)
+        if isinstance(desc, T.WDesc):
+            assert again.plane_bytes == used
+        else:
+            assert again.ws_bytes == used[-1]
