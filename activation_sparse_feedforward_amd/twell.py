@@ -491,13 +491,25 @@ def alloc_moe_ws(desc: MoeDesc, device="cuda") -> torch.Tensor:
     return torch.empty(desc.ws_bytes, dtype=torch.uint8, device=device)
 
 
-def _fit(t, name: str, nbytes: int, dtype: torch.dtype) -> int:
-    """Pointer of a contiguous GPU tensor of the dtype with at least nbytes."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.nbytes >= nbytes and t.is_contiguous():
+def _device(t, name: str) -> int:
+    """The GPU that all tensors of a call are on, told by one of them."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: must be a GPU tensor (got {t.device})")
+    return dev
+
+
+def _fit(t, name: str, nbytes: int, dtype: torch.dtype, dev: int) -> int:
+    """Pointer of a contiguous tensor of the dtype with at least nbytes on GPU dev."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.nbytes >= nbytes
+            and t.is_contiguous()):
         return t.data_ptr()
     if t is None:
         raise TypeError(f"{name}: expected a torch.Tensor")
-    return _ptr(t, name, nbytes, dtype)  # says what is wrong
+    _ptr(t, name, nbytes, dtype)  # says what is wrong
+    raise ValueError(f"{name}: on cuda:{t.get_device()}, expected cuda:{dev}")
 
 
 def _shaped(t, name: str, shape: tuple) -> None:
@@ -510,25 +522,28 @@ def _shaped(t, name: str, shape: tuple) -> None:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
 
 
-def _planes(desc: WDesc, w: Weights, name: str) -> CPlanes:
+def _planes(desc: WDesc, w: Weights, name: str, dev: int) -> CPlanes:
     codes, scales = desc.plane_bytes
     c, s = w.codes, w.scales
-    if (scales and isinstance(c, torch.Tensor) and c.is_cuda and c.dtype is _CODE_DTYPE and c.nbytes >= codes
-            and c.is_contiguous() and isinstance(s, torch.Tensor) and s.is_cuda and s.dtype is _SCALE_DTYPE
-            and s.nbytes >= scales and s.is_contiguous()):  # _fit of both, without the calls
+    if (scales and isinstance(c, torch.Tensor) and c.get_device() == dev and c.dtype is _CODE_DTYPE
+            and c.nbytes >= codes and c.is_contiguous() and isinstance(s, torch.Tensor) and s.get_device() == dev
+            and s.dtype is _SCALE_DTYPE and s.nbytes >= scales and s.is_contiguous()):  # _fit of both, no calls
         return CPlanes(c.data_ptr(), s.data_ptr())
-    return CPlanes(_fit(w.codes, name + ".codes", codes, _CODE_DTYPE),
-                   _fit(w.scales, name + ".scales", scales, _SCALE_DTYPE) if scales else 0)
+    return CPlanes(_fit(w.codes, name + ".codes", codes, _CODE_DTYPE, dev),
+                   _fit(w.scales, name + ".scales", scales, _SCALE_DTYPE, dev) if scales else 0)
 
 
-def _rows(t: torch.Tensor, name: str, n: int, width: int, dtype: torch.dtype) -> tuple:
-    """Pointer and row stride of n rows of ``width`` elements, each row contiguous."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.shape == (n, width):
+def _rows(t: torch.Tensor, name: str, n: int, width: int, dtype: torch.dtype, dev: int) -> tuple:
+    """Pointer and row stride of n rows of ``width`` elements on GPU dev, each row contiguous."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous()
+            and t.shape == (n, width)):
         return t.data_ptr(), width
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a GPU tensor (got {t.device})")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, expected cuda:{dev}")
     if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != (n, width):
@@ -541,16 +556,32 @@ def _rows(t: torch.Tensor, name: str, n: int, width: int, dtype: torch.dtype) ->
     return t.data_ptr(), s0 if n > 1 else width
 
 
-def _stream_of(t: torch.Tensor, stream) -> int:
-    """The stream's handle; by default the one current on t's device."""
-    if stream is None:
-        return _raw_stream(t.get_device())
-    return _stream(stream)
-
-
 # The handle alone: building a Stream object costs more than the other checks of a call together.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+@functools.lru_cache(maxsize=None)
+def _device_count() -> int:
+    return torch.cuda.device_count()
+
+
+_current_device = torch.cuda.current_device
+
+
+def _current_is(dev: int) -> None:
+    """Every GPU has a default stream of handle 0, which to a launch means the current GPU's: the tensors have to be
+    there."""
+    if dev != _current_device():
+        raise ValueError(f"tensors on cuda:{dev}, default stream of the current device, cuda:{_current_device()}")
+
+
+def _stream_on(dev: int, stream) -> int:
+    """The stream's handle; by default the current one of GPU dev."""
+    handle = _raw_stream(dev) if stream is None else _stream(stream)
+    if not handle and _device_count() > 1:
+        _current_is(dev)
+    return handle
 
 
 def _any_dtype(t, name: str) -> int:
@@ -566,10 +597,11 @@ def twell_weights_pack(desc: WDesc, w, planes: Weights, transposed: bool = False
     """Lay out w [experts, rows, cols] ([experts, cols, rows] if transposed; bf16, or fp32 for 4 bits) into planes.
     A flat w is taken in that order; any other shape is refused."""
     code = _any_dtype(w, "w")
+    dev = _device(w, "w")
     _shaped(w, "w", (desc.experts, desc.cols, desc.rows) if transposed else (desc.experts, desc.rows, desc.cols))
     n = desc.experts * desc.rows * desc.cols * w.element_size()
-    st = library().twell_weights_pack(desc._ref, _fit(w, "w", n, w.dtype), code, 1 if transposed else 0,
-                                      _planes(desc, planes, "planes"), _stream_of(w, stream))
+    st = library().twell_weights_pack(desc._ref, _fit(w, "w", n, w.dtype, dev), code, 1 if transposed else 0,
+                                      _planes(desc, planes, "planes", dev), _stream_on(dev, stream))
     if st:
         _check("twell_weights_pack", st)
 
@@ -577,10 +609,11 @@ def twell_weights_pack(desc: WDesc, w, planes: Weights, transposed: bool = False
 def twell_weights_unpack(desc: WDesc, planes: Weights, w, stream=None):
     """Write the values that planes stand for to w [experts, rows, cols] (bf16, or fp32 for 4 bits; flat will do)."""
     code = _any_dtype(w, "w")
+    dev = _device(w, "w")
     _shaped(w, "w", (desc.experts, desc.rows, desc.cols))
     n = desc.experts * desc.rows * desc.cols * w.element_size()
-    st = library().twell_weights_unpack(desc._ref, _planes(desc, planes, "planes"), _fit(w, "w", n, w.dtype), code,
-                                        _stream_of(w, stream))
+    st = library().twell_weights_unpack(desc._ref, _planes(desc, planes, "planes", dev),
+                                        _fit(w, "w", n, w.dtype, dev), code, _stream_on(dev, stream))
     if st:
         _check("twell_weights_unpack", st)
 
@@ -591,11 +624,16 @@ def twell_linear_fwd(desc: WDesc, planes: Weights, x, y, stream=None):
     shape, dtype = x.shape, x.dtype
     if len(shape) != 2:
         raise ValueError(f"x: shape {tuple(shape)}, expected {('T', desc.cols)}")
-    T = shape[0]
-    px, ldx = _rows(x, "x", T, desc.cols, dtype)
-    py, ldy = _rows(y, "y", T, desc.rows, dtype)
-    st = library().twell_linear_fwd(desc._ref, _planes(desc, planes, "planes"), T, code, px, ldx, py, ldy,
-                                    _raw_stream(x.get_device()) if stream is None else _stream(stream))
+    T, dev = shape[0], x.get_device()
+    if dev < 0:
+        _device(x, "x")
+    px, ldx = _rows(x, "x", T, desc.cols, dtype, dev)
+    py, ldy = _rows(y, "y", T, desc.rows, dtype, dev)
+    handle = _raw_stream(dev) if stream is None else _stream(stream)  # _stream_on without the call
+    if not handle and _device_count() > 1:
+        _current_is(dev)
+    st = library().twell_linear_fwd(desc._ref, _planes(desc, planes, "planes", dev), T, code, px, ldx, py, ldy,
+                                    handle)
     if st:
         _check("twell_linear_fwd", st)
 
@@ -604,18 +642,19 @@ def twell_moe_fwd(desc: MoeDesc, x, w_router, weights: MoeWeights, out: MoeOut, 
     """Router, chosen experts and their weighted sum for desc.T tokens (see include/twell.h).  x and out.y may have
     strided rows; ws holds moe_ws_bytes(desc) bytes."""
     dt, T, d, ref, din, dout, router, pairs, need = desc._call
-    px, ldx = _rows(x, "x", T, d, dt)
+    dev = _device(x, "x")
+    px, ldx = _rows(x, "x", T, d, dt, dev)
     y, ids, wts = out
-    py, ldy = _rows(y, "out.y", T, d, dt)
+    py, ldy = _rows(y, "out.y", T, d, dt, dev)
     gate, up, down = weights
     _shaped(w_router, "w_router", (desc.experts, d))
     if router_bias is not None:
         _shaped(router_bias, "router_bias", (desc.experts,))
     st = library().twell_moe_fwd(
-        ref if ldx == d and ldy == d else desc._strided(ldx, ldy), px, _fit(w_router, "w_router", router, dt),
-        _fit(router_bias, "router_bias", desc.experts * 4, torch.float32) if router_bias is not None else None,
-        _planes(din, gate, "gate"), _planes(din, up, "up"), _planes(dout, down, "down"), py,
-        _fit(ids, "out.ids", pairs, torch.int32), _fit(wts, "out.weights", pairs, torch.float32),
-        _fit(ws, "ws", need, torch.uint8), need, _raw_stream(x.get_device()) if stream is None else _stream(stream))
+        ref if ldx == d and ldy == d else desc._strided(ldx, ldy), px, _fit(w_router, "w_router", router, dt, dev),
+        _fit(router_bias, "router_bias", desc.experts * 4, torch.float32, dev) if router_bias is not None else None,
+        _planes(din, gate, "gate", dev), _planes(din, up, "up", dev), _planes(dout, down, "down", dev), py,
+        _fit(ids, "out.ids", pairs, torch.int32, dev), _fit(wts, "out.weights", pairs, torch.float32, dev),
+        _fit(ws, "ws", need, torch.uint8, dev), need, _stream_on(dev, stream))
     if st:
         _check("twell_moe_fwd", st)

@@ -204,3 +204,55 @@ def test_descriptors_are_copied_and_sent_after_their_first_use_as_before(desc):
             assert again.plane_bytes == used
         else:
             assert again.ws_bytes == used[-1]
+
+
+class _On(torch.Tensor):
+    """A host tensor that claims to be on GPU `dev`; calls that hold it have no tokens, so that nothing is launched."""
+    dev = 0
+    is_cuda = True
+
+    def get_device(self):
+        return self.dev
+
+    @classmethod
+    def make(cls, dev, *shape, dtype=torch.bfloat16):
+        t = torch.zeros(*shape, dtype=dtype).as_subclass(cls)
+        t.dev = dev
+        return t
+
+
+def test_tensors_have_to_be_on_one_device_where_the_launch_goes(monkeypatch):
+    """A launch on the default stream goes to the current device, and all tensors of a call are on one: tensors of
+    another are refused, whichever argument it is."""
+    monkeypatch.setattr(T, "_device_count", lambda: 2)
+    wd, md = T.WDesc(1, 64, 128, 4, 64), T.MoeDesc(0, 128, 64, 2, 1, "bf16", 4, 64)
+
+    def planes(desc, dev):
+        return T.Weights(_On.make(dev, desc.plane_bytes[0], dtype=torch.uint8),
+                         _On.make(dev, desc.plane_bytes[1] // 2))
+
+    def linear(x=0, w=0, y=0):
+        T.twell_linear_fwd(wd, planes(wd, w), _On.make(x, 0, 128), _On.make(y, 0, 64), stream=0)
+
+    def moe(x=0, r=0, b=0, gate=0, up=0, down=0, y=0, ids=0, wts=0, ws=0):
+        out = T.MoeOut(_On.make(y, 0, 128), _On.make(ids, 0, 1, dtype=torch.int32),
+                       _On.make(wts, 0, 1, dtype=torch.float32))
+        T.twell_moe_fwd(md, _On.make(x, 0, 128), _On.make(r, 2, 128),
+                        T.MoeWeights(planes(md.in_desc, gate), planes(md.in_desc, up), planes(md.out_desc, down)), out,
+                        _On.make(ws, 256, dtype=torch.uint8), router_bias=_On.make(b, 2, dtype=torch.float32), stream=0)
+
+    for current, other in ((0, 1), (1, 0)):
+        monkeypatch.setattr(T, "_current_device", lambda: current)
+        for call, names in ((linear, "x w y"), (moe, "x r b gate up down y ids wts ws")):
+            names = names.split()
+            call(**dict.fromkeys(names, current))
+            for name in names:
+                with pytest.raises(ValueError, match=f"cuda:{other}"):
+                    call(**{**dict.fromkeys(names, current), name: other})
+            with pytest.raises(ValueError, match=f"cuda:{other}"):
+                call(**dict.fromkeys(names, other))
+    monkeypatch.setattr(T, "_current_device", lambda: 0)
+    with pytest.raises(ValueError, match="cuda:1"):
+        T.twell_weights_pack(wd, _On.make(0, 1, 64, 128), planes(wd, 1), stream=0)
+    with pytest.raises(ValueError, match="cuda:1"):
+        T.twell_weights_unpack(wd, planes(wd, 1), _On.make(0, 1, 64, 128), stream=0)
