@@ -103,7 +103,7 @@ typedef uint32_t u32x4_a4_t __attribute__((ext_vector_type(4), aligned(4)));
 
 // The 16 bytes of a row p of K elements that begin at element k, zeros beyond the
 // row's end.  One load, of the row's last 16 bytes at the latest, and a shift:
-// eight loads one by one take 5.0 us instead of 4.0 (7 tokens of 5001 x 1999).
+// eight loads one by one take 5.4 us instead of 4.4 (7 tokens of 5001 x 1999).
 __device__ __forceinline__ u32x4_t piece_until(const uint16_t* p, int k, int K) {
   if (K < 8) {
     u32x4_t r{0, 0, 0, 0};
@@ -121,8 +121,7 @@ __device__ __forceinline__ u32x4_t piece_until(const uint16_t* p, int k, int K) 
   return u32x4_t{static_cast<uint32_t>(first), static_cast<uint32_t>(first >> 32), static_cast<uint32_t>(second),
                  static_cast<uint32_t>(second >> 32)};
 }
-// Four elements are as well loaded one by one (7 tokens of 5001 x 1999: 6.1 us
-// against 6.3).
+// Four elements are as well loaded one by one (the other way was 3 % slower).
 __device__ __forceinline__ u32x4_t piece_until(const float* p, int k, int K) {
   u32x4_t r{0, 0, 0, 0};
 #pragma unroll
@@ -232,7 +231,7 @@ struct Tokens {
   static constexpr int kPartBytes = kRows * 256;
   // fp32 values are cut on their way into LDS where there are fewer rows than
   // the matrix has, since 16 / kRows matrix rows read each (an expert layer of 8
-  // tokens, 2 of 16 experts of 1024 x 1024: 21.9 us against 26.1); with all 16
+  // tokens, 2 of 16 experts of 1024 x 1024: 20.3 us against 21.5); with all 16
   // rows in use the work is the same and the LDS half as much again.
   static constexpr bool kCutFirst = Src::kCuts && TQ <= 2;
   static constexpr int kLdsBytes = (kCutFirst ? Src::kPlanes : Src::kParts) * kPartBytes;  // of one wave

@@ -97,9 +97,9 @@ hipError_t go(const LinearArgs& a, hipStream_t s) {
 
 // Tiles per workgroup, NR in [kLeast, kMost]: the workgroups go round the CUs
 // one after another, and one costs NR tiles and its tokens, about a tile's time.
-// (100 tokens of 8192 x 8192: 28.7 us with four tiles in one round against 44.6
-// with three in two; one token of 20480 x 2048: 7.2 with three in two rounds
-// against 8.0 with four in two.)
+// (100 tokens of 8192 x 8192: 30.4 us with four tiles in one round against 44.2
+// with three in two; one token of 20480 x 2048: 7.1 with three in two rounds
+// against 9.1 with four in two.)
 template <class E, int G, int TQ, int kLeast, int kMost>
 hipError_t by_rows(const LinearArgs& a, int cus, hipStream_t s) {
   const int64_t groups = (a.T + 4 * TQ - 1) / (4 * TQ);
@@ -122,15 +122,16 @@ template <class E, int G>
 hipError_t by_tokens(const LinearArgs& a, hipStream_t s) {
   const int resident = lockstep_resident(), cus = resident > 0 ? resident : 256;
   // As many tokens as there are at once (their weights are unpacked once), but
-  // fewer where that leaves CUs without work: 50 tokens of 700 x 6000 take 7.8 us
-  // by sixteens against 12.6 by 32, 16 of 2048 x 8192 5.2 by eights against 6.2.
+  // fewer where that leaves CUs without work: 50 tokens of 700 x 6000 take 5.9 us
+  // by sixteens against 8.6 by 32, 16 of 2048 x 8192 5.9 by eights against 6.4.
   auto fills = [&](int tokens) { return static_cast<int64_t>(a.tiles) * ((a.T + tokens - 1) / tokens) <= cus; };
   if (a.T <= 4 || fills(4)) return by_rows<E, G, 1, 1, 4>(a, cus, s);
   if (a.T <= 8 || fills(8)) return by_rows<E, G, 2, 1, 4>(a, cus, s);
   if (a.T <= 16 || fills(16)) return by_rows<E, G, 4, 1, 4>(a, cus, s);
   if constexpr (E::kBytes == 2) {
     // 64 tokens a workgroup save unpacking the codes twice, once that still
-    // leaves a workgroup for every CU
+    // leaves a workgroup for every CU: 128 tokens of 16384 x 2048 22.0 us against
+    // 27.0, but 64 of 8192 x 8192 22.7 against 19.8
     if (a.T > 32 && (a.tiles + 2) / 3 * ((a.T + 63) / 64) >= cus) return by_rows<E, G, 16, 3, 4>(a, cus, s);
     return by_rows<E, G, 8, 1, 4>(a, cus, s);
   }

@@ -12,14 +12,16 @@
 // (4) moe_join_kernel adds them up in the order of the choices; few tokens with
 // little to read take moe_down_few_kernel instead of both.
 // Nothing depends on timing.  Only chosen experts' weights are read, each once
-// per 16 of its tokens.
+// per 16 of its tokens (by moe_down_few_kernel once per token).
 //
-// Bound by reading them.  16 tokens, 4 of 32 bf16 experts of 2048 x 1024: 67 us for
-// 355 MB, of which up 38 (6.1 TB/s), down 22 (5.3), route 4.6, join 4.7.  64
-// tokens, 8 of 64 in 4 bits: 62 us for 215 MB, of which up 29 (4.9 TB/s), down 22
-// (3.3), route 5.9, join 4.7; unpacking keeps the vector units busy for nearly half
-// of that.  One token, 2 of 8 bf16 experts of 1024 x 4096: 15.4 us for 50 MB, up 9.9
-// and down 6.4, bound by starting and draining two launches of one round each.
+// Bound by reading them.  16 tokens, 4 of 32 bf16 experts of 2048 x 1024: 68 us for
+// 355 MB, of which up 40 (6.1 TB/s), down 22 (5.3), route 4.6, join 4.6.  64
+// tokens, 8 of 64 in 4 bits: 66 us for 215 MB, of which up 32 (4.5 TB/s), down 24
+// (2.9), route 6.0, join 4.7; unpacking keeps the vector units busy for half of up
+// and a third of down, and down moves as many bytes of h, in two planes, as of
+// codes.  One token, 2 of 8 bf16 experts of 1024 x 4096: 15.4 us for 50 MB, up 9.9
+// and down 6.3, bound by starting and draining two launches of one round each, the
+// second on 64 CUs.
 #include "few_token.hpp"
 #include "internal.hpp"
 
@@ -201,7 +203,7 @@ __device__ __forceinline__ void tell_choice(const MoeArgs& a, int64_t t, const C
 }
 
 // More than four tokens: a workgroup per token.  Bound by one CU's share of the
-// L2's bandwidth: 5.9 us for 64 experts of d 2048, 4.6 for 32.
+// L2's bandwidth: 6.0 us for 64 experts of d 2048, 4.6 for 32.
 template <class E>
 __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a) {
   __shared__ float logit[kMoeMaxExperts];
@@ -218,7 +220,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void moe_route_kernel(MoeArgs a
   if (wave == 0) tell_choice(a, t, choose(a, logit, lane), lane);
 }
 
-// Up to four tokens: a wave per logit spreads the router over the chip, 3.0 us
+// Up to four tokens: a wave per logit spreads the router over the chip, 2.8 us
 // for 256 KB of it where one workgroup takes 5.8, nearly all of it launch and one
 // trip to memory; the up kernel's workgroups choose for themselves.
 constexpr int kLogitWaves = 4;
@@ -234,9 +236,10 @@ __global__ __launch_bounds__(kLogitWaves* kWave) void moe_logits_kernel(MoeArgs 
 
 // What a workgroup of the up kernel works out for itself for up to four tokens:
 // the choices, and where that is a matter of one or two logits a wave the logits
-// too (1 token, 2 of 8 experts, d 1024: 15.3 us for a call against 16.6; 4 of 16,
-// d 2048: 11.6 against 12.2; 4 of 32: 12.9 against 12.4; 64 logits on 4 waves:
-// 14.0 against 9.9).
+// too (1 token, 2 of 8 experts, d 1024: 15.4 us for a call against 16.7; 4 of 16,
+// d 2048: 12.4 against 12.9; 4 of 32: 13.5 against 12.9; 8 of 64: 22.7 against
+// 16.6).  64 KB of router: 8 experts of d 4096 take 15.0 against 16.2; with 128 KB
+// it is 18.4 against 19.4 for 8 of d 8192, and 15.3 either way for 16 of d 4096.
 constexpr int kOwnPerWave = 2;
 constexpr int64_t kOwnBytes = 64 << 10;
 constexpr int kOwnLogits = kOwnPerWave * kMostWaves;
@@ -372,9 +375,13 @@ __device__ __forceinline__ int64_t token_of(int pair, const MoeArgs& a) {
 
 // Waves a SIMD that the registers are to leave room for: four, but three where
 // four spill and that shows, which is with fp32 data and 16-bit weights (64 tokens,
-// 4 of 16 experts of 1500 x 700: 62 us against 75) and in the down kernel with
-// fp32 data (the same in 4 bits: 56 us against 63; the up kernel gains and loses
-// by it).
+// 4 of 16 experts of 1500 x 700: 62 us against 77) and in the down kernel with
+// fp32 data (the same in 4 bits: 55 us against 60; the up kernel gains and loses
+// by it).  With four, the down kernel for bf16 data and 4 bits keeps 10 to 19
+// registers in memory, and still that is the better on most sizes: 64 tokens, 8 of
+// 64 experts of 2048 x 1024 66 us against 69 with three, 4 tokens 34 against 38, 48
+// tokens, 2 of 8 of 1024 x 4096 35 against 33.  Up with fp32 data and 4 bits keeps 2
+// to 6 in memory, down 5.
 template <class E, int BITS, bool DOWN>
 constexpr int least_waves() { return E::kBytes == 4 && (BITS == 16 || DOWN) ? 3 : 4; }
 
@@ -430,9 +437,10 @@ __device__ __forceinline__ void up_pairs(const MoeArgs& a, const Tiles<2 * NT>& 
     const float act = a.act == 0 ? (g < 0.f ? 0.f : g) : g / (1.f + expf(-g));
     float h = weights[pair[i]] * act * u;
     if (ti + r >= a.tiles_f) h = 0.f;  // neurons that fill the last block of 128
-    // the down projection reads h as bf16 values whose sum is h: two of them
-    // keep 16 bits, so that only the output's own rounding is seen in bf16;
-    // three keep all 24 for fp32
+    // the down projection reads h as bf16 values whose sum is h: three keep all 24
+    // bits for fp32; two keep 16, which moves a bf16 y by 1e-4 of its norm where its
+    // own rounding moves it by 1.7e-3 (with 24 bits for it 64 tokens in 4 bits take
+    // 72.6 us instead of 66.9, one token 16.6 instead of 15.4)
     uint16_t* out = a.h + static_cast<int64_t>(pair[i]) * a.h_row + (ti + r) * kTileRows + (l & 15);
 #pragma unroll
     for (int s = 0; s < (E::kBytes == 2 ? 2 : 3); ++s) {
@@ -650,7 +658,11 @@ hipError_t go_route(const MoeArgs& a, hipStream_t s) {
 
 // Waves per workgroup: as few as still make kFillWaves waves.  A workgroup's
 // waves wait for each other twice, so what fills the chip with single waves
-// streams best.
+// streams best.  Half as many and twice as many waves are slower: 64 tokens, 8 of
+// 64 experts of 2048 x 1024 in 4 bits 65.4 us against 68.0 and 68.4, 512 tokens 541
+// against 581 and 556, 1 token, 2 of 8 of 1024 x 4096 12.8 against 13.7 and 12.8;
+// but not with fp32 data, whose waves hold more: 64 tokens, 4 of 16 bf16 experts of
+// 1500 x 700 62.2 against 55.6 with half as many.
 constexpr int64_t kFillWaves = 4096;
 int waves_for(int64_t groups, int blocks) {
   int w = 1;
@@ -681,26 +693,28 @@ hipError_t go_down(const MoeArgs& a, hipStream_t s) {
   return launch(moe_join_kernel<E>, join, 256, 0, s, a);
 }
 
-// Up to so many (pair, block)s for a workgroup, and bytes in all, the one kernel
-// for few tokens is the faster: it reads an expert's weights once per pair, on as
-// many CUs as there are tiles of outputs, but saves a launch and the way of the
-// parts through memory.  Whole calls, this one against the other: 1 token, 2 of 8
-// bf16 experts of 1024 x 4096 (64 blocks, 16 MB) 15.4 against 19.5 us; 8 tokens, 1
-// of 4 in 4 bits, 512 x 512 (32) 10.7 against 11.7; 16 tokens, 1 of 8, 1024 x 512
-// (64) 13.1 against 13.1, in fp32 18.0 against 16.4; 5 tokens, 3 of 7, 1001 x 707
-// (90) 15.3 against 13.8; 1 token, 8 of 64 bf16 experts of 2048 x 1024 (64, 32 MB)
-// 31.8 against 28.7.
+// Up to so many (pair, block)s for a workgroup, and bytes in all, few tokens take the
+// one kernel: it reads an expert's weights once per pair, on as many CUs as there
+// are tiles of outputs, but saves a launch and the way of the parts through memory.
+// Whole calls, this one against the other: 1 token, 2 of 8 experts of 1024 x 4096
+// (64 blocks) 15.4 against 18.1 us in bf16, 12.8 against 14.9 in 4 bits; 8 tokens, 1
+// of 4 in 4 bits, 512 x 512 (32) 10.8 against 11.6; 16 tokens, 1 of 8, 1024 x 512
+// (64) 13.2 against 13.2, in fp32 14.7 against 13.6; 5 tokens, 3 of 7, 1001 x 707
+// (90) 16.1 against 14.6.  Beyond 24 MB it depends on what is in the caches: 1 token,
+// 2 of 8 bf16 experts of 2048 x 4096 (32 MB) 25.5 against 24.6 with the weights of
+// three calls before still there, 25.9 against 27.2 with those of twelve.
 template <class E>
 bool one_down(const MoeArgs& a, int block_bytes) {
   const int64_t blocks = static_cast<int64_t>(a.T) * a.k * a.blocks_f;
   return a.T <= 16 && blocks <= few_blocks<E>() && blocks * a.tiles_d * block_bytes <= int64_t(24) << 20;
 }
 
-// Whether NT of `tiles` tiles a workgroup leave work for most CUs: more tiles
-// share the tokens' way through LDS, fewer give more CUs something to read (64
-// tokens, 2 of 4 experts of 512 x 512 in 4 bits: 18.7 us with one and one tile
-// against 25.9 with two and four; 12 tokens, 6 of 40 experts of 700 x 300: 23.1
-// against 19.3).
+// Whether NT of `tiles` tiles a workgroup leave work for most CUs, three quarters:
+// more tiles share the tokens' way through LDS, fewer give more CUs something to
+// read.  With half of the CUs 4 tokens, 2 of 8 experts of 1024 x 4096 in 4 bits take
+// 26.8 us against 24.1 and 16, 1 of 8 of 1024 x 512, 14.0 against 13.2 (but 40, 2 of
+// 8 of 1024 x 700, 18.5 against 19.3); with all of them 5 tokens, 3 of 7 of 1001 x
+// 707, 15.0 against 14.6.
 bool fills(const MoeArgs& a, int cus, int tiles, int NT) {
   return static_cast<int64_t>((tiles + NT - 1) / NT) * a.most_chosen * 4 >= int64_t(3) * cus;
 }

@@ -370,7 +370,8 @@ twell_status twell_moe_sizes(const twell_moe_desc* d, size_t* ws);
  * are fp32.  With infinite inputs, and with hidden values that overflow, the
  * token's y is NaN.  Deterministic.  ws: twell_moe_sizes() bytes; nothing in it
  * needs to start at zero.  Made for few tokens: 64 of them at a time, an expert's
- * weights once per 16 of its tokens.  T = 0 is a no-op. */
+ * weights once per 16 of its tokens (its down projection once per token where
+ * there is little to read).  T = 0 is a no-op. */
 twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w_router, const float* router_bias,
                            twell_wplanes gate, twell_wplanes up, twell_wplanes down, void* y, int32_t* ids,
                            float* weights, void* ws, size_t ws_bytes, void* stream);
