@@ -215,6 +215,53 @@ struct MoeArgs {
   float* z;            // [T * k][d] the pairs' outputs (more than four tokens)
 };
 
+// Pairs (token, choice) sorted by expert.
+struct TokensSortArgs {
+  const int32_t* ids;  // [pairs]
+  int32_t* offsets;    // [E + 1]
+  int32_t* pair_row;   // [pairs]
+  int32_t* hist;       // [workgroups][E] workspace
+  int64_t pairs;
+  int64_t run;         // pairs of a workgroup (set by the launcher)
+  int32_t E, bits;     // bits: of the numbers 0 .. E (set by the launcher)
+};
+// Workgroups of a sort: what its workspace has rows of counts for.
+int tokens_sort_blocks(int64_t pairs);
+
+// Rows moved to their sorted places and back.
+struct TokensArgs {
+  const void* x;           // gather: [T x d]
+  const void* dy;          // combine's backward: [T x d]
+  const void* rows;        // [T * k x d]
+  void* rows_out;          // gather, combine's backward (or null there): [T * k x d]
+  void* y;                 // combine: [T x d]
+  const int32_t* pair_row;  // [T * k]
+  const float* weights;    // [T * k]; combine: null = 1
+  float* dweights;         // [T * k] or null
+  int64_t T, pairs, ld_tokens, ld_rows, ld_out;  // ld_out: of rows_out
+  int32_t d, k, pieces;    // pieces: of a row, one wave each (set by the launcher)
+};
+
+// Layer norm.
+constexpr int kNormMostWidth = 16384;
+constexpr int kNormMostBlocks = 1024;
+struct NormArgs {
+  const void* x;
+  const void* w;  // or null: ones
+  const void* b;  // or null: zeros
+  void* y;
+  float* stats;   // [T][2] mean, rstd; or null
+  const float* stats_in;
+  const void* dy;
+  void* dx;
+  float *dw, *db;  // either may be null
+  float* part;     // [blocks][2][d] workspace
+  int64_t T, ldx, ldy, lddx;  // ldy: of y, and of dy
+  int32_t d, blocks;
+  float eps;
+};
+int norm_blocks(int64_t T);
+
 // dtype: 0 = fp32, 1 = bf16.  Each returns hipSuccess or the launch error.
 hipError_t launch_gate_pack(const PackArgs& a, int dtype, hipStream_t s);
 hipError_t launch_fused_updown(const FusedArgs& a, int dtype, hipStream_t s);
@@ -239,6 +286,12 @@ hipError_t launch_weights_pack(const WeightsArgs& a, int dtype, bool transposed,
 hipError_t launch_weights_unpack(const WeightsArgs& a, int dtype, hipStream_t s);
 hipError_t launch_linear4(const LinearArgs& a, int dtype, hipStream_t s);
 hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t s);
+hipError_t launch_tokens_sort(TokensSortArgs a, hipStream_t s);
+hipError_t launch_tokens_gather(const TokensArgs& a, int dtype, hipStream_t s);
+hipError_t launch_tokens_combine(const TokensArgs& a, int dtype, hipStream_t s);
+hipError_t launch_tokens_combine_bwd(const TokensArgs& a, int dtype, hipStream_t s);
+hipError_t launch_norm_fwd(const NormArgs& a, int dtype, int w_dtype, hipStream_t s);
+hipError_t launch_norm_bwd(const NormArgs& a, int dtype, int w_dtype, hipStream_t s);
 
 // Lockstep launches: how many workgroups of one lockstep kernel (one per CU)
 // the current device runs at once; 0 if it cannot be queried.

@@ -220,6 +220,59 @@ MoeWs moe_ws(const twell_moe_desc* d) {
   return w;
 }
 
+// ---------------------------------------------------------------- a layer over many tokens
+twell_status check_elems(const void* p, int32_t dtype) { return p && elem_aligned(p, dtype) ? TWELL_OK : TWELL_EINVAL; }
+
+constexpr int64_t kMaxElems = int64_t(1) << 33;  // tokens x width: what the grids of one launch reach
+
+twell_status check_tokens(const twell_tokens_desc* d) {
+  if (!d || d->T < 0 || d->d_model <= 0 || d->experts <= 0 || d->top_k <= 0) return TWELL_EINVAL;
+  if (!known_dtype(d->dtype) || d->ld_tokens < d->d_model || d->ld_rows < d->d_model) return TWELL_EINVAL;
+  if (d->T > kMaxSide || d->d_model > kMaxSide || d->T * d->d_model > kMaxElems) return TWELL_EUNSUPPORTED;
+  if (d->experts > twell::kMoeMaxExperts || d->top_k > twell::kMoeMaxTopK) return TWELL_EUNSUPPORTED;
+  if (d->ld_tokens > kMaxStride || d->ld_rows > kMaxStride) return TWELL_EUNSUPPORTED;
+  return TWELL_OK;
+}
+// Counts of each workgroup of the sort.
+size_t tokens_ws(const twell_tokens_desc* d) {
+  return align256(static_cast<size_t>(twell::tokens_sort_blocks(d->T * d->top_k)) * d->experts * 4);
+}
+twell::TokensArgs tokens_args(const twell_tokens_desc* d, const int32_t* pair_row) {
+  twell::TokensArgs a{};
+  a.pair_row = pair_row;
+  a.T = d->T;
+  a.pairs = d->T * d->top_k;
+  a.ld_tokens = d->ld_tokens;
+  a.ld_rows = d->ld_rows;
+  a.d = d->d_model;
+  a.k = d->top_k;
+  return a;
+}
+
+twell_status check_norm(const twell_norm_desc* d) {
+  if (!d || d->T < 0 || d->d_model <= 0 || !known_dtype(d->dtype) || !known_dtype(d->w_dtype)) return TWELL_EINVAL;
+  if (!(d->eps >= 0.f) || d->eps > 3.4e38f) return TWELL_EINVAL;
+  if (d->ldx < d->d_model || d->ldy < d->d_model || d->lddx < d->d_model) return TWELL_EINVAL;
+  if (d->T > kMaxSide || d->d_model > twell::kNormMostWidth) return TWELL_EUNSUPPORTED;
+  if (d->ldx > kMaxStride || d->ldy > kMaxStride || d->lddx > kMaxStride) return TWELL_EUNSUPPORTED;
+  return TWELL_OK;
+}
+// Each workgroup's sums of dw and db.
+size_t norm_ws(const twell_norm_desc* d) {
+  return align256(static_cast<size_t>(twell::norm_blocks(d->T)) * 2 * d->d_model * 4);
+}
+twell::NormArgs norm_args(const twell_norm_desc* d) {
+  twell::NormArgs a{};
+  a.T = d->T;
+  a.ldx = d->ldx;
+  a.ldy = d->ldy;
+  a.lddx = d->lddx;
+  a.d = d->d_model;
+  a.blocks = twell::norm_blocks(d->T);
+  a.eps = d->eps;
+  return a;
+}
+
 }  // namespace
 
 namespace twell {
@@ -704,6 +757,127 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
     TWELL_TRY(from_hip(twell::launch_moe(a, d->dtype, s)));
   }
   return TWELL_OK;
+}
+
+twell_status twell_tokens_sizes(const twell_tokens_desc* d, size_t* ws) {
+  TWELL_TRY(check_tokens(d));
+  if (!ws) return TWELL_EINVAL;
+  *ws = tokens_ws(d);
+  return TWELL_OK;
+}
+
+twell_status twell_tokens_sort(const twell_tokens_desc* d, const int32_t* ids, int32_t* offsets, int32_t* pair_row,
+                               void* ws, size_t ws_bytes, void* stream) {
+  TWELL_TRY(check_tokens(d));
+  if (!offsets || !aligned4(offsets)) return TWELL_EINVAL;
+  if (d->T > 0 && (!ids || !pair_row || !aligned4(ids) || !aligned4(pair_row))) return TWELL_EINVAL;
+  if (!ws || !aligned16(ws) || ws_bytes < tokens_ws(d)) return TWELL_EINVAL;
+  twell::TokensSortArgs a{};
+  a.ids = ids;
+  a.offsets = offsets;
+  a.pair_row = pair_row;
+  a.hist = static_cast<int32_t*>(ws);
+  a.pairs = d->T * d->top_k;
+  a.E = d->experts;
+  return from_hip(twell::launch_tokens_sort(a, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_tokens_gather(const twell_tokens_desc* d, const void* x, const int32_t* pair_row, void* rows,
+                                 void* stream) {
+  TWELL_TRY(check_tokens(d));
+  if (d->T == 0) return TWELL_OK;
+  TWELL_TRY(check_elems(x, d->dtype));
+  TWELL_TRY(check_elems(rows, d->dtype));
+  if (!pair_row || !aligned4(pair_row)) return TWELL_EINVAL;
+  twell::TokensArgs a = tokens_args(d, pair_row);
+  a.x = x;
+  a.rows_out = rows;
+  a.ld_out = d->ld_rows;
+  return from_hip(twell::launch_tokens_gather(a, d->dtype, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_tokens_combine(const twell_tokens_desc* d, const void* rows, const int32_t* pair_row,
+                                  const float* weights, void* y, void* stream) {
+  TWELL_TRY(check_tokens(d));
+  if (d->T == 0) return TWELL_OK;
+  TWELL_TRY(check_elems(rows, d->dtype));
+  TWELL_TRY(check_elems(y, d->dtype));
+  if (!pair_row || !aligned4(pair_row) || (weights && !aligned4(weights))) return TWELL_EINVAL;
+  twell::TokensArgs a = tokens_args(d, pair_row);
+  a.rows = rows;
+  a.weights = weights;
+  a.y = y;
+  return from_hip(twell::launch_tokens_combine(a, d->dtype, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_tokens_combine_bwd(const twell_tokens_desc* d, const void* rows, const int32_t* pair_row,
+                                      const float* weights, const void* dy, void* drows, int64_t ld_drows,
+                                      float* dweights, void* stream) {
+  TWELL_TRY(check_tokens(d));
+  if (drows && ld_drows < d->d_model) return TWELL_EINVAL;
+  if (drows && ld_drows > kMaxStride) return TWELL_EUNSUPPORTED;
+  if (d->T == 0 || (!drows && !dweights)) return TWELL_OK;
+  TWELL_TRY(check_elems(dy, d->dtype));
+  if (dweights) TWELL_TRY(check_elems(rows, d->dtype));
+  if (drows) TWELL_TRY(check_elems(drows, d->dtype));
+  if (!pair_row || !aligned4(pair_row) || !weights || !aligned4(weights) || (dweights && !aligned4(dweights)))
+    return TWELL_EINVAL;
+  twell::TokensArgs a = tokens_args(d, pair_row);
+  a.rows = rows;
+  a.weights = weights;
+  a.dy = dy;
+  a.rows_out = drows;
+  a.ld_out = ld_drows;
+  a.dweights = dweights;
+  return from_hip(twell::launch_tokens_combine_bwd(a, d->dtype, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_layernorm_sizes(const twell_norm_desc* d, size_t* ws) {
+  TWELL_TRY(check_norm(d));
+  if (!ws) return TWELL_EINVAL;
+  *ws = norm_ws(d);
+  return TWELL_OK;
+}
+
+twell_status twell_layernorm_fwd(const twell_norm_desc* d, const void* x, const void* w, const void* b, void* y,
+                                 float* stats, void* stream) {
+  TWELL_TRY(check_norm(d));
+  if (d->T == 0) return TWELL_OK;
+  TWELL_TRY(check_elems(x, d->dtype));
+  TWELL_TRY(check_elems(y, d->dtype));
+  if ((w && !elem_aligned(w, d->w_dtype)) || (b && !elem_aligned(b, d->w_dtype)) || (stats && !aligned4(stats)))
+    return TWELL_EINVAL;
+  twell::NormArgs a = norm_args(d);
+  a.x = x;
+  a.w = w;
+  a.b = b;
+  a.y = y;
+  a.stats = stats;
+  return from_hip(twell::launch_norm_fwd(a, d->dtype, d->w_dtype, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_layernorm_bwd(const twell_norm_desc* d, const void* x, const void* w, const float* stats,
+                                 const void* dy, void* dx, float* dw, float* db, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  TWELL_TRY(check_norm(d));
+  if (d->T > 0) {
+    TWELL_TRY(check_elems(x, d->dtype));
+    TWELL_TRY(check_elems(dy, d->dtype));
+    TWELL_TRY(check_elems(dx, d->dtype));
+    if (!stats || !aligned4(stats) || (w && !elem_aligned(w, d->w_dtype))) return TWELL_EINVAL;
+    if (!ws || !aligned16(ws) || ws_bytes < norm_ws(d)) return TWELL_EINVAL;
+  }
+  if ((dw && !aligned4(dw)) || (db && !aligned4(db))) return TWELL_EINVAL;
+  twell::NormArgs a = norm_args(d);
+  a.x = x;
+  a.w = w;
+  a.stats_in = stats;
+  a.dy = dy;
+  a.dx = dx;
+  a.dw = dw;
+  a.db = db;
+  a.part = static_cast<float*>(ws);
+  return from_hip(twell::launch_norm_bwd(a, d->dtype, d->w_dtype, static_cast<hipStream_t>(stream)));
 }
 
 const char* twell_status_str(twell_status s) {

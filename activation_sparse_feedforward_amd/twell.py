@@ -28,7 +28,9 @@ TWELL_FP32, TWELL_BF16 = 0, 1
 EXPORTED = ("twell_sizes", "twell_pack", "twell_pack_classic", "twell_ffn_fwd", "twell_ffn_fwd_hybrid",
             "twell_ffn_bwd", "twell_dense_ffn_fwd", "twell_status_str", "twell_ffn_fwd_hybrid_noalloc",
             "twell_weights_sizes", "twell_weights_pack", "twell_weights_unpack", "twell_linear_fwd",
-            "twell_moe_sizes", "twell_moe_fwd")
+            "twell_moe_sizes", "twell_moe_fwd", "twell_tokens_sizes", "twell_tokens_sort", "twell_tokens_gather",
+            "twell_tokens_combine", "twell_tokens_combine_bwd", "twell_layernorm_sizes", "twell_layernorm_fwd",
+            "twell_layernorm_bwd")
 
 
 class TwellError(RuntimeError):
@@ -77,6 +79,18 @@ class CMoeDesc(ctypes.Structure):
                 ("group", ctypes.c_int32), ("act", ctypes.c_int32), ("renorm", ctypes.c_int32)]
 
 
+class CTokensDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("ld_tokens", ctypes.c_int64), ("ld_rows", ctypes.c_int64),
+                ("d_model", ctypes.c_int32), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class CNormDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("lddx", ctypes.c_int64),
+                ("d_model", ctypes.c_int32), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -107,6 +121,14 @@ def library() -> ctypes.CDLL:
             "twell_linear_fwd": (ST, [ctypes.POINTER(CWDesc), CPlanes, I64, I32, P, I64, P, I64, P]),
             "twell_moe_sizes": (ST, [ctypes.POINTER(CMoeDesc), ctypes.POINTER(SZ)]),
             "twell_moe_fwd": (ST, [ctypes.POINTER(CMoeDesc), P, P, P, CPlanes, CPlanes, CPlanes, P, P, P, P, SZ, P]),
+            "twell_tokens_sizes": (ST, [ctypes.POINTER(CTokensDesc), ctypes.POINTER(SZ)]),
+            "twell_tokens_sort": (ST, [ctypes.POINTER(CTokensDesc), P, P, P, P, SZ, P]),
+            "twell_tokens_gather": (ST, [ctypes.POINTER(CTokensDesc), P, P, P, P]),
+            "twell_tokens_combine": (ST, [ctypes.POINTER(CTokensDesc), P, P, P, P, P]),
+            "twell_tokens_combine_bwd": (ST, [ctypes.POINTER(CTokensDesc), P, P, P, P, P, I64, P, P]),
+            "twell_layernorm_sizes": (ST, [ctypes.POINTER(CNormDesc), ctypes.POINTER(SZ)]),
+            "twell_layernorm_fwd": (ST, [ctypes.POINTER(CNormDesc), P, P, P, P, P, P]),
+            "twell_layernorm_bwd": (ST, [ctypes.POINTER(CNormDesc), P, P, P, P, P, P, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -658,3 +680,200 @@ def twell_moe_fwd(desc: MoeDesc, x, w_router, weights: MoeWeights, out: MoeOut, 
         _fit(ws, "ws", need, torch.uint8, dev), need, _stream_on(dev, stream))
     if st:
         _check("twell_moe_fwd", st)
+
+
+# ----------------------------------------------------------------------------- a layer over many tokens
+@dataclass(frozen=True)
+class TokensDesc(_Keeping):
+    """T tokens of ``d_model`` elements, ``top_k`` choices among ``experts`` each."""
+    T: int
+    d_model: int
+    experts: int
+    top_k: int
+    dtype: str  # "fp32" | "bf16": of tokens and rows
+
+    @functools.cached_property
+    def torch_dtype(self) -> torch.dtype:
+        if self.dtype not in _TORCH:
+            raise ValueError(f"dtype {self.dtype!r}: expected one of {tuple(_TORCH)}")
+        return _TORCH[self.dtype]
+
+    @functools.cached_property
+    def pairs(self) -> int:
+        return self.T * self.top_k
+
+    def _strided(self, ld_tokens: int, ld_rows: int):
+        return ctypes.byref(CTokensDesc(
+            **_c_ints(64, T=self.T, ld_tokens=ld_tokens, ld_rows=ld_rows),
+            **_c_ints(32, d_model=self.d_model, experts=self.experts, top_k=self.top_k),
+            dtype=_CODE[self.torch_dtype]))
+
+    @functools.cached_property
+    def _ref(self):  # contiguous rows
+        return self._strided(self.d_model, self.d_model)
+
+    def _at(self, ld_tokens: int, ld_rows: int):
+        d = self.d_model
+        return self._ref if ld_tokens == d and ld_rows == d else self._strided(ld_tokens, ld_rows)
+
+    @functools.cached_property
+    def ws_bytes(self) -> int:
+        """Bytes of twell_tokens_sort's workspace."""
+        out = ctypes.c_size_t()
+        _check("twell_tokens_sizes", library().twell_tokens_sizes(self._ref, ctypes.byref(out)))
+        return int(out.value)
+
+
+class TokensOrder(NamedTuple):
+    """The order of (token, choice) pairs by expert."""
+    offsets: torch.Tensor   # int32 [experts + 1]: the first row of each expert, and the number of rows
+    pair_row: torch.Tensor  # int32 [T, top_k]: the row of each pair, -1 where it has none
+
+
+@dataclass(frozen=True)
+class NormDesc(_Keeping):
+    """Layer norm of T rows of ``d_model`` elements."""
+    T: int
+    d_model: int
+    dtype: str  # "fp32" | "bf16": of rows
+    eps: float = 1e-5
+
+    @functools.cached_property
+    def torch_dtype(self) -> torch.dtype:
+        if self.dtype not in _TORCH:
+            raise ValueError(f"dtype {self.dtype!r}: expected one of {tuple(_TORCH)}")
+        return _TORCH[self.dtype]
+
+    def _strided(self, w_dtype: int, ldx: int, ldy: int, lddx: int):
+        return ctypes.byref(CNormDesc(**_c_ints(64, T=self.T, ldx=ldx, ldy=ldy, lddx=lddx),
+                                      **_c_ints(32, d_model=self.d_model), dtype=_CODE[self.torch_dtype],
+                                      w_dtype=w_dtype, eps=float(self.eps)))
+
+    @functools.cached_property
+    def _refs(self) -> tuple:  # contiguous rows, by w_dtype
+        d = self.d_model
+        return self._strided(TWELL_FP32, d, d, d), self._strided(TWELL_BF16, d, d, d)
+
+    def _at(self, w_dtype: int, ldx: int, ldy: int, lddx: int):
+        return (self._refs[w_dtype] if ldx == ldy == lddx == self.d_model else self._strided(w_dtype, ldx, ldy, lddx))
+
+    @functools.cached_property
+    def ws_bytes(self) -> int:
+        """Bytes of twell_layernorm_bwd's workspace."""
+        out = ctypes.c_size_t()
+        _check("twell_layernorm_sizes", library().twell_layernorm_sizes(self._refs[0], ctypes.byref(out)))
+        return int(out.value)
+
+
+def alloc_tokens_order(desc: TokensDesc, device="cuda") -> TokensOrder:
+    return TokensOrder(torch.empty(desc.experts + 1, dtype=torch.int32, device=device),
+                       torch.empty((desc.T, desc.top_k), dtype=torch.int32, device=device))
+
+
+def alloc_tokens_ws(desc: TokensDesc, device="cuda") -> torch.Tensor:
+    return torch.empty(desc.ws_bytes, dtype=torch.uint8, device=device)
+
+
+def alloc_norm_ws(desc: NormDesc, device="cuda") -> torch.Tensor:
+    return torch.empty(desc.ws_bytes, dtype=torch.uint8, device=device)
+
+
+def _exactly(t, name: str, shape: tuple, dtype: torch.dtype, dev: int) -> int:
+    """Pointer of a contiguous tensor of just this shape and dtype on GPU dev."""
+    if isinstance(t, torch.Tensor) and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    return _fit(t, name, 0, dtype, dev)
+
+
+def twell_tokens_sort(desc: TokensDesc, ids, order: TokensOrder, ws, stream=None):
+    """The order of pairs by expert: ids int32 [T, top_k] to order.offsets and order.pair_row (see include/twell.h)."""
+    dev = _device(ids, "ids")
+    shape = (desc.T, desc.top_k)
+    st = library().twell_tokens_sort(
+        desc._ref, _exactly(ids, "ids", shape, torch.int32, dev),
+        _exactly(order.offsets, "order.offsets", (desc.experts + 1,), torch.int32, dev),
+        _exactly(order.pair_row, "order.pair_row", shape, torch.int32, dev),
+        _fit(ws, "ws", desc.ws_bytes, torch.uint8, dev), desc.ws_bytes, _stream_on(dev, stream))
+    if st:
+        _check("twell_tokens_sort", st)
+
+
+def twell_tokens_gather(desc: TokensDesc, x, order: TokensOrder, rows, stream=None):
+    """rows[pair_row[t, i]] = x[t]; rows [T * top_k, d_model].  x and rows may have strided rows."""
+    dev, dt, d = _device(x, "x"), desc.torch_dtype, desc.d_model
+    px, ldx = _rows(x, "x", desc.T, d, dt, dev)
+    pr, ldr = _rows(rows, "rows", desc.pairs, d, dt, dev)
+    st = library().twell_tokens_gather(
+        desc._at(ldx, ldr), px, _exactly(order.pair_row, "order.pair_row", (desc.T, desc.top_k), torch.int32, dev), pr,
+        _stream_on(dev, stream))
+    if st:
+        _check("twell_tokens_gather", st)
+
+
+def twell_tokens_combine(desc: TokensDesc, rows, order: TokensOrder, weights, y, stream=None):
+    """y[t] = sum of weights[t, i] rows[pair_row[t, i]]; weights fp32 [T, top_k], or None for ones."""
+    dev, dt, d = _device(rows, "rows"), desc.torch_dtype, desc.d_model
+    shape = (desc.T, desc.top_k)
+    pr, ldr = _rows(rows, "rows", desc.pairs, d, dt, dev)
+    py, ldy = _rows(y, "y", desc.T, d, dt, dev)
+    st = library().twell_tokens_combine(
+        desc._at(ldy, ldr), pr, _exactly(order.pair_row, "order.pair_row", shape, torch.int32, dev),
+        None if weights is None else _exactly(weights, "weights", shape, torch.float32, dev), py,
+        _stream_on(dev, stream))
+    if st:
+        _check("twell_tokens_combine", st)
+
+
+def twell_tokens_combine_bwd(desc: TokensDesc, rows, order: TokensOrder, weights, dy, drows, dweights, stream=None):
+    """Gradients of twell_tokens_combine with weights: drows [T * top_k, d_model] and dweights fp32 [T, top_k], either
+    of them None if it is not wanted (rows may be None without dweights)."""
+    dev, dt, d = _device(dy, "dy"), desc.torch_dtype, desc.d_model
+    shape = (desc.T, desc.top_k)
+    pg, ldg = _rows(dy, "dy", desc.T, d, dt, dev)
+    if rows is None and dweights is not None:
+        raise TypeError("rows: expected a torch.Tensor")
+    pr, ldr = (None, d) if rows is None else _rows(rows, "rows", desc.pairs, d, dt, dev)
+    po, ldo = (None, d) if drows is None else _rows(drows, "drows", desc.pairs, d, dt, dev)
+    st = library().twell_tokens_combine_bwd(
+        desc._at(ldg, ldr), pr, _exactly(order.pair_row, "order.pair_row", shape, torch.int32, dev),
+        _exactly(weights, "weights", shape, torch.float32, dev), pg, po, ldo,
+        None if dweights is None else _exactly(dweights, "dweights", shape, torch.float32, dev),
+        _stream_on(dev, stream))
+    if st:
+        _check("twell_tokens_combine_bwd", st)
+
+
+def _norm_weights(desc: NormDesc, w, b, dev: int) -> tuple:
+    code = TWELL_FP32 if w is None and b is None else _any_dtype(b if w is None else w, "b" if w is None else "w")
+    dtype = torch.bfloat16 if code == TWELL_BF16 else torch.float32
+    return (code, *(None if t is None else _exactly(t, n, (desc.d_model,), dtype, dev) for t, n in ((w, "w"), (b, "b"))))
+
+
+def twell_layernorm_fwd(desc: NormDesc, x, w, b, y, stats=None, stream=None):
+    """y = (x - mean) rstd w + b over each row; w and b [d_model] in one dtype (bf16 or fp32), or None; stats fp32
+    [T, 2] gets mean and rstd for twell_layernorm_bwd.  y may be x."""
+    dev, dt, d = _device(x, "x"), desc.torch_dtype, desc.d_model
+    px, ldx = _rows(x, "x", desc.T, d, dt, dev)
+    py, ldy = _rows(y, "y", desc.T, d, dt, dev)
+    code, pw, pb = _norm_weights(desc, w, b, dev)
+    st = library().twell_layernorm_fwd(
+        desc._at(code, ldx, ldy, d), px, pw, pb, py,
+        None if stats is None else _exactly(stats, "stats", (desc.T, 2), torch.float32, dev), _stream_on(dev, stream))
+    if st:
+        _check("twell_layernorm_fwd", st)
+
+
+def twell_layernorm_bwd(desc: NormDesc, x, w, stats, dy, dx, dw, db, ws, stream=None):
+    """Gradients of twell_layernorm_fwd: dx [T, d_model], dw and db fp32 [d_model] (either may be None), overwritten.
+    dx may be x or dy."""
+    dev, dt, d = _device(x, "x"), desc.torch_dtype, desc.d_model
+    px, ldx = _rows(x, "x", desc.T, d, dt, dev)
+    pg, ldg = _rows(dy, "dy", desc.T, d, dt, dev)
+    po, ldo = _rows(dx, "dx", desc.T, d, dt, dev)
+    code, pw, _ = _norm_weights(desc, w, None, dev)
+    st = library().twell_layernorm_bwd(
+        desc._at(code, ldx, ldg, ldo), px, pw, _exactly(stats, "stats", (desc.T, 2), torch.float32, dev), pg, po,
+        *(None if t is None else _exactly(t, n, (d,), torch.float32, dev) for t, n in ((dw, "dw"), (db, "db"))),
+        _fit(ws, "ws", desc.ws_bytes, torch.uint8, dev), desc.ws_bytes, _stream_on(dev, stream))
+    if st:
+        _check("twell_layernorm_bwd", st)

@@ -376,6 +376,96 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
                            twell_wplanes gate, twell_wplanes up, twell_wplanes down, void* y, int32_t* ids,
                            float* weights, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A mixture-of-experts layer over many tokens, for training and long prompts:
+ * tokens sorted by expert and back with their weights, and layer norm, each
+ * with its gradients.
+ *
+ * As above, odd widths and strided rows: tensors need only the alignment of
+ * their elements (int32 and fp32 arrays 4 bytes, workspaces 16).  Tensors of one
+ * call must not overlap where not said otherwise.  Limits: 2^20 tokens, T x
+ * d_model up to 2^33, 1024 experts, top_k up to 32, strides up to 2^40 elements
+ * (TWELL_EUNSUPPORTED beyond).  T = 0 reads no tensor.  All are deterministic. */
+
+/* T tokens, top_k choices among `experts` each.  A pair p = t * top_k + i is
+ * choice i of token t; there are up to T * top_k sorted rows.  Rows of
+ * token tensors are ld_tokens elements apart, those of row tensors ld_rows. */
+typedef struct {
+  int64_t T;
+  int64_t ld_tokens;
+  int64_t ld_rows;
+  int32_t d_model;
+  int32_t experts;
+  int32_t top_k;
+  int32_t dtype; /* twell_dtype */
+} twell_tokens_desc;
+
+/* Workspace bytes of twell_tokens_sort.  Host only. */
+twell_status twell_tokens_sizes(const twell_tokens_desc* d, size_t* ws);
+
+/* The order of pairs by expert, stable (a lower pair first):
+ *   ids [T x top_k] -> offsets [experts + 1], pair_row [T x top_k]
+ * Rows offsets[e] .. offsets[e + 1] - 1 are expert e's, offsets[0] = 0; row
+ * pair_row[p] belongs to pair p.  A pair whose id is not one of 0 .. experts - 1
+ * is left out: pair_row[p] = -1.  A token may choose an expert twice.  ws: nothing
+ * in it needs to start at zero. */
+twell_status twell_tokens_sort(const twell_tokens_desc* d, const int32_t* ids, int32_t* offsets, int32_t* pair_row,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/* rows[pair_row[p]] = x[p / top_k]: x [T x d_model], rows [T * top_k x d_model].
+ * Rows behind offsets[experts] are left as they are.  Its gradient is
+ * twell_tokens_combine without weights; it is that call's. */
+twell_status twell_tokens_gather(const twell_tokens_desc* d, const void* x, const int32_t* pair_row, void* rows,
+                                 void* stream);
+
+/* y[t] = sum_i weights[t, i] rows[pair_row[t, i]], fp32 sums over ascending i
+ * rounded once.  weights [T x top_k] fp32, or NULL: ones.  A pair left out, and
+ * one whose weight is 0, adds nothing, whatever the row holds. */
+twell_status twell_tokens_combine(const twell_tokens_desc* d, const void* rows, const int32_t* pair_row,
+                                  const float* weights, void* y, void* stream);
+
+/* The gradients of twell_tokens_combine with weights:
+ *   drows[pair_row[t, i]] = weights[t, i] dy[t],  dweights[t, i] = rows[pair_row[t, i]] . dy[t]
+ * dy [T x d_model]; drows like rows, its rows ld_drows apart; dweights [T x top_k]
+ * fp32, 0 for a pair left out.  Either output may be NULL; rows may be NULL
+ * without dweights.  drows may be rows itself (ld_drows = ld_rows).  Rows behind
+ * offsets[experts] are left as they are. */
+twell_status twell_tokens_combine_bwd(const twell_tokens_desc* d, const void* rows, const int32_t* pair_row,
+                                      const float* weights, const void* dy, void* drows, int64_t ld_drows,
+                                      float* dweights, void* stream);
+
+/* Layer norm of T rows of d_model (up to 16384) elements; rows of x are ldx
+ * apart, those of y and dy ldy, those of dx lddx.  dtype: of x, y, dy and dx;
+ * w_dtype: of w and b. */
+typedef struct {
+  int64_t T;
+  int64_t ldx;
+  int64_t ldy;
+  int64_t lddx;
+  int32_t d_model;
+  int32_t dtype;   /* twell_dtype */
+  int32_t w_dtype; /* twell_dtype */
+  float eps;       /* >= 0 */
+} twell_norm_desc;
+
+/* Workspace bytes of twell_layernorm_bwd.  Host only. */
+twell_status twell_layernorm_sizes(const twell_norm_desc* d, size_t* ws);
+
+/* y = (x - mean) rstd w + b, rstd = 1 / sqrt(mean((x - mean)^2) + eps), over each
+ * row; fp32 sums.  w [d_model] or NULL: ones; b [d_model] or NULL: zeros.  stats
+ * [T x 2] fp32 gets mean and rstd of each row for the backward call; may be NULL.
+ * y may be x itself (ldy = ldx). */
+twell_status twell_layernorm_fwd(const twell_norm_desc* d, const void* x, const void* w, const void* b, void* y,
+                                 float* stats, void* stream);
+
+/* With h = (x - mean) rstd and g = dy w:
+ *   dx = rstd (g - mean(g) - h mean(g h)),  dw = sum_t dy h,  db = sum_t dy
+ * dx [T x d_model] is overwritten, and may be x or dy itself (same stride); dw and db
+ * [d_model] fp32 are overwritten (zeros for T = 0); either may be NULL. */
+twell_status twell_layernorm_bwd(const twell_norm_desc* d, const void* x, const void* w, const float* stats,
+                                 const void* dy, void* dx, float* dw, float* db, void* ws, size_t ws_bytes,
+                                 void* stream);
+
 /* Static description of a status code. */
 const char* twell_status_str(twell_status s);
 
