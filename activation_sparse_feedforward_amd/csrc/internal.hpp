@@ -262,6 +262,41 @@ struct NormArgs {
 };
 int norm_blocks(int64_t T);
 
+// Weights in e4m3 (fp8.hpp): E matrices of N rows x K inputs, and transposed.
+struct F8PackArgs {
+  const void* w;  // packing
+  void* out;      // unpacking
+  uint8_t *codes, *scales;
+  uint8_t *codes_t, *scales_t;  // of K rows x N inputs, or null
+  int32_t experts, N, K;
+  int32_t tiles, blocks, quads;        // ceil(N / 16), ceil(K / 128), ceil(blocks / 4)
+  int32_t tiles_t, blocks_t, quads_t;  // of the transposed matrix
+};
+// Rows [T x K] to e4m3, the tiles of 16 of each expert behind one another.
+struct F8RowsArgs {
+  const void* x;
+  uint8_t *codes, *scales;
+  const int32_t* offsets;  // [experts + 1], or null: one expert with all rows
+  int64_t T, ldx, most_tiles;  // most_tiles: of 16 rows that codes and scales hold
+  int32_t K, blocks, quads, experts;
+};
+// y [T x N] = rows times their expert's weights.
+struct F8GemmArgs {
+  const uint8_t *w_codes, *w_scales, *x_codes, *x_scales;
+  void* y;
+  const int32_t* offsets;
+  int64_t T, ldy, most_tiles;
+  int32_t N, tiles, blocks, quads, experts;
+};
+// dw [experts][N x K] = dy^T x over each expert's rows.
+struct WgradArgs {
+  const void *x, *dy;
+  float* dw;
+  const int32_t* offsets;
+  int64_t T, ldx, ldy;
+  int32_t N, K, experts;
+};
+
 // dtype: 0 = fp32, 1 = bf16.  Each returns hipSuccess or the launch error.
 hipError_t launch_gate_pack(const PackArgs& a, int dtype, hipStream_t s);
 hipError_t launch_fused_updown(const FusedArgs& a, int dtype, hipStream_t s);
@@ -286,6 +321,11 @@ hipError_t launch_weights_pack(const WeightsArgs& a, int dtype, bool transposed,
 hipError_t launch_weights_unpack(const WeightsArgs& a, int dtype, hipStream_t s);
 hipError_t launch_linear4(const LinearArgs& a, int dtype, hipStream_t s);
 hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t s);
+hipError_t launch_f8_pack(const F8PackArgs& a, int dtype, hipStream_t s);
+hipError_t launch_f8_unpack(const F8PackArgs& a, int dtype, hipStream_t s);
+hipError_t launch_f8_rows(const F8RowsArgs& a, int dtype, hipStream_t s);
+hipError_t launch_f8_gemm(const F8GemmArgs& a, int dtype, hipStream_t s);
+hipError_t launch_wgrad(const WgradArgs& a, int dtype, hipStream_t s);
 hipError_t launch_tokens_sort(TokensSortArgs a, hipStream_t s);
 hipError_t launch_tokens_gather(const TokensArgs& a, int dtype, hipStream_t s);
 hipError_t launch_tokens_combine(const TokensArgs& a, int dtype, hipStream_t s);

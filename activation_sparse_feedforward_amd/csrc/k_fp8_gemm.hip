@@ -1,0 +1,212 @@
+// y = Q(x) Q(W)^T: rows and weights in e4m3 (fp8.hpp), one matrix or one per
+// expert over sorted rows.
+#include "fp8.hpp"
+#include "launch.hpp"
+#include "rows.hpp"
+
+namespace twell {
+namespace {
+
+// A fragment: one lane's 32 codes.
+struct F8Frag {
+  u32x4_t v[2];
+  __device__ __forceinline__ void read(const uint8_t* block, int lane) {
+    v[0] = *reinterpret_cast<const u32x4_t*>(block + lane * 16);
+    v[1] = *reinterpret_cast<const u32x4_t*>(block + 1024 + lane * 16);
+  }
+};
+
+// acc += a b over 128 inputs, w = weights (rows of the result), x = tokens
+// (columns).  sw, sx: scale bytes in bits 0..7.
+__device__ __forceinline__ void f8_mfma(f32x4_t& acc, const F8Frag& w, uint32_t sw, const F8Frag& x, uint32_t sx) {
+  i32x8_t a, b;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = static_cast<int>(w.v[i / 4][i % 4]);
+    b[i] = static_cast<int>(x.v[i / 4][i % 4]);
+  }
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, static_cast<int>(sw), 0,
+                                                         static_cast<int>(sx));
+}
+
+// The codes as bf16 values, scales and all: exact, but below 2^-126.
+struct Bf16Frag {
+  bf16x8_t v[4];
+  __device__ __forceinline__ void from(const F8Frag& f, uint32_t byte) {
+    const float scale = f8_scale(byte & 255u);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t c = f.v[s / 2][2 * (s % 2) + i / 2];
+        const bf16x2_t p = i % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, scale, true)
+                                 : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, scale, false);
+        v[s][2 * i] = p[0];
+        v[s][2 * i + 1] = p[1];
+      }
+  }
+};
+__device__ __forceinline__ void bf16_mfma(f32x4_t& acc, const Bf16Frag& w, const Bf16Frag& x) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[s], x.v[s], acc, 0, 0, 0);
+}
+
+// Register r of lane l of an accumulator: weight row 4 (l / 16) + r, token l % 16.
+template <class E>
+__device__ __forceinline__ void store_acc(const F8GemmArgs& a, int64_t row, int n, const f32x4_t& acc) {
+  using S = typename E::storage;
+  S* y = static_cast<S*>(a.y) + row * a.ldy + n;
+  if (n + 4 <= a.N) {
+    if constexpr (E::kBytes == 2) {
+      typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
+      *reinterpret_cast<u32x2_any_t*>(y) = u32x2_any_t{bf16_pair(acc[0], acc[1]), bf16_pair(acc[2], acc[3])};
+    } else {
+      store16(y, __builtin_bit_cast(u32x4_t, acc));
+    }
+    return;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (n + r < a.N) {
+      if constexpr (E::kBytes == 2) y[r] = static_cast<uint16_t>(bf16_pair(acc[r], 0.f));
+      else y[r] = acc[r];
+    }
+}
+
+// Tiles of (WW x 16 FW) weight rows x (WX x 16 FX) tokens, WW x WX waves.  Both
+// operands go to LDS with direct 16-byte loads, two stages of one block (128
+// inputs): the loads of the next block fly while this one is multiplied.
+template <int WW, int WX, int FW, int FX>
+struct F8Tile {
+  static constexpr int kWaves = WW * WX;
+  static constexpr int kTilesW = WW * FW, kTilesX = WX * FX;
+  static constexpr int kN = 16 * kTilesW, kM = 16 * kTilesX;
+  static constexpr int kStage = (kTilesW + kTilesX) * kF8Bytes;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kLoads = 2 * (kTilesW + kTilesX) / kWaves;  // 1 KB each, of a wave
+};
+
+template <class E, int WW, int WX, int FW, int FX>
+__global__ __launch_bounds__(WW* WX* kWave) void f8_gemm_kernel(F8GemmArgs a) {
+  using Tile = F8Tile<WW, WX, FW, FX>;
+  extern __shared__ __align__(16) uint8_t lds_tiles[];
+  constexpr bool kExact = E::kBytes == 4;  // fp32 results: see launch_f8_gemm
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // groups of 8 token tiles, all weight tiles of a group in a row
+  const int nt = (a.tiles + Tile::kTilesW - 1) / Tile::kTilesW;
+  const int id = xcd_run(blockIdx.x, gridDim.x);
+  const int mts = gridDim.x / nt, group = id / (8 * nt), first = group * 8, size = min(8, mts - first);
+  const int in = id - group * 8 * nt, mt = first + in % size, tn = in / size;
+  const F8Place p = f8_locate(a.offsets, a.experts, a.T, Tile::kM, mt);
+  if (p.expert < 0 || p.tile16 + min(p.tiles16, Tile::kTilesX) > a.most_tiles) return;
+
+  const uint8_t* wcodes = a.w_codes + static_cast<int64_t>(p.expert) * a.tiles * a.blocks * kF8Bytes;
+  const uint8_t* wscales = a.w_scales + static_cast<int64_t>(p.expert) * a.tiles * a.quads * kF8Scales;
+  const uint8_t* xcodes = a.x_codes + p.tile16 * a.blocks * kF8Bytes;
+  const uint8_t* xscales = a.x_scales + p.tile16 * a.quads * kF8Scales;
+  const int w0 = tn * Tile::kTilesW;
+  // tiles past the matrix or the expert's rows are the last one again; their results are not stored
+  auto w_tile = [&](int i) { return static_cast<int64_t>(min(w0 + i, a.tiles - 1)); };
+  auto x_tile = [&](int i) { return static_cast<int64_t>(min(i, p.tiles16 - 1)); };
+
+  const uint8_t* from[Tile::kLoads];
+#pragma unroll
+  for (int q = 0; q < Tile::kLoads; ++q) {
+    const int half = wave * Tile::kLoads + q, t = half >> 1;
+    const uint8_t* src = t < Tile::kTilesW ? wcodes + w_tile(t) * a.blocks * kF8Bytes
+                                           : xcodes + x_tile(t - Tile::kTilesW) * a.blocks * kF8Bytes;
+    from[q] = src + (half & 1) * 1024 + lane * 16;
+  }
+  auto issue = [&](int kb, uint8_t* stage) {
+#pragma unroll
+    for (int q = 0; q < Tile::kLoads; ++q)
+      direct16(from[q] + static_cast<int64_t>(kb) * kF8Bytes, stage + (wave * Tile::kLoads + q) * 1024);
+  };
+
+  const int fw0 = (wave / WX) * FW, fx0 = (wave % WX) * FX;
+  f32x4_t acc[FW][FX];
+#pragma unroll
+  for (int i = 0; i < FW; ++i)
+#pragma unroll
+    for (int j = 0; j < FX; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint32_t sw[FW], sx[FX];
+  issue(0, lds_tiles);
+  for (int kb = 0; kb < a.blocks; ++kb) {
+    const uint8_t* stage = lds_tiles + (kb & 1) * Tile::kStage;
+    if ((kb & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < FW; ++i)
+        sw[i] = *reinterpret_cast<const uint32_t*>(wscales + (w_tile(fw0 + i) * a.quads + (kb >> 2)) * kF8Scales +
+                                                   (lane & 15) * 4);
+#pragma unroll
+      for (int j = 0; j < FX; ++j)
+        sx[j] = *reinterpret_cast<const uint32_t*>(xscales + (x_tile(fx0 + j) * a.quads + (kb >> 2)) * kF8Scales +
+                                                   (lane & 15) * 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < FW; ++i) sw[i] >>= 8;
+#pragma unroll
+      for (int j = 0; j < FX; ++j) sx[j] >>= 8;
+    }
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kb + 1 < a.blocks) issue(kb + 1, lds_tiles + ((kb + 1) & 1) * Tile::kStage);
+    F8Frag x[FX];
+#pragma unroll
+    for (int j = 0; j < FX; ++j) x[j].read(stage + (Tile::kTilesW + fx0 + j) * kF8Bytes, lane);
+    if constexpr (kExact) {
+      Bf16Frag xb[FX];
+#pragma unroll
+      for (int j = 0; j < FX; ++j) xb[j].from(x[j], sx[j]);
+#pragma unroll
+      for (int i = 0; i < FW; ++i) {
+        F8Frag w;
+        w.read(stage + (fw0 + i) * kF8Bytes, lane);
+        Bf16Frag wb;
+        wb.from(w, sw[i]);
+#pragma unroll
+        for (int j = 0; j < FX; ++j) bf16_mfma(acc[i][j], wb, xb[j]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < FW; ++i) {
+        F8Frag w;
+        w.read(stage + (fw0 + i) * kF8Bytes, lane);
+#pragma unroll
+        for (int j = 0; j < FX; ++j) f8_mfma(acc[i][j], w, sw[i], x[j], sx[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < FX; ++j) {
+    const int r = (fx0 + j) * 16 + (lane & 15);
+    if (r >= p.rows) continue;
+#pragma unroll
+    for (int i = 0; i < FW; ++i) {
+      const int n = (w0 + fw0 + i) * 16 + 4 * (lane >> 4);
+      if (n < a.N) store_acc<E>(a, p.row0 + r, n, acc[i][j]);
+    }
+  }
+}
+
+template <class E, int WW, int WX, int FW, int FX>
+hipError_t go_tile(const F8GemmArgs& a, hipStream_t s) {
+  using Tile = F8Tile<WW, WX, FW, FX>;
+  const int64_t nt = (a.tiles + Tile::kTilesW - 1) / Tile::kTilesW;
+  const int64_t mt = a.offsets ? a.T / Tile::kM + a.experts : (a.T + Tile::kM - 1) / Tile::kM;
+  return launch_lds<&f8_gemm_kernel<E, WW, WX, FW, FX>, Tile::kLds>(
+      dim3(static_cast<unsigned>(nt * mt)), Tile::kWaves * kWave, Tile::kLds, s, a);
+}
+
+}  // namespace
+
+// bf16 results: the matrix core multiplies the codes.  It cuts the products of 8
+// consecutive inputs to multiples of 2^-13 of the largest one's power of two and
+// adds them in fp32, so a sum is off by less than 7 * 2^-13 of the largest product
+// of each 8 (1.35e-5 of its norm for Gaussian data); a code's own rounding is 2^-4,
+// the result's 2^-8.  fp32 results have the same codes multiplied as bf16 values,
+// exactly, with fp32 sums, at half the rate or less.
+hipError_t launch_f8_gemm(const F8GemmArgs& a, int dtype, hipStream_t s) {
+  return dtype == 1 ? go_tile<EBf16, 2, 2, 4, 4>(a, s) : go_tile<EF32, 2, 2, 4, 4>(a, s);
+}
+
+}  // namespace twell

@@ -273,6 +273,99 @@ twell::NormArgs norm_args(const twell_norm_desc* d) {
   return a;
 }
 
+twell_status check_fp8(const twell_fp8_desc* d) {
+  if (!d || d->experts <= 0 || d->rows <= 0 || d->cols <= 0) return TWELL_EINVAL;
+  if (d->experts > twell::kMoeMaxExperts || d->rows > kMaxSide || d->cols > kMaxSide) return TWELL_EUNSUPPORTED;
+  if (static_cast<int64_t>(d->rows) * d->cols > kMaxMatrix) return TWELL_EUNSUPPORTED;
+  return TWELL_OK;
+}
+twell_status check_fp8_planes(const twell_wplanes& p) {
+  return p.codes && p.scales && aligned16(p.codes) && aligned16(p.scales) ? TWELL_OK : TWELL_EINVAL;
+}
+int32_t quads_of(int32_t blocks) { return (blocks + 3) / 4; }
+twell_fp8_desc transposed(const twell_fp8_desc* d) { return {d->experts, d->cols, d->rows}; }
+
+twell::F8PackArgs fp8_pack_args(const twell_fp8_desc* d, const twell_wplanes& p) {
+  twell::F8PackArgs a{};
+  a.codes = static_cast<uint8_t*>(p.codes);
+  a.scales = static_cast<uint8_t*>(p.scales);
+  a.experts = d->experts;
+  a.N = d->rows;
+  a.K = d->cols;
+  a.tiles = tiles_of(d->rows);
+  a.blocks = blocks_of(d->cols);
+  a.quads = quads_of(a.blocks);
+  a.tiles_t = tiles_of(d->cols);
+  a.blocks_t = blocks_of(d->rows);
+  a.quads_t = quads_of(a.blocks_t);
+  return a;
+}
+
+// What a call with T rows asks of T, offsets and the rows' tensors.
+constexpr int64_t kMaxProduct = int64_t(1) << 37;  // rows x width of a result: what the grid of one launch reaches
+twell_status check_fp8_rows(const twell_fp8_desc* d, int64_t T, const int32_t* offsets, int32_t dtype) {
+  TWELL_TRY(check_fp8(d));
+  if (T < 0 || !known_dtype(dtype) || !aligned4(offsets) || (!offsets && d->experts != 1)) return TWELL_EINVAL;
+  if (T > kMaxSide || T * d->rows > kMaxProduct || T * d->cols > kMaxProduct) return TWELL_EUNSUPPORTED;
+  return TWELL_OK;
+}
+twell_status check_stride(int64_t ld, int64_t width) {
+  return ld < width ? TWELL_EINVAL : ld > kMaxStride ? TWELL_EUNSUPPORTED : TWELL_OK;
+}
+
+// Workspace of a product: the codes and scales of T rows of `cols` inputs, whose
+// tiles of 16 begin anew for each expert.
+struct Fp8Ws {
+  int64_t most_tiles;
+  size_t codes, scales, total;
+};
+Fp8Ws fp8_ws(const twell_fp8_desc* d, int64_t T) {
+  Fp8Ws w{};
+  const size_t blocks = static_cast<size_t>(blocks_of(d->cols));
+  w.most_tiles = T / 16 + d->experts;
+  w.codes = 0;
+  w.scales = static_cast<size_t>(w.most_tiles) * blocks * 2048;
+  w.total = align256(w.scales + static_cast<size_t>(w.most_tiles) * ((blocks + 3) / 4) * 64);
+  return w;
+}
+
+// y = Q(x) W^T, arguments checked.
+twell_status fp8_product(const twell_fp8_desc* d, const twell_wplanes& p, int64_t T, const int32_t* offsets,
+                         int32_t dtype, const void* x, int64_t ldx, void* y, int64_t ldy, void* ws, hipStream_t s) {
+  const Fp8Ws w = fp8_ws(d, T);
+  const int32_t blocks = blocks_of(d->cols);
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  twell::F8RowsArgs r{};
+  r.x = x;
+  r.codes = wsb + w.codes;
+  r.scales = wsb + w.scales;
+  r.offsets = offsets;
+  r.T = T;
+  r.ldx = ldx;
+  r.most_tiles = w.most_tiles;
+  r.K = d->cols;
+  r.blocks = blocks;
+  r.quads = quads_of(blocks);
+  r.experts = d->experts;
+  TWELL_TRY(from_hip(twell::launch_f8_rows(r, dtype, s)));
+  twell::F8GemmArgs g{};
+  g.w_codes = static_cast<const uint8_t*>(p.codes);
+  g.w_scales = static_cast<const uint8_t*>(p.scales);
+  g.x_codes = r.codes;
+  g.x_scales = r.scales;
+  g.y = y;
+  g.offsets = offsets;
+  g.T = T;
+  g.ldy = ldy;
+  g.most_tiles = w.most_tiles;
+  g.N = d->rows;
+  g.tiles = tiles_of(d->rows);
+  g.blocks = blocks;
+  g.quads = r.quads;
+  g.experts = d->experts;
+  return from_hip(twell::launch_f8_gemm(g, dtype, s));
+}
+
 }  // namespace
 
 namespace twell {
@@ -878,6 +971,104 @@ twell_status twell_layernorm_bwd(const twell_norm_desc* d, const void* x, const 
   a.db = db;
   a.part = static_cast<float*>(ws);
   return from_hip(twell::launch_norm_bwd(a, d->dtype, d->w_dtype, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_fp8_weights_sizes(const twell_fp8_desc* d, twell_wsizes_t* out) {
+  TWELL_TRY(check_fp8(d));
+  if (!out) return TWELL_EINVAL;
+  const size_t tiles = static_cast<size_t>(d->experts) * static_cast<size_t>(tiles_of(d->rows));
+  const int32_t blocks = blocks_of(d->cols);
+  out->codes = tiles * static_cast<size_t>(blocks) * 2048;
+  out->scales = tiles * static_cast<size_t>(quads_of(blocks)) * 64;
+  return TWELL_OK;
+}
+
+twell_status twell_fp8_weights_pack(const twell_fp8_desc* d, const void* w, int32_t w_dtype, twell_wplanes out,
+                                    const twell_wplanes* out_t, void* stream) {
+  TWELL_TRY(check_fp8(d));
+  if (!known_dtype(w_dtype)) return TWELL_EINVAL;
+  TWELL_TRY(check_elems(w, w_dtype));
+  TWELL_TRY(check_fp8_planes(out));
+  twell::F8PackArgs a = fp8_pack_args(d, out);
+  a.w = w;
+  if (out_t) {
+    TWELL_TRY(check_fp8_planes(*out_t));
+    a.codes_t = static_cast<uint8_t*>(out_t->codes);
+    a.scales_t = static_cast<uint8_t*>(out_t->scales);
+  }
+  return from_hip(twell::launch_f8_pack(a, w_dtype, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_fp8_weights_unpack(const twell_fp8_desc* d, twell_wplanes in, void* w, int32_t w_dtype,
+                                      void* stream) {
+  TWELL_TRY(check_fp8(d));
+  if (!known_dtype(w_dtype)) return TWELL_EINVAL;
+  TWELL_TRY(check_elems(w, w_dtype));
+  TWELL_TRY(check_fp8_planes(in));
+  twell::F8PackArgs a = fp8_pack_args(d, in);
+  a.out = w;
+  return from_hip(twell::launch_f8_unpack(a, w_dtype, static_cast<hipStream_t>(stream)));
+}
+
+twell_status twell_fp8_linear_sizes(const twell_fp8_desc* d, int64_t T, size_t* ws_fwd, size_t* ws_bwd) {
+  TWELL_TRY(check_fp8(d));
+  if (T < 0 || !ws_fwd || !ws_bwd) return TWELL_EINVAL;
+  if (T > kMaxSide) return TWELL_EUNSUPPORTED;
+  const twell_fp8_desc t = transposed(d);
+  *ws_fwd = fp8_ws(d, T).total;
+  *ws_bwd = fp8_ws(&t, T).total;
+  return TWELL_OK;
+}
+
+twell_status twell_fp8_linear_fwd(const twell_fp8_desc* d, twell_wplanes w, int64_t T, const int32_t* offsets,
+                                  int32_t dtype, const void* x, int64_t ldx, void* y, int64_t ldy, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  TWELL_TRY(check_fp8_rows(d, T, offsets, dtype));
+  TWELL_TRY(check_stride(ldx, d->cols));
+  TWELL_TRY(check_stride(ldy, d->rows));
+  if (T == 0) return TWELL_OK;
+  TWELL_TRY(check_elems(x, dtype));
+  TWELL_TRY(check_elems(y, dtype));
+  TWELL_TRY(check_fp8_planes(w));
+  if (!ws || !aligned16(ws) || ws_bytes < fp8_ws(d, T).total) return TWELL_EINVAL;
+  return fp8_product(d, w, T, offsets, dtype, x, ldx, y, ldy, ws, static_cast<hipStream_t>(stream));
+}
+
+twell_status twell_fp8_linear_bwd(const twell_fp8_desc* d, twell_wplanes w_t, int64_t T, const int32_t* offsets,
+                                  int32_t dtype, const void* x, int64_t ldx, const void* dy, int64_t lddy, void* dx,
+                                  int64_t lddx, float* dw, void* ws, size_t ws_bytes, void* stream) {
+  TWELL_TRY(check_fp8_rows(d, T, offsets, dtype));
+  TWELL_TRY(check_stride(lddy, d->rows));
+  if (dw) TWELL_TRY(check_stride(ldx, d->cols));
+  if (dx) TWELL_TRY(check_stride(lddx, d->cols));
+  if (dw && !aligned4(dw)) return TWELL_EINVAL;
+  const twell_fp8_desc t = transposed(d);
+  if (T > 0 && (dx || dw)) {
+    TWELL_TRY(check_elems(dy, dtype));
+    if (dw) TWELL_TRY(check_elems(x, dtype));
+    if (dx) {
+      TWELL_TRY(check_elems(dx, dtype));
+      TWELL_TRY(check_fp8_planes(w_t));
+      if (!ws || !aligned16(ws) || ws_bytes < fp8_ws(&t, T).total) return TWELL_EINVAL;
+    }
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dw) {
+    twell::WgradArgs a{};
+    a.x = x;
+    a.dy = dy;
+    a.dw = dw;
+    a.offsets = T > 0 ? offsets : nullptr;
+    a.T = T;
+    a.ldx = ldx;
+    a.ldy = lddy;
+    a.N = d->rows;
+    a.K = d->cols;
+    a.experts = d->experts;
+    TWELL_TRY(from_hip(twell::launch_wgrad(a, dtype, s)));
+  }
+  if (!dx || T == 0) return TWELL_OK;
+  return fp8_product(&t, w_t, T, offsets, dtype, dy, lddy, dx, lddx, ws, s);
 }
 
 const char* twell_status_str(twell_status s) {

@@ -30,7 +30,8 @@ EXPORTED = ("twell_sizes", "twell_pack", "twell_pack_classic", "twell_ffn_fwd", 
             "twell_weights_sizes", "twell_weights_pack", "twell_weights_unpack", "twell_linear_fwd",
             "twell_moe_sizes", "twell_moe_fwd", "twell_tokens_sizes", "twell_tokens_sort", "twell_tokens_gather",
             "twell_tokens_combine", "twell_tokens_combine_bwd", "twell_layernorm_sizes", "twell_layernorm_fwd",
-            "twell_layernorm_bwd")
+            "twell_layernorm_bwd", "twell_fp8_weights_sizes", "twell_fp8_weights_pack", "twell_fp8_weights_unpack",
+            "twell_fp8_linear_sizes", "twell_fp8_linear_fwd", "twell_fp8_linear_bwd")
 
 
 class TwellError(RuntimeError):
@@ -85,6 +86,10 @@ class CTokensDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class CFp8Desc(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32)]
+
+
 class CNormDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("lddx", ctypes.c_int64),
                 ("d_model", ctypes.c_int32), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
@@ -129,6 +134,13 @@ def library() -> ctypes.CDLL:
             "twell_layernorm_sizes": (ST, [ctypes.POINTER(CNormDesc), ctypes.POINTER(SZ)]),
             "twell_layernorm_fwd": (ST, [ctypes.POINTER(CNormDesc), P, P, P, P, P, P]),
             "twell_layernorm_bwd": (ST, [ctypes.POINTER(CNormDesc), P, P, P, P, P, P, P, P, SZ, P]),
+            "twell_fp8_weights_sizes": (ST, [ctypes.POINTER(CFp8Desc), ctypes.POINTER(CWSizes)]),
+            "twell_fp8_weights_pack": (ST, [ctypes.POINTER(CFp8Desc), P, I32, CPlanes, ctypes.POINTER(CPlanes), P]),
+            "twell_fp8_weights_unpack": (ST, [ctypes.POINTER(CFp8Desc), CPlanes, P, I32, P]),
+            "twell_fp8_linear_sizes": (ST, [ctypes.POINTER(CFp8Desc), I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]),
+            "twell_fp8_linear_fwd": (ST, [ctypes.POINTER(CFp8Desc), CPlanes, I64, P, I32, P, I64, P, I64, P, SZ, P]),
+            "twell_fp8_linear_bwd": (ST, [ctypes.POINTER(CFp8Desc), CPlanes, I64, P, I32, P, I64, P, I64, P, I64, P, P,
+                                          SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -877,3 +889,140 @@ def twell_layernorm_bwd(desc: NormDesc, x, w, stats, dy, dx, dw, db, ws, stream=
         _fit(ws, "ws", desc.ws_bytes, torch.uint8, dev), desc.ws_bytes, _stream_on(dev, stream))
     if st:
         _check("twell_layernorm_bwd", st)
+
+
+@dataclass(frozen=True)
+class Fp8Desc(_Keeping):
+    """``experts`` matrices of ``rows`` outputs x ``cols`` inputs in 8-bit floating point, a scale for 128 x 128."""
+    experts: int
+    rows: int
+    cols: int
+
+    @functools.cached_property
+    def transposed(self) -> "Fp8Desc":
+        return Fp8Desc(self.experts, self.cols, self.rows)
+
+    @functools.cached_property
+    def _ref(self):
+        return ctypes.byref(CFp8Desc(**_c_ints(32, experts=self.experts, rows=self.rows, cols=self.cols)))
+
+    @functools.cached_property
+    def plane_bytes(self) -> tuple:
+        """Bytes of the planes (codes, scales)."""
+        out = CWSizes()
+        _check("twell_fp8_weights_sizes", library().twell_fp8_weights_sizes(self._ref, ctypes.byref(out)))
+        return int(out.codes), int(out.scales)
+
+
+@functools.lru_cache(maxsize=1024)
+def _fp8_ws(desc: Fp8Desc, T: int) -> tuple:
+    fwd, bwd = ctypes.c_size_t(), ctypes.c_size_t()
+    _c_ints(64, T=T)
+    _check("twell_fp8_linear_sizes",
+           library().twell_fp8_linear_sizes(desc._ref, T, ctypes.byref(fwd), ctypes.byref(bwd)))
+    return int(fwd.value), int(bwd.value)
+
+
+def fp8_ws_bytes(desc: Fp8Desc, T: int) -> int:
+    """Bytes of a workspace that does for twell_fp8_linear_fwd and _bwd with T rows."""
+    return max(_fp8_ws(desc, T))
+
+
+def alloc_fp8_weights(desc: Fp8Desc, device="cuda") -> Weights:
+    codes, scales = desc.plane_bytes
+    return Weights(torch.empty(codes, dtype=_CODE_DTYPE, device=device),
+                   torch.empty(scales, dtype=torch.uint8, device=device))
+
+
+def alloc_fp8_ws(desc: Fp8Desc, T: int, device="cuda") -> torch.Tensor:
+    return torch.empty(fp8_ws_bytes(desc, T), dtype=torch.uint8, device=device)
+
+
+def _fp8_planes(desc: Fp8Desc, w: Weights, name: str, dev: int) -> CPlanes:
+    codes, scales = desc.plane_bytes
+    return CPlanes(_fit(w.codes, name + ".codes", codes, torch.uint8, dev),
+                   _fit(w.scales, name + ".scales", scales, torch.uint8, dev))
+
+
+def _offsets(desc: Fp8Desc, offsets, dev: int):
+    if offsets is None:
+        if desc.experts != 1:
+            raise ValueError(f"offsets: needed with {desc.experts} experts")
+        return None
+    return _exactly(offsets, "offsets", (desc.experts + 1,), torch.int32, dev)
+
+
+def _two_axes(t, name: str, width: int) -> int:
+    """How many rows of ``width`` elements a tensor has."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {('T', width)}")
+    return t.shape[0]
+
+
+def twell_fp8_weights_pack(desc: Fp8Desc, w, planes: Weights, planes_t: Optional[Weights] = None, stream=None):
+    """Round w [experts, rows, cols] (bf16 or fp32; a flat one is taken in that order) to 8-bit planes; planes_t, of
+    desc.transposed, gets the transposed matrices."""
+    code = _any_dtype(w, "w")
+    dev = _device(w, "w")
+    _shaped(w, "w", (desc.experts, desc.rows, desc.cols))
+    n = desc.experts * desc.rows * desc.cols * w.element_size()
+    pt = None if planes_t is None else ctypes.byref(_fp8_planes(desc.transposed, planes_t, "planes_t", dev))
+    st = library().twell_fp8_weights_pack(desc._ref, _fit(w, "w", n, w.dtype, dev), code,
+                                          _fp8_planes(desc, planes, "planes", dev), pt, _stream_on(dev, stream))
+    if st:
+        _check("twell_fp8_weights_pack", st)
+
+
+def twell_fp8_weights_unpack(desc: Fp8Desc, planes: Weights, w, stream=None):
+    """Write the values that planes stand for to w [experts, rows, cols] (bf16 or fp32; flat will do)."""
+    code = _any_dtype(w, "w")
+    dev = _device(w, "w")
+    _shaped(w, "w", (desc.experts, desc.rows, desc.cols))
+    n = desc.experts * desc.rows * desc.cols * w.element_size()
+    st = library().twell_fp8_weights_unpack(desc._ref, _fp8_planes(desc, planes, "planes", dev),
+                                            _fit(w, "w", n, w.dtype, dev), code, _stream_on(dev, stream))
+    if st:
+        _check("twell_fp8_weights_unpack", st)
+
+
+def twell_fp8_linear_fwd(desc: Fp8Desc, planes: Weights, x, y, ws, offsets=None, stream=None):
+    """y [T, rows] = x [T, cols], rounded to 8 bits on the way, times the matrix, or each row's expert's: rows
+    offsets[e] .. offsets[e + 1] - 1 are expert e's (see include/twell.h).  x and y may have strided rows."""
+    code = _any_dtype(x, "x")
+    T, dev = _two_axes(x, "x", desc.cols), _device(x, "x")
+    px, ldx = _rows(x, "x", T, desc.cols, x.dtype, dev)
+    py, ldy = _rows(y, "y", T, desc.rows, x.dtype, dev)
+    need = _fp8_ws(desc, T)[0]
+    st = library().twell_fp8_linear_fwd(desc._ref, _fp8_planes(desc, planes, "planes", dev), T,
+                                        _offsets(desc, offsets, dev), code, px, ldx, py, ldy,
+                                        _fit(ws, "ws", need, torch.uint8, dev), need, _stream_on(dev, stream))
+    if st:
+        _check("twell_fp8_linear_fwd", st)
+
+
+def twell_fp8_linear_bwd(desc: Fp8Desc, planes_t: Optional[Weights], x, dy, dx, dw, ws, offsets=None, stream=None):
+    """Gradients of twell_fp8_linear_fwd: dx [T, cols] through planes_t (of desc.transposed) and dw fp32 [experts, rows,
+    cols] from x and dy, overwritten; either may be None (then what it alone needs may be too)."""
+    code = _any_dtype(dy, "dy")
+    T, dev, d = _two_axes(dy, "dy", desc.rows), _device(dy, "dy"), desc.cols
+    pg, ldg = _rows(dy, "dy", T, desc.rows, dy.dtype, dev)
+    if x is None and dw is not None:
+        raise TypeError("x: expected a torch.Tensor")
+    px, ldx = (None, d) if x is None else _rows(x, "x", T, d, dy.dtype, dev)
+    po, ldo, need, pws, planes = None, d, 0, None, CPlanes(None, None)
+    if dx is not None:
+        if planes_t is None:
+            raise TypeError("planes_t: expected Weights")
+        po, ldo = _rows(dx, "dx", T, d, dy.dtype, dev)
+        need = _fp8_ws(desc, T)[1]
+        pws, planes = _fit(ws, "ws", need, torch.uint8, dev), _fp8_planes(desc.transposed, planes_t, "planes_t", dev)
+    pw = None
+    if dw is not None:
+        _shaped(dw, "dw", (desc.experts, desc.rows, d))
+        pw = _fit(dw, "dw", desc.experts * desc.rows * d * 4, torch.float32, dev)
+    st = library().twell_fp8_linear_bwd(desc._ref, planes, T, _offsets(desc, offsets, dev), code, px, ldx, pg, ldg, po,
+                                        ldo, pw, pws, need, _stream_on(dev, stream))
+    if st:
+        _check("twell_fp8_linear_bwd", st)

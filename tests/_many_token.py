@@ -84,3 +84,63 @@ def capture(fn):
         fn()
     torch.cuda.synchronize()
     return g
+
+
+# ----------------------------------------------------------------------------- 8-bit floating point
+E4M3 = np.array([(m / 8 if e == 0 else 1 + m / 8) * 2.0 ** (max(e, 1) - 7) for e in range(16) for m in range(8)][:127])
+
+
+def e4m3_nearest(v):
+    """The nearest of e4m3's values to each |v| <= 448, ties to the even code; NaN stays."""
+    a = np.abs(np.where(np.isnan(v), 0, v))
+    hi = np.clip(np.searchsorted(E4M3, a), 1, 126)
+    lo = hi - 1
+    d = (a - E4M3[lo]) - (E4M3[hi] - a)
+    code = np.where((d < 0) | ((d == 0) & (lo % 2 == 0)), lo, hi)
+    return np.where(np.isnan(v), np.nan, np.copysign(E4M3[code], v))
+
+
+def e4m3_scale(most):
+    """The smallest power of two from 2^-126 on that takes magnitudes up to `most` to 448 or less."""
+    s = np.full(np.shape(most), 2.0 ** -126)
+    for e in range(-125, 121):
+        s = np.where(most > 448 * s, 2.0 ** e, s)
+    return s
+
+
+def _finite(v):
+    return np.where(np.isfinite(v), v, np.nan)
+
+
+def e4m3_rows(x):
+    """What rows stand for, a scale for each 128 of a row."""
+    out = np.empty_like(x)
+    for b in range(0, x.shape[1], 128):
+        p = _finite(x[:, b:b + 128])
+        s = e4m3_scale(np.abs(np.where(np.isnan(p), 0, p)).max(1, keepdims=True))
+        out[:, b:b + 128] = e4m3_nearest(p / s) * s
+    return out
+
+
+def e4m3_weights(w):
+    """What weights [N, K] stand for, a scale for each 128 x 128."""
+    out = np.empty_like(w)
+    for a in range(0, w.shape[0], 128):
+        for b in range(0, w.shape[1], 128):
+            p = _finite(w[a:a + 128, b:b + 128])
+            s = e4m3_scale(np.abs(np.where(np.isnan(p), 0, p)).max())
+            out[a:a + 128, b:b + 128] = e4m3_nearest(p / s) * s
+    return out
+
+
+def product_bound(x, w, y, dtype):
+    """How far a product of codes x [T, K], w [N, K] may be off from y = x w^T: each product and its addition a half
+    step of fp32 of the magnitudes' sum; in bf16 also what the matrix core cuts off (7 products of each 8 consecutive
+    inputs, less than 2^-13 of the largest each) and the result's half step."""
+    x, w = np.abs(x), np.abs(w)
+    K = x.shape[1]
+    e = (K + 8) * U32 * (x @ w.T)
+    if dtype == "bf16":
+        for k in range(0, K, 8):
+            e += 7 * 2.0 ** -13 * (x[:, None, k:k + 8] * w[None, :, k:k + 8]).max(2)
+    return 1.01 * e + HALF[dtype] * (np.abs(y) + 1.01 * e)

@@ -2,9 +2,8 @@
 HIP call."""
 import copy
 import ctypes
-import pickle
-
 import os
+import pickle
 
 import pytest
 import torch
@@ -202,6 +201,147 @@ def test_norm_binding_refuses_what_does_not_fit(monkeypatch):
         fwd(y=None)
 
 
+def _f8(**kw):
+    return T.CFp8Desc(**{**dict(experts=2, rows=64, cols=128), **kw})
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({}, OK), ({"rows": 1, "cols": 1}, OK), ({"experts": 1024}, OK), ({"rows": 1 << 20, "cols": 1 << 14}, OK),
+    ({"experts": 0}, INVAL), ({"rows": 0}, INVAL), ({"cols": -1}, INVAL),
+    ({"experts": 1025}, UNSUP), ({"rows": (1 << 20) + 1}, UNSUP), ({"cols": (1 << 20) + 1}, UNSUP),
+    ({"rows": 1 << 20, "cols": (1 << 14) + 1}, UNSUP),
+])
+def test_fp8_descriptor(kw, code):
+    lib, d, n, a, b = T.library(), ctypes.byref(_f8(**kw)), T.CWSizes(), ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.twell_fp8_weights_sizes(d, ctypes.byref(n)) == code
+    assert lib.twell_fp8_weights_sizes(d, None) != OK
+    assert lib.twell_fp8_linear_sizes(d, 5, ctypes.byref(a), ctypes.byref(b)) == code
+    if code != OK:
+        pl = T.CPlanes(P, P)
+        assert lib.twell_fp8_weights_pack(d, P, T.TWELL_BF16, pl, None, None) == code
+        assert lib.twell_fp8_weights_unpack(d, pl, P, T.TWELL_BF16, None) == code
+        assert lib.twell_fp8_linear_fwd(d, pl, 1, P, T.TWELL_BF16, P, 1 << 30, P, 1 << 30, P, 1 << 40, None) == code
+        assert lib.twell_fp8_linear_bwd(d, pl, 1, P, T.TWELL_BF16, P, 1 << 30, P, 1 << 30, P, 1 << 30, P, P, 1 << 40,
+                                        None) == code
+
+
+def test_fp8_sizes():
+    for rows, cols in ((16, 128), (17, 129), (1, 1), (1001, 707), (64, 1024)):
+        tiles, blocks = -(-rows // 16), -(-cols // 128)
+        assert T.Fp8Desc(3, rows, cols).plane_bytes == (3 * tiles * blocks * 2048, 3 * tiles * -(-blocks // 4) * 64)
+        assert T.Fp8Desc(3, rows, cols).transposed == T.Fp8Desc(3, cols, rows)
+    lib, a, b = T.library(), ctypes.c_size_t(), ctypes.c_size_t()
+    d = ctypes.byref(_f8())
+    assert lib.twell_fp8_linear_sizes(d, -1, ctypes.byref(a), ctypes.byref(b)) == INVAL
+    assert lib.twell_fp8_linear_sizes(d, 1, None, ctypes.byref(b)) == INVAL
+    assert lib.twell_fp8_linear_sizes(d, 1, ctypes.byref(a), None) == INVAL
+    assert lib.twell_fp8_linear_sizes(d, (1 << 20) + 1, ctypes.byref(a), ctypes.byref(b)) == UNSUP
+    # rows of 128 and of 64 inputs: one block each, up to a tile more for each expert
+    assert T.fp8_ws_bytes(T.Fp8Desc(2, 64, 128), 100) >= 8 * (2048 + 64)
+
+
+def test_fp8_pack_and_unpack_refuse():
+    lib, d, pl, bf = T.library(), ctypes.byref(_f8()), T.CPlanes(P, P), T.TWELL_BF16
+    for f in (lambda w, t, pl: lib.twell_fp8_weights_pack(d, w, t, pl, None, None),
+              lambda w, t, pl: lib.twell_fp8_weights_unpack(d, pl, w, t, None)):
+        for w, t, p in ((None, bf, pl), (P + 1, bf, pl), (P + 2, T.TWELL_FP32, pl), (P, 2, pl),
+                        (P, bf, T.CPlanes(0, P)), (P, bf, T.CPlanes(P, 0)), (P, bf, T.CPlanes(P + 8, P)),
+                        (P, bf, T.CPlanes(P, P + 4))):
+            assert f(w, t, p) == INVAL
+    for t in (T.CPlanes(0, P), T.CPlanes(P, 0), T.CPlanes(P + 8, P)):
+        assert lib.twell_fp8_weights_pack(d, P, bf, pl, ctypes.byref(t), None) == INVAL
+
+
+def test_fp8_linear_refuses():
+    lib, d = T.library(), _f8()
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.twell_fp8_linear_sizes(ctypes.byref(d), 10, ctypes.byref(a), ctypes.byref(b)) == OK
+    good = dict(d=ctypes.byref(d), p=T.CPlanes(P, P), T_=10, off=P, t=T.TWELL_BF16, x=P, ldx=128, y=P, ldy=64, dx=P,
+                lddx=128, dw=P, ws=P, n=max(a.value, b.value))
+
+    def fwd(**kw):
+        g = {**good, **kw}
+        return lib.twell_fp8_linear_fwd(g["d"], g["p"], g["T_"], g["off"], g["t"], g["x"], g["ldx"], g["y"], g["ldy"],
+                                        g["ws"], g["n"], None)
+
+    def bwd(**kw):
+        g = {**good, **kw}
+        return lib.twell_fp8_linear_bwd(g["d"], g["p"], g["T_"], g["off"], g["t"], g["x"], g["ldx"], g["y"], g["ldy"],
+                                        g["dx"], g["lddx"], g["dw"], g["ws"], g["n"], None)
+
+    both = [dict(d=None), dict(T_=-1), dict(off=None), dict(off=P + 2), dict(t=2), dict(x=None), dict(x=P + 1),
+            dict(y=None), dict(y=P + 1), dict(ldx=127), dict(ldy=63), dict(p=T.CPlanes(0, P)), dict(p=T.CPlanes(P, 0)),
+            dict(p=T.CPlanes(P + 8, P)), dict(ws=None), dict(ws=P + 8), dict(n=100)]
+    for kw in both:
+        assert fwd(**kw) == INVAL, kw
+        assert bwd(**kw) == INVAL, kw
+    for kw in (dict(dx=P + 1), dict(lddx=127), dict(dw=P + 2)):
+        assert bwd(**kw) == INVAL, kw
+    for kw in (dict(T_=(1 << 20) + 1), dict(ldx=(1 << 40) + 1), dict(ldy=(1 << 40) + 1)):
+        assert fwd(**kw) == UNSUP and bwd(**kw) == UNSUP, kw
+    assert bwd(lddx=(1 << 40) + 1) == UNSUP
+    wide = ctypes.byref(_f8(rows=1 << 18))
+    assert fwd(d=wide, ldy=1 << 18, T_=(1 << 19) + 1, n=1 << 50) == UNSUP
+    assert fwd(T_=0, x=None, y=None, p=T.CPlanes(0, 0), ws=None, n=0) == OK
+    assert bwd(T_=0, x=None, y=None, p=T.CPlanes(0, 0), ws=None, n=0, dx=None, dw=None) == OK
+    assert bwd(dx=None, dw=None, x=None, y=None, p=T.CPlanes(0, 0), ws=None, n=0) == OK  # nothing is asked for
+
+
+def _f8_planes(desc, dev=0, short=0):
+    codes, scales = desc.plane_bytes
+    return T.Weights(_On.make(dev, codes - short, dtype=torch.uint8), _On.make(dev, scales, dtype=torch.uint8))
+
+
+def test_fp8_binding_refuses_what_does_not_fit(monkeypatch):
+    monkeypatch.setattr(T, "_device_count", lambda: 2)
+    monkeypatch.setattr(T, "_current_device", lambda: 0)
+    desc, u8, f32 = T.Fp8Desc(2, 64, 128), torch.uint8, torch.float32
+    on = _On.make
+    good = dict(p=_f8_planes(desc), t=_f8_planes(desc.transposed), x=on(0, 0, 128), y=on(0, 0, 64), dx=on(0, 0, 128),
+                ws=on(0, 1 << 16, dtype=u8), off=on(0, 3, dtype=torch.int32))
+
+    def fwd(**kw):
+        g = {**good, **kw}
+        T.twell_fp8_linear_fwd(desc, g["p"], g["x"], g["y"], g["ws"], offsets=g["off"], stream=0)
+
+    def bwd(dw=None, **kw):
+        g = {**good, **kw}
+        T.twell_fp8_linear_bwd(desc, g["t"], g["x"], g["y"], g["dx"], dw, g["ws"], offsets=g["off"], stream=0)
+
+    fwd()
+    bwd()
+    bwd(x=None)
+    for kw in (dict(x=on(0, 0, 127)), dict(x=on(0, 128)), dict(x=on(0, 0, 128, dtype=torch.float16)),
+               dict(x=on(1, 0, 128)), dict(y=on(0, 0, 65)), dict(y=on(0, 1, 64)), dict(y=on(0, 0, 64, dtype=f32)),
+               dict(y=on(1, 0, 64)), dict(ws=on(0, 10, dtype=u8)), dict(ws=on(1, 1 << 16, dtype=u8)), dict(off=None),
+               dict(off=on(0, 2, dtype=torch.int32)), dict(off=on(0, 3, dtype=torch.int64)),
+               dict(off=on(1, 3, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            fwd(**kw)
+        if kw.get("x") is None or kw["x"].shape != (128,):
+            with pytest.raises(ValueError):
+                bwd(**kw)
+    for p in (_f8_planes(desc, short=1), _f8_planes(desc, dev=1)):
+        with pytest.raises(ValueError):
+            fwd(p=p)
+    for kw in (dict(dx=on(0, 0, 127)), dict(dx=on(0, 0, 128, dtype=f32)), dict(dx=on(1, 0, 128)),
+               dict(t=_f8_planes(desc.transposed, short=1)), dict(dw=on(0, 2, 128, 64, dtype=f32)), dict(dw=on(0, 2, 64, 128)),
+               dict(dw=on(1, 2, 64, 128, dtype=f32))):
+        with pytest.raises(ValueError):
+            bwd(**kw)
+    for kw in (dict(x=None, dw=on(0, 2, 64, 128, dtype=f32)), dict(t=None), dict(ws=None)):
+        with pytest.raises(TypeError):
+            bwd(**kw)
+    with pytest.raises(ValueError, match="shape"):
+        T.twell_fp8_weights_pack(desc, on(0, 2, 128, 64), good["p"], stream=0)
+    with pytest.raises(ValueError):
+        T.twell_fp8_weights_pack(desc, on(0, 2, 64, 128), good["p"], _f8_planes(desc.transposed, dev=1), stream=0)
+    with pytest.raises(ValueError):
+        T.twell_fp8_weights_pack(desc, on(0, 2, 64, 128), _f8_planes(desc, short=1), stream=0)
+    with pytest.raises(ValueError):
+        T.twell_fp8_weights_unpack(desc, good["p"], on(0, 2, 64, 128, dtype=torch.float16), stream=0)
+
+
 @pytest.mark.parametrize("make", [lambda d: T.TokensDesc(1, 64, 8, 2, d).ws_bytes, lambda d: T.NormDesc(1, 64, d).ws_bytes])
 def test_unknown_dtypes_are_refused(make):
     make("fp32")
@@ -219,10 +359,20 @@ def test_numbers_beyond_c_integers_do_not_wrap():
         T.NormDesc(1, 64 + (1 << 32), "bf16").ws_bytes
     with pytest.raises(T.TwellError):
         T.NormDesc(1, 64, "bf16", float("nan")).ws_bytes
+    for big in (1 << 32, -(1 << 32)):
+        for make in (lambda: T.Fp8Desc(1 + big, 64, 64), lambda: T.Fp8Desc(1, 64 + big, 64), lambda: T.Fp8Desc(1, 64, 64 + big)):
+            with pytest.raises(ValueError, match="32 bits"):
+                make().plane_bytes
+    with pytest.raises(ValueError, match="64 bits"):
+        T.fp8_ws_bytes(T.Fp8Desc(1, 64, 64), 1 << 64)
 
 
-@pytest.mark.parametrize("desc", [T.TokensDesc(3, 64, 8, 2, "bf16"), T.NormDesc(3, 64, "fp32", 1e-6)])
+@pytest.mark.parametrize("desc", [T.TokensDesc(3, 64, 8, 2, "bf16"), T.NormDesc(3, 64, "fp32", 1e-6), T.Fp8Desc(2, 64, 32)])
 def test_descriptors_are_copied_and_pickled_after_use(desc):
-    used = desc.ws_bytes
+    if isinstance(desc, T.Fp8Desc):
+        used, name = desc.plane_bytes, "plane_bytes"
+        desc.transposed
+    else:
+        used, name = desc.ws_bytes, "ws_bytes"
     for again in (copy.copy(desc), copy.deepcopy(desc), pickle.loads(pickle.dumps(desc))):
-        assert again == desc and hash(again) == hash(desc) and again.ws_bytes == used
+        assert again == desc and hash(again) == hash(desc) and getattr(again, name) == used
