@@ -14,6 +14,7 @@
 
 #include "common.hpp"
 #include "internal.hpp"
+#include "rows.hpp"
 
 namespace twell {
 
@@ -33,21 +34,88 @@ __device__ __forceinline__ uint32_t f8_scale_byte(uint32_t most) {
 }
 __device__ __forceinline__ float f8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Bits of |v|, 0 for an infinity or a NaN: those become NaN codes and have no
-// part in the scale.
-__device__ __forceinline__ uint32_t finite_magnitude(float v) {
-  const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
+// The largest of a value over the four lanes that hold a row's block.
+__device__ __forceinline__ uint32_t max_over_row(uint32_t m) {
+  const auto a = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  m = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  return max(b[0], b[1]);
 }
 
-// Four values over their scale, rounded to e4m3 (to nearest even; the only
-// rounding there is).  An infinity becomes a NaN.
-__device__ __forceinline__ uint32_t f8_codes(const float* v, float scale) {
-  i16x2_t r{0, 0};
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v[0], v[1], scale, false);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v[2], v[3], scale, true);
-  return __builtin_bit_cast(uint32_t, r);
-}
+// One lane's 32 inputs of a row's block, from memory to codes.  An infinity or a
+// NaN has no part in the scale and becomes a NaN code.
+template <class E>
+struct F8Inputs;
+template <>
+struct F8Inputs<EBf16> {
+  u32x4_t raw[4];  // of each step
+  __device__ __forceinline__ void load(const uint16_t* row, int c0, int lane, int K) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) raw[s] = load_piece<EBf16>(row, c0 + 32 * s + 8 * (lane >> 4), K);
+  }
+  // Bits of the largest magnitude, as fp32.
+  __device__ __forceinline__ uint32_t most() const {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t m{0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, raw[i / 4][i % 4] & 0x7fff7fffu));
+    if (__any(m[0] >= 0x7f80 || m[1] >= 0x7f80)) {
+      m = u16x2_t{0, 0};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        u16x2_t v = __builtin_bit_cast(u16x2_t, raw[i / 4][i % 4] & 0x7fff7fffu);
+        v[0] = v[0] < 0x7f80 ? v[0] : 0;
+        v[1] = v[1] < 0x7f80 ? v[1] : 0;
+        m = __builtin_elementwise_max(m, v);
+      }
+    }
+    return static_cast<uint32_t>(max(m[0], m[1])) << 16;
+  }
+  // Over the scale, rounded to nearest even: the only rounding there is.
+  __device__ __forceinline__ void codes(float scale, u32x4_t (&c)[2]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      i16x2_t r{0, 0};
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, pair(2 * i), scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, pair(2 * i + 1), scale, true);
+      c[i / 4][i % 4] = __builtin_bit_cast(uint32_t, r);
+    }
+  }
+
+ private:
+  __device__ __forceinline__ bf16x2_t pair(int i) const {
+    const bf16x8_t v = __builtin_bit_cast(bf16x8_t, raw[i / 4]);  // whole, as above (AxpyCoef)
+    return bf16x2_t{v[2 * (i % 4)], v[2 * (i % 4) + 1]};
+  }
+};
+template <>
+struct F8Inputs<EF32> {
+  float f[32];
+  __device__ __forceinline__ void load(const float* row, int c0, int lane, int K) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4)
+      Piece<EF32>::unpack(load_piece<EF32>(row, c0 + 32 * (i / 8) + 8 * (lane >> 4) + i % 8, K), f + i);
+  }
+  __device__ __forceinline__ uint32_t most() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t u = __float_as_uint(f[i]) & 0x7fffffffu;
+      m = max(m, u < 0x7f800000u ? u : 0u);
+    }
+    return m;
+  }
+  __device__ __forceinline__ void codes(float scale, u32x4_t (&c)[2]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      i16x2_t r{0, 0};
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, f[4 * i], f[4 * i + 1], scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, f[4 * i + 2], f[4 * i + 3], scale, true);
+      c[i / 4][i % 4] = __builtin_bit_cast(uint32_t, r);
+    }
+  }
+};
 
 // Where the rows of tile `index` are: tiles of `unit` rows, numbered expert by
 // expert, the last of each expert short.  Called by whole waves; every result is

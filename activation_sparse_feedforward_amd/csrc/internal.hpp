@@ -288,6 +288,15 @@ struct F8GemmArgs {
   int64_t T, ldy, most_tiles;
   int32_t N, tiles, blocks, quads, experts;
 };
+// The same from the rows themselves, where each expert has few.
+struct F8FewArgs {
+  const uint8_t *w_codes, *w_scales;
+  const void* x;
+  void* y;
+  const int32_t* offsets;
+  int64_t T, ldx, ldy;
+  int32_t N, K, tiles, blocks, quads, experts;
+};
 // dw [experts][N x K] = dy^T x over each expert's rows.
 struct WgradArgs {
   const void *x, *dy;
@@ -325,6 +334,7 @@ hipError_t launch_f8_pack(const F8PackArgs& a, int dtype, hipStream_t s);
 hipError_t launch_f8_unpack(const F8PackArgs& a, int dtype, hipStream_t s);
 hipError_t launch_f8_rows(const F8RowsArgs& a, int dtype, hipStream_t s);
 hipError_t launch_f8_gemm(const F8GemmArgs& a, int dtype, hipStream_t s);
+hipError_t launch_f8_few(const F8FewArgs& a, int dtype, hipStream_t s);
 hipError_t launch_wgrad(const WgradArgs& a, int dtype, hipStream_t s);
 hipError_t launch_tokens_sort(TokensSortArgs a, hipStream_t s);
 hipError_t launch_tokens_gather(const TokensArgs& a, int dtype, hipStream_t s);

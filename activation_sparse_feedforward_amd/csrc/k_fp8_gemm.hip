@@ -52,8 +52,8 @@ __device__ __forceinline__ void bf16_mfma(f32x4_t& acc, const Bf16Frag& w, const
 }
 
 // Register r of lane l of an accumulator: weight row 4 (l / 16) + r, token l % 16.
-template <class E>
-__device__ __forceinline__ void store_acc(const F8GemmArgs& a, int64_t row, int n, const f32x4_t& acc) {
+template <class E, class Args>
+__device__ __forceinline__ void store_acc(const Args& a, int64_t row, int n, const f32x4_t& acc) {
   using S = typename E::storage;
   S* y = static_cast<S*>(a.y) + row * a.ldy + n;
   if (n + 4 <= a.N) {
@@ -188,6 +188,102 @@ __global__ __launch_bounds__(WW* WX* kWave) void f8_gemm_kernel(F8GemmArgs a) {
   }
 }
 
+// ------------------------------------------------------------------ few rows
+// With few rows for each expert what counts is reading the weights once, at
+// memory's rate, and one trip to memory where they are few too: weights go from
+// memory to the matrix core's registers, without LDS.  A workgroup has 16 rows
+// and NT x 16 weight rows; its waves take turns at the blocks of inputs and add
+// their sums through LDS, in the order of the waves.  A wave fetches U blocks of
+// weights, and the rows' inputs, before it uses the first.  Each wave rounds the
+// inputs that it needs itself: one launch, and the same codes every time.
+constexpr int kFewWaves = 8;
+
+template <class E, int NT, int U>
+__global__ __launch_bounds__(kFewWaves* kWave) void f8_few_kernel(F8FewArgs a) {
+  using S = typename E::storage;
+  extern __shared__ __align__(16) float lds_sums[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const F8Place p = f8_locate(a.offsets, a.experts, a.T, 16, blockIdx.y);
+  if (p.expert < 0) return;
+  const int tile0 = blockIdx.x * NT, r = lane & 15;
+  const S* row = static_cast<const S*>(a.x) + (p.row0 + (r < p.rows ? r : 0)) * a.ldx;
+  const uint8_t *codes[NT], *scales[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    // a tile past the matrix is the last one again; its results are not stored
+    const int64_t t = static_cast<int64_t>(p.expert) * a.tiles + min(tile0 + i, a.tiles - 1);
+    codes[i] = a.w_codes + t * a.blocks * kF8Bytes;
+    scales[i] = a.w_scales + t * a.quads * kF8Scales + r * 4;
+  }
+  f32x4_t acc[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int b0 = wave; b0 < a.blocks; b0 += waves * U) {
+    F8Frag w[U][NT];
+    uint32_t sw[U][NT];
+    F8Inputs<E> in[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * waves;
+      if (b < a.blocks) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          w[u][i].read(codes[i] + static_cast<int64_t>(b) * kF8Bytes, lane);
+          sw[u][i] = scales[i][(b >> 2) * kF8Scales + (b & 3)];
+        }
+        in[u].load(row, b * kF8Block, lane, a.K);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b0 + u * waves >= a.blocks) break;
+      const uint32_t sx = f8_scale_byte(max_over_row(in[u].most()));
+      F8Frag x;
+      in[u].codes(f8_scale(sx), x.v);
+      if constexpr (E::kBytes == 4) {
+        Bf16Frag xb;
+        xb.from(x, sx);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          Bf16Frag wb;
+          wb.from(w[u][i], sw[u][i]);
+          bf16_mfma(acc[i], wb, xb);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) f8_mfma(acc[i], w[u][i], sw[u][i], x, sx);
+      }
+    }
+  }
+  if (waves > 1) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      *reinterpret_cast<f32x4_t*>(lds_sums + ((wave * NT + i) * kWave + lane) * 4) = acc[i];
+    __syncthreads();
+  }
+  for (int i = wave; i < NT; i += waves) {
+    f32x4_t sum = acc[0];
+    if (waves > 1) {
+      sum = *reinterpret_cast<const f32x4_t*>(lds_sums + (i * kWave + lane) * 4);
+      for (int v = 1; v < waves; ++v) sum += *reinterpret_cast<const f32x4_t*>(lds_sums + ((v * NT + i) * kWave + lane) * 4);
+    } else {
+#pragma unroll
+      for (int j = 1; j < NT; ++j) sum = i == j ? acc[j] : sum;
+    }
+    const int n = (tile0 + i) * 16 + 4 * (lane >> 4);
+    if (r < p.rows && n < a.N) store_acc<E>(a, p.row0 + r, n, sum);
+  }
+}
+
+template <class E, int NT, int U>
+hipError_t go_few(const F8FewArgs& a, hipStream_t s) {
+  int waves = kFewWaves;
+  while (waves > 1 && waves > a.blocks) waves >>= 1;
+  const dim3 grid((a.tiles + NT - 1) / NT, static_cast<unsigned>(a.offsets ? a.T / 16 + a.experts : (a.T + 15) / 16));
+  return launch(f8_few_kernel<E, NT, U>, grid, waves * kWave, waves * NT * kWave * 16, s, a);
+}
+
 template <class E, int WW, int WX, int FW, int FX>
 hipError_t go_tile(const F8GemmArgs& a, hipStream_t s) {
   using Tile = F8Tile<WW, WX, FW, FX>;
@@ -207,6 +303,10 @@ hipError_t go_tile(const F8GemmArgs& a, hipStream_t s) {
 // exactly, with fp32 sums, at half the rate or less.
 hipError_t launch_f8_gemm(const F8GemmArgs& a, int dtype, hipStream_t s) {
   return dtype == 1 ? go_tile<EBf16, 2, 2, 4, 4>(a, s) : go_tile<EF32, 2, 2, 4, 4>(a, s);
+}
+
+hipError_t launch_f8_few(const F8FewArgs& a, int dtype, hipStream_t s) {
+  return dtype == 1 ? go_few<EBf16, 2, 2>(a, s) : go_few<EF32, 2, 2>(a, s);
 }
 
 }  // namespace twell

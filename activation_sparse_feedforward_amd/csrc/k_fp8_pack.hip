@@ -8,30 +8,6 @@ namespace {
 
 constexpr int kPackWaves = 4;
 
-// A lane's 32 values of a block: row `row`, or zeros.
-template <class E>
-__device__ __forceinline__ void load_block_row(const typename E::storage* row, int c0, int lane, int K, float (&f)[32]) {
-  constexpr int kN = Piece<E>::kN;
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-#pragma unroll
-    for (int i = 0; i < 8; i += kN)
-      Piece<E>::unpack(load_piece<E>(row, c0 + 32 * s + 8 * (lane >> 4) + i, K), &f[8 * s + i]);
-}
-
-// A lane's 32 codes over `scale`.
-__device__ __forceinline__ void block_codes(const float (&f)[32], float scale, u32x4_t (&c)[2]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) c[i / 4][i % 4] = f8_codes(&f[4 * i], scale);
-}
-
-__device__ __forceinline__ uint32_t most_of(const float (&f)[32]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) m = max(m, finite_magnitude(f[i]));
-  return m;
-}
-
 // One workgroup per 128 x 128 weights, which share a scale, so that the codes of
 // the transposed matrix are the same numbers.  Reading and writing bound it; the
 // transposed codes go through LDS byte by byte, a tenth of that time.
@@ -45,19 +21,16 @@ __global__ __launch_bounds__(kPackWaves* kWave) void f8_pack_kernel(F8PackArgs a
   const int cb = blockIdx.x, rb = blockIdx.y;
   const int64_t e = blockIdx.z;
   const S* w = static_cast<const S*>(a.w) + e * a.N * a.K;
-  float f[2][32];
+  F8Inputs<E> in[2];
   uint32_t m = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int r = rb * 128 + (2 * wave + t) * 16 + (lane & 15);
-    if (r < a.N) {
-      load_block_row<E>(w + static_cast<int64_t>(r) * a.K, cb * 128, lane, a.K, f[t]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) f[t][i] = 0.f;
-    }
-    m = max(m, most_of(f[t]));
+    // rows past the matrix are zeros: none of their inputs exists
+    in[t].load(w + static_cast<int64_t>(min(r, a.N - 1)) * a.K, cb * 128, lane, r < a.N ? a.K : 0);
   }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) m = max(m, in[t].most());
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), x)));
   if (lane == 0) most[wave] = m;
@@ -68,7 +41,7 @@ __global__ __launch_bounds__(kPackWaves* kWave) void f8_pack_kernel(F8PackArgs a
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     u32x4_t c[2];
-    block_codes(f[t], scale, c);
+    in[t].codes(scale, c);
     const int tile = rb * 8 + 2 * wave + t;
     if (tile < a.tiles) {
       uint8_t* to = a.codes + ((e * a.tiles + tile) * a.blocks + cb) * kF8Bytes + lane * 16;
@@ -171,15 +144,12 @@ __global__ __launch_bounds__(kPackWaves* kWave) void f8_rows_kernel(F8RowsArgs a
   for (int j = 0; j < 4; ++j) {
     const int b = quad * 4 + j;
     if (b >= a.blocks) break;
-    float f[32];
-    load_block_row<E>(row, b * 128, lane, a.K, f);
-    uint32_t m = most_of(f);
-    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
-    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
-    const uint32_t byte = f8_scale_byte(m);
+    F8Inputs<E> in;
+    in.load(row, b * 128, lane, a.K);
+    const uint32_t byte = f8_scale_byte(max_over_row(in.most()));
     word |= byte << (8 * j);
     u32x4_t c[2];
-    block_codes(f, f8_scale(byte), c);
+    in.codes(f8_scale(byte), c);
     uint8_t* to = a.codes + (p.tile16 * a.blocks + b) * kF8Bytes + lane * 16;
     *reinterpret_cast<u32x4_t*>(to) = c[0];
     *reinterpret_cast<u32x4_t*>(to + 1024) = c[1];
