@@ -165,9 +165,20 @@ __device__ __forceinline__ F8Place f8_locate(const int32_t* offsets, int experts
   return p;
 }
 
-// 16 bytes a lane straight to LDS: lane l's go to lds + 16 l (lds wave-uniform).
-__device__ __forceinline__ void direct16(const uint8_t* from, uint8_t* lds) {
-  __builtin_amdgcn_global_load_lds(from, lds, 16, 0, 0);
+// Memory from base on, for the loads below: a base in scalar registers and 32-bit
+// offsets, so that a loop of loads needs no vector registers for addresses.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const uint8_t* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, 0xffffffffu, 0x00027000);
+}
+// 16 bytes a lane straight to LDS: from base + lane_offset + offset (wave-uniform);
+// lane l's go to lds + 16 l (lds wave-uniform).
+__device__ __forceinline__ void direct16(__amdgpu_buffer_rsrc_t base, uint32_t lane_offset, uint32_t offset, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, lds, 16, lane_offset, offset, 0, 0);
+}
+
+// 16 bytes a lane to registers, from the same place.
+__device__ __forceinline__ u32x4_t buffer16(__amdgpu_buffer_rsrc_t base, uint32_t lane_offset, uint32_t offset) {
+  return __builtin_amdgcn_raw_buffer_load_b128(base, lane_offset, offset, 0);
 }
 
 // Workgroup id to tile: ids go round-robin to the 8 XCDs, each of which gets a

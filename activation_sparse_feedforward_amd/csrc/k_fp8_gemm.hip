@@ -10,9 +10,9 @@ namespace {
 // A fragment: one lane's 32 codes.
 struct F8Frag {
   u32x4_t v[2];
-  __device__ __forceinline__ void read(const uint8_t* block, int lane) {
-    v[0] = *reinterpret_cast<const u32x4_t*>(block + lane * 16);
-    v[1] = *reinterpret_cast<const u32x4_t*>(block + 1024 + lane * 16);
+  __device__ __forceinline__ void read(const uint8_t* at) {  // the block + 16 lane
+    v[0] = *reinterpret_cast<const u32x4_t*>(at);
+    v[1] = *reinterpret_cast<const u32x4_t*>(at + 1024);
   }
 };
 
@@ -73,119 +73,247 @@ __device__ __forceinline__ void store_acc(const Args& a, int64_t row, int n, con
     }
 }
 
-// Tiles of (WW x 16 FW) weight rows x (WX x 16 FX) tokens, WW x WX waves.  Both
-// operands go to LDS with direct 16-byte loads, two stages of one block (128
-// inputs): the loads of the next block fly while this one is multiplied.
-template <int WW, int WX, int FW, int FX>
-struct F8Tile {
-  static constexpr int kWaves = WW * WX;
-  static constexpr int kTilesW = WW * FW, kTilesX = WX * FX;
-  static constexpr int kN = 16 * kTilesW, kM = 16 * kTilesX;
-  static constexpr int kStage = (kTilesW + kTilesX) * kF8Bytes;
-  static constexpr int kLds = 2 * kStage;
-  static constexpr int kLoads = 2 * (kTilesW + kTilesX) / kWaves;  // 1 KB each, of a wave
+// ------------------------------------------------------------------ many rows
+// What a workgroup of four waves works on: tiles of 16 kW weight rows x 16 kX rows.
+template <int kW, int kX>
+struct F8Work {
+  F8Place p;
+  int w0;                          // first tile of weight rows
+  int w_last, x_last;              // last tiles that exist, of the matrix and of the rows from p.row0 on
+  const uint8_t *w_codes, *w_scales;  // of the expert's tile 0
+  const uint8_t *x_codes, *x_scales;  // of p.tile16
+
+  __device__ __forceinline__ bool init(const F8GemmArgs& a) {
+    // groups of 8 tiles of rows, all tiles of weights of a group in a row
+    const int nt = (a.tiles + kW - 1) / kW;
+    const int id = xcd_run(blockIdx.x, gridDim.x);
+    const int mts = gridDim.x / nt, group = id / (8 * nt), first = group * 8, size = min(8, mts - first);
+    const int in = id - group * 8 * nt, mt = first + in % size;
+    p = f8_locate(a.offsets, a.experts, a.T, 16 * kX, mt);
+    if (p.expert < 0 || p.tile16 + min(p.tiles16, kX) > a.most_tiles) return false;
+    w0 = in / size * kW;
+    w_last = a.tiles - 1;
+    x_last = p.tiles16 - 1;
+    w_codes = a.w_codes + static_cast<int64_t>(p.expert) * a.tiles * a.blocks * kF8Bytes;
+    w_scales = a.w_scales + static_cast<int64_t>(p.expert) * a.tiles * a.quads * kF8Scales;
+    x_codes = a.x_codes + p.tile16 * a.blocks * kF8Bytes;
+    x_scales = a.x_scales + p.tile16 * a.quads * kF8Scales;
+    return true;
+  }
+  // tiles past the matrix or the expert's rows are the last one again; their results are not stored
+  __device__ __forceinline__ int w_tile(int i) const { return min(w0 + i, w_last); }
+  __device__ __forceinline__ int x_tile(int i) const { return min(i, x_last); }
+  template <class E, int FW, int FX>
+  __device__ __forceinline__ void store(const F8GemmArgs& a, int fw0, int fx0, const f32x4_t (&acc)[FW][FX]) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < FX; ++j) {
+      const int r = (fx0 + j) * 16 + (lane & 15);
+      if (r >= p.rows) continue;
+#pragma unroll
+      for (int i = 0; i < FW; ++i) {
+        const int n = (w0 + fw0 + i) * 16 + 4 * (lane >> 4);
+        if (n < a.N) store_acc<E>(a, p.row0 + r, n, acc[i][j]);
+      }
+    }
+  }
 };
 
-template <class E, int WW, int WX, int FW, int FX>
-__global__ __launch_bounds__(WW* WX* kWave) void f8_gemm_kernel(F8GemmArgs a) {
-  using Tile = F8Tile<WW, WX, FW, FX>;
-  extern __shared__ __align__(16) uint8_t lds_tiles[];
-  constexpr bool kExact = E::kBytes == 4;  // fp32 results: see launch_f8_gemm
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // groups of 8 token tiles, all weight tiles of a group in a row
-  const int nt = (a.tiles + Tile::kTilesW - 1) / Tile::kTilesW;
-  const int id = xcd_run(blockIdx.x, gridDim.x);
-  const int mts = gridDim.x / nt, group = id / (8 * nt), first = group * 8, size = min(8, mts - first);
-  const int in = id - group * 8 * nt, mt = first + in % size, tn = in / size;
-  const F8Place p = f8_locate(a.offsets, a.experts, a.T, Tile::kM, mt);
-  if (p.expert < 0 || p.tile16 + min(p.tiles16, Tile::kTilesX) > a.most_tiles) return;
+// bf16 results.  A wave has 64 weight rows of its own, whose codes go from memory to
+// registers, one block (128 inputs) ahead, and all 16 FX rows of the workgroup,
+// whose codes go to LDS with direct loads, three blocks ahead, and from there to
+// registers three fragments ahead.  So a fragment from LDS feeds four matrix
+// instructions and LDS carries 2 KB for 131 k operations of each wave: with both
+// operands in LDS and 64 x 64 a wave it would be twice that, which bounds it.
+template <int FX>
+struct F8Gemm {
+  static constexpr int kStages = 4, kStage = FX * kF8Bytes, kLds = kStages * kStage;
+  static constexpr int kLoads = FX / 2;  // direct loads of a wave and block, 1 KB each
+  static_assert(kLoads <= 8, "a wait for all but kLoads covers what came before a block's eight loads of weights");
 
-  const uint8_t* wcodes = a.w_codes + static_cast<int64_t>(p.expert) * a.tiles * a.blocks * kF8Bytes;
-  const uint8_t* wscales = a.w_scales + static_cast<int64_t>(p.expert) * a.tiles * a.quads * kF8Scales;
-  const uint8_t* xcodes = a.x_codes + p.tile16 * a.blocks * kF8Bytes;
-  const uint8_t* xscales = a.x_scales + p.tile16 * a.quads * kF8Scales;
-  const int w0 = tn * Tile::kTilesW;
-  // tiles past the matrix or the expert's rows are the last one again; their results are not stored
-  auto w_tile = [&](int i) { return static_cast<int64_t>(min(w0 + i, a.tiles - 1)); };
-  auto x_tile = [&](int i) { return static_cast<int64_t>(min(i, p.tiles16 - 1)); };
+  const F8GemmArgs& a;
+  F8Work<16, FX> work;
+  int lane, wave;
+  __amdgpu_buffer_rsrc_t w_rows, x_rows;
+  uint32_t w_from[4], x_from[kLoads];  // at block 0
+  uint8_t* lds;
+  f32x4_t acc[4][FX];
+  F8Frag x[4];  // ring
 
-  const uint8_t* from[Tile::kLoads];
-#pragma unroll
-  for (int q = 0; q < Tile::kLoads; ++q) {
-    const int half = wave * Tile::kLoads + q, t = half >> 1;
-    const uint8_t* src = t < Tile::kTilesW ? wcodes + w_tile(t) * a.blocks * kF8Bytes
-                                           : xcodes + x_tile(t - Tile::kTilesW) * a.blocks * kF8Bytes;
-    from[q] = src + (half & 1) * 1024 + lane * 16;
+  __device__ __forceinline__ void fetch_x(int q, int kb, uint8_t* stage) {
+    direct16(x_rows, lane * 16, x_from[q] + kb * kF8Bytes, stage + (wave * kLoads + q) * 1024);
   }
-  auto issue = [&](int kb, uint8_t* stage) {
+  __device__ __forceinline__ void fetch_w(F8Frag& w, int i, int half, int kb) {
+    w.v[half] = buffer16(w_rows, lane * 16, w_from[i] + kb * kF8Bytes + half * 1024);
+  }
+  // One block, with everything else that has to happen meanwhile dealt out between
+  // the matrix instructions (sched_barrier pins the order: with one wave a SIMD
+  // anything issued in clumps leaves the matrix core idle).
+  __device__ __forceinline__ void block(int kb, const F8Frag (&w)[4], F8Frag (&w_next)[4], uint32_t sw,
+                                        const uint32_t (&sx)[FX]) {
+    // of what this wave has fetched only the last block's rows may still be under way, so the next block's are
+    // there; and all waves are done with the block before this one, whose place is filled now
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* here = lds + (kb & 3) * kStage + lane * 16;
+    const uint8_t* next = lds + ((kb + 1) & 3) * kStage + lane * 16;
+    // past the end: the last block again, not used (a branch here would move matrix instructions)
+    const int kw = min(kb + 1, a.blocks - 1), kx = min(kb + 3, a.blocks - 1);
+    uint8_t* fill = lds + ((kb + 3) & 3) * kStage;
 #pragma unroll
-    for (int q = 0; q < Tile::kLoads; ++q)
-      direct16(from[q] + static_cast<int64_t>(kb) * kF8Bytes, stage + (wave * Tile::kLoads + q) * 1024);
-  };
-
-  const int fw0 = (wave / WX) * FW, fx0 = (wave % WX) * FX;
-  f32x4_t acc[FW][FX];
+    for (int j = 0; j < FX; ++j) {
 #pragma unroll
-  for (int i = 0; i < FW; ++i)
-#pragma unroll
-    for (int j = 0; j < FX; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  uint32_t sw[FW], sx[FX];
-  issue(0, lds_tiles);
-  for (int kb = 0; kb < a.blocks; ++kb) {
-    const uint8_t* stage = lds_tiles + (kb & 1) * Tile::kStage;
-    if ((kb & 3) == 0) {
-#pragma unroll
-      for (int i = 0; i < FW; ++i)
-        sw[i] = *reinterpret_cast<const uint32_t*>(wscales + (w_tile(fw0 + i) * a.quads + (kb >> 2)) * kF8Scales +
-                                                   (lane & 15) * 4);
-#pragma unroll
-      for (int j = 0; j < FX; ++j)
-        sx[j] = *reinterpret_cast<const uint32_t*>(xscales + (x_tile(fx0 + j) * a.quads + (kb >> 2)) * kF8Scales +
-                                                   (lane & 15) * 4);
-    } else {
-#pragma unroll
-      for (int i = 0; i < FW; ++i) sw[i] >>= 8;
-#pragma unroll
-      for (int j = 0; j < FX; ++j) sx[j] >>= 8;
+      for (int i = 0; i < 4; ++i) {
+        f8_mfma(acc[i][j], w[i], sw, x[j % 4], sx[j]);
+        if (i == 0) x[(j + 3) % 4].read(j + 3 < FX ? here + (j + 3) * kF8Bytes : next + (j + 3 - FX) * kF8Bytes);
+        else if (j * 3 + i - 1 < 8) fetch_w(w_next[(j * 3 + i - 1) / 2], (j * 3 + i - 1) / 2, (j * 3 + i - 1) % 2, kw);
+        else if (j * 3 + i - 9 < kLoads) fetch_x(j * 3 + i - 9, kx, fill);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+  }
+
+  __device__ __forceinline__ void run() {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int blocks = a.blocks, quads = a.quads;
+    w_rows = f8_buffer(work.w_codes + static_cast<int64_t>(work.w0) * blocks * kF8Bytes);
+    x_rows = f8_buffer(work.x_codes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w_from[i] = static_cast<uint32_t>(work.w_tile(4 * wave + i) - work.w0) * blocks * kF8Bytes;
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int half = wave * kLoads + q;
+      x_from[q] = static_cast<uint32_t>(work.x_tile(half >> 1)) * blocks * kF8Bytes + (half & 1) * 1024;
+    }
+    // 128 rows of weights, which a wave's lie in, share their scales
+    const uint8_t* ws = work.w_scales + static_cast<int64_t>(work.w_tile(4 * wave)) * quads * kF8Scales;
+    const uint8_t* xs = work.x_scales + (lane & 15) * 4;
+    auto w_word = [&](int q) { return *reinterpret_cast<const uint32_t*>(ws + q * kF8Scales); };
+    auto x_word = [&](int j, int q) {
+      return *reinterpret_cast<const uint32_t*>(xs + (static_cast<int64_t>(work.x_tile(j)) * quads + q) * kF8Scales);
+    };
+    F8Frag wa[4], wb[4];
+    uint32_t sw_next = w_word(0), sx_next[FX];
+#pragma unroll
+    for (int j = 0; j < FX; ++j) sx_next[j] = x_word(j, 0);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) fetch_x(q, 0, lds);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) fetch_w(wa[q / 2], q / 2, q % 2, 0);
+#pragma unroll
+    for (int kb = 1; kb < 3; ++kb)
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) fetch_x(q, min(kb, blocks - 1), lds + kb * kStage);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < FX; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kb + 1 < a.blocks) issue(kb + 1, lds_tiles + ((kb + 1) & 1) * Tile::kStage);
-    F8Frag x[FX];
 #pragma unroll
-    for (int j = 0; j < FX; ++j) x[j].read(stage + (Tile::kTilesW + fx0 + j) * kF8Bytes, lane);
-    if constexpr (kExact) {
-      Bf16Frag xb[FX];
+    for (int j = 0; j < 3; ++j) x[j].read(lds + lane * 16 + j * kF8Bytes);
+    // four blocks at a time, whose scales share words; the next four's are fetched before them
+    for (int kb0 = 0; kb0 < blocks; kb0 += 4) {
+      uint32_t sw = sw_next, sx[FX];
 #pragma unroll
-      for (int j = 0; j < FX; ++j) xb[j].from(x[j], sx[j]);
+      for (int j = 0; j < FX; ++j) sx[j] = sx_next[j];
+      const int q = min((kb0 >> 2) + 1, quads - 1), end = min(kb0 + 4, blocks);
+      sw_next = w_word(q);
 #pragma unroll
-      for (int i = 0; i < FW; ++i) {
-        F8Frag w;
-        w.read(stage + (fw0 + i) * kF8Bytes, lane);
-        Bf16Frag wb;
-        wb.from(w, sw[i]);
+      for (int j = 0; j < FX; ++j) sx_next[j] = x_word(j, q);
+#pragma nounroll
+      for (int kb = kb0; kb < end; ++kb) {
+        block(kb, wa, wb, sw, sx);
+        sw >>= 8;
 #pragma unroll
-        for (int j = 0; j < FX; ++j) bf16_mfma(acc[i][j], wb, xb[j]);
+        for (int j = 0; j < FX; ++j) sx[j] >>= 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wa[i] = wb[i];
       }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load is still on its way to LDS when the workgroup ends
+    work.template store<EBf16>(a, 4 * wave, 0, acc);
+  }
+};
+
+template <int FX>
+__global__ __launch_bounds__(256, FX < 16 ? 2 : 1) void f8_gemm_kernel(F8GemmArgs a) {
+  extern __shared__ __align__(16) uint8_t lds_tiles[];
+  F8Gemm<FX> g{a};
+  if (!g.work.init(a)) return;
+  g.lds = lds_tiles;
+  g.run();
+}
+
+// fp32 results: codes widened to bf16, four instructions a block.  2 x 2 waves of 64 x 64, both operands through
+// LDS in two stages.
+constexpr int kExactTiles = 8;  // of 16 weight rows, and of 16 rows
+constexpr int kExactStage = 2 * kExactTiles * kF8Bytes;
+__global__ __launch_bounds__(256) void f8_gemm_exact_kernel(F8GemmArgs a) {
+  constexpr int F = kExactTiles / 2, kLoads = kExactStage / 4096;  // of a wave
+  extern __shared__ __align__(16) uint8_t lds_tiles[];
+  F8Work<kExactTiles, kExactTiles> work;
+  if (!work.init(a)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fw0 = (wave >> 1) * F, fx0 = (wave & 1) * F;
+  // waves 0 and 1 fetch weights, 2 and 3 rows
+  const bool of_w = wave < 2;
+  const auto from = f8_buffer(of_w ? work.w_codes + static_cast<int64_t>(work.w0) * a.blocks * kF8Bytes : work.x_codes);
+  uint32_t at[kLoads];
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    const int half = (wave & 1) * kLoads + q, t = half >> 1;
+    at[q] = static_cast<uint32_t>(of_w ? work.w_tile(t) - work.w0 : work.x_tile(t)) * a.blocks * kF8Bytes + (half & 1) * 1024;
+  }
+  auto fetch = [&](int kb) {
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q)
+      direct16(from, lane * 16, at[q] + kb * kF8Bytes, lds_tiles + (kb & 1) * kExactStage + (wave * kLoads + q) * 1024);
+  };
+  f32x4_t acc[F][F];
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint32_t sw = 0, sx[F];
+  fetch(0);
+  for (int kb = 0; kb < a.blocks; ++kb) {
+    const uint8_t* stage = lds_tiles + (kb & 1) * kExactStage + lane * 16;
+    if ((kb & 3) == 0) {
+      const int q = kb >> 2;
+      sw = *reinterpret_cast<const uint32_t*>(work.w_scales +
+                                              (static_cast<int64_t>(work.w_tile(fw0)) * a.quads + q) * kF8Scales);
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        sx[j] = *reinterpret_cast<const uint32_t*>(
+            work.x_scales + (static_cast<int64_t>(work.x_tile(fx0 + j)) * a.quads + q) * kF8Scales + (lane & 15) * 4);
     } else {
+      sw >>= 8;
 #pragma unroll
-      for (int i = 0; i < FW; ++i) {
-        F8Frag w;
-        w.read(stage + (fw0 + i) * kF8Bytes, lane);
+      for (int j = 0; j < F; ++j) sx[j] >>= 8;
+    }
+    // the reads of the stage that is filled next were used before this barrier
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kb + 1 < a.blocks) fetch(kb + 1);
+    Bf16Frag xb[F];
 #pragma unroll
-        for (int j = 0; j < FX; ++j) f8_mfma(acc[i][j], w, sw[i], x[j], sx[j]);
-      }
+    for (int j = 0; j < F; ++j) {
+      F8Frag x;
+      x.read(stage + (kExactTiles + fx0 + j) * kF8Bytes);
+      xb[j].from(x, sx[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      F8Frag w;
+      w.read(stage + (fw0 + i) * kF8Bytes);
+      Bf16Frag wb;
+      wb.from(w, sw);
+#pragma unroll
+      for (int j = 0; j < F; ++j) bf16_mfma(acc[i][j], wb, xb[j]);
     }
   }
-#pragma unroll
-  for (int j = 0; j < FX; ++j) {
-    const int r = (fx0 + j) * 16 + (lane & 15);
-    if (r >= p.rows) continue;
-#pragma unroll
-    for (int i = 0; i < FW; ++i) {
-      const int n = (w0 + fw0 + i) * 16 + 4 * (lane >> 4);
-      if (n < a.N) store_acc<E>(a, p.row0 + r, n, acc[i][j]);
-    }
-  }
+  work.template store<EF32>(a, fw0, fx0, acc);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -229,7 +357,7 @@ __global__ __launch_bounds__(kFewWaves* kWave) void f8_few_kernel(F8FewArgs a) {
       if (b < a.blocks) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          w[u][i].read(codes[i] + static_cast<int64_t>(b) * kF8Bytes, lane);
+          w[u][i].read(codes[i] + static_cast<int64_t>(b) * kF8Bytes + lane * 16);
           sw[u][i] = scales[i][(b >> 2) * kF8Scales + (b & 3)];
         }
         in[u].load(row, b * kF8Block, lane, a.K);
@@ -284,13 +412,15 @@ hipError_t go_few(const F8FewArgs& a, hipStream_t s) {
   return launch(f8_few_kernel<E, NT, U>, grid, waves * kWave, waves * NT * kWave * 16, s, a);
 }
 
-template <class E, int WW, int WX, int FW, int FX>
-hipError_t go_tile(const F8GemmArgs& a, hipStream_t s) {
-  using Tile = F8Tile<WW, WX, FW, FX>;
-  const int64_t nt = (a.tiles + Tile::kTilesW - 1) / Tile::kTilesW;
-  const int64_t mt = a.offsets ? a.T / Tile::kM + a.experts : (a.T + Tile::kM - 1) / Tile::kM;
-  return launch_lds<&f8_gemm_kernel<E, WW, WX, FW, FX>, Tile::kLds>(
-      dim3(static_cast<unsigned>(nt * mt)), Tile::kWaves * kWave, Tile::kLds, s, a);
+template <int kW, int kX>
+dim3 tile_grid(const F8GemmArgs& a) {
+  const int64_t nt = (a.tiles + kW - 1) / kW;
+  const int64_t mt = a.offsets ? a.T / (16 * kX) + a.experts : (a.T + 16 * kX - 1) / (16 * kX);
+  return dim3(static_cast<unsigned>(nt * mt));
+}
+template <int FX>
+hipError_t go_gemm(const F8GemmArgs& a, hipStream_t s) {
+  return launch_lds<&f8_gemm_kernel<FX>, F8Gemm<FX>::kLds>(tile_grid<16, FX>(a), 256, F8Gemm<FX>::kLds, s, a);
 }
 
 }  // namespace
@@ -302,7 +432,10 @@ hipError_t go_tile(const F8GemmArgs& a, hipStream_t s) {
 // the result's 2^-8.  fp32 results have the same codes multiplied as bf16 values,
 // exactly, with fp32 sums, at half the rate or less.
 hipError_t launch_f8_gemm(const F8GemmArgs& a, int dtype, hipStream_t s) {
-  return dtype == 1 ? go_tile<EBf16, 2, 2, 4, 4>(a, s) : go_tile<EF32, 2, 2, 4, 4>(a, s);
+  if (dtype != 1)
+    return launch_lds<&f8_gemm_exact_kernel, 2 * kExactStage>(tile_grid<kExactTiles, kExactTiles>(a), 256,
+                                                              2 * kExactStage, s, a);
+  return go_gemm<8>(a, s);
 }
 
 hipError_t launch_f8_few(const F8FewArgs& a, int dtype, hipStream_t s) {
