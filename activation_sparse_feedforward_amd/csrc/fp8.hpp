@@ -165,10 +165,11 @@ __device__ __forceinline__ F8Place f8_locate(const int32_t* offsets, int experts
   return p;
 }
 
-// Memory from base on, for the loads below: a base in scalar registers and 32-bit
-// offsets, so that a loop of loads needs no vector registers for addresses.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const uint8_t* base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, 0xffffffffu, 0x00027000);
+// `bytes` of memory from base on, for the loads below: a base in scalar registers
+// and 32-bit offsets, so that a loop of loads needs no vector registers for
+// addresses.  Loads past the bytes give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const uint8_t* base, uint32_t bytes = 0xffffffffu) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes, 0x00027000);
 }
 // 16 bytes a lane straight to LDS: from base + lane_offset + offset (wave-uniform);
 // lane l's go to lds + 16 l (lds wave-uniform).

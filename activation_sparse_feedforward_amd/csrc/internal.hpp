@@ -301,10 +301,12 @@ struct F8FewArgs {
 struct WgradArgs {
   const void *x, *dy;
   float* dw;
+  float* part;  // [parts][experts][N x K] workspace where there are several
   const int32_t* offsets;
   int64_t T, ldx, ldy;
-  int32_t N, K, experts;
+  int32_t N, K, experts, parts;
 };
+int wgrad_parts(int64_t T, int N, int K, int experts);
 
 // dtype: 0 = fp32, 1 = bf16.  Each returns hipSuccess or the launch error.
 hipError_t launch_gate_pack(const PackArgs& a, int dtype, hipStream_t s);

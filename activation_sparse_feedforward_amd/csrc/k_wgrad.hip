@@ -12,6 +12,51 @@
 namespace twell {
 namespace {
 
+// The rows of a workgroup: part blockIdx.z of gridDim.z of an expert's.  The
+// experts with most rows go first (up to 64 experts; among more of them one weighs
+// less), so that what is left at the end is short.
+struct GradRows {
+  int expert;
+  int64_t first, last;
+  float* out;  // the expert's dW, or this part's share of it
+};
+__device__ __forceinline__ GradRows grad_rows(const WgradArgs& a, int unit) {
+  GradRows r{static_cast<int>(blockIdx.y), 0, a.T, nullptr};
+  if (a.offsets) {
+    const int top = static_cast<int>(a.T);
+    int b = 0, n = -1;
+    const int lane = threadIdx.x & 63;
+    auto rows_of = [&](int e) {
+      b = min(max(a.offsets[e], 0), top);
+      n = min(max(a.offsets[e + 1], b), top) - b;
+    };
+    if (a.experts <= 64) {
+      if (lane < a.experts) rows_of(lane);
+      int before = 0;
+      for (int e = 0; e < a.experts; ++e) {
+        const int m = __builtin_amdgcn_readlane(n, e);
+        before += m > n || (m == n && e < lane) ? 1 : 0;
+      }
+      const uint64_t mine = __ballot(lane < a.experts && before == r.expert);
+      r.expert = __builtin_amdgcn_readfirstlane(__builtin_ctzll(mine));
+      b = __builtin_amdgcn_readlane(b, r.expert);
+      n = __builtin_amdgcn_readlane(n, r.expert);
+    } else {
+      rows_of(r.expert);
+    }
+    r.first = b;
+    r.last = b + n;
+  }
+  const int64_t n = r.last - r.first, parts = gridDim.z;
+  if (parts > 1) {
+    const int64_t each = (n + parts * unit - 1) / (parts * unit) * unit, end = r.last;
+    r.first = min(r.first + blockIdx.z * each, end);
+    r.last = min(r.first + each, end);
+  }
+  r.out = (parts > 1 ? a.part : a.dw) + (static_cast<int64_t>(blockIdx.z) * a.experts + r.expert) * a.N * a.K;
+  return r;
+}
+
 constexpr int kGradWaves = 4;  // 2 x 2
 
 // One operand's tile of kTokens x kCols in LDS.
@@ -74,17 +119,11 @@ __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
   using Tl = GradTile<E>;
   __shared__ __align__(16) char lds[2][2 * Tl::kBytes];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = blockIdx.y;
   const int tiles_k = (a.K + 127) / 128;
   const int id = xcd_run(blockIdx.x, gridDim.x);
   const int n0 = id / tiles_k * 128, k0 = id % tiles_k * 128;
-  int64_t first = 0, last = a.T;
-  if (a.offsets) {
-    const int top = static_cast<int>(a.T);
-    const int b = min(max(a.offsets[e], 0), top);
-    first = b;
-    last = min(max(a.offsets[e + 1], b), top);
-  }
+  const GradRows r = grad_rows(a, Tl::kTokens);
+  const int64_t first = r.first, last = r.last;
   const S* dy = static_cast<const S*>(a.dy);
   const S* x = static_cast<const S*>(a.x);
   constexpr int kN = Piece<E>::kN, kPieces = Tl::kCols / kN;  // of a row
@@ -144,7 +183,7 @@ __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
   for (int i = 0; i < 4; ++i) {
     const int n = n0 + cn + 16 * i + (lane & 15);
     if (n >= a.N) continue;
-    float* row = a.dw + (static_cast<int64_t>(e) * a.N + n) * a.K;
+    float* row = r.out + static_cast<int64_t>(n) * a.K;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = k0 + ck + 16 * j + 4 * (lane >> 4);
@@ -153,12 +192,200 @@ __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
   }
 }
 
+// ------------------------------------------------------------------ 256 x 256 tiles, bf16
+// For rows that begin at 16 bytes.  Steps of 32 tokens x 256 columns of dy and of x;
+// a wave fetches a quarter of a step to registers four steps ahead, writes it to
+// LDS two steps ahead, and reads its fragments one step ahead.  128 x 128 a wave,
+// one wave a SIMD: a fragment feeds eight matrix instructions, so that LDS carries
+// 96 bytes a cycle (64 x 64 a wave take 192, which bounds the kernel above).
+// (Direct loads to LDS would save the registers, but the compiler waits for all of
+// them before every transposed read.)
+constexpr int kWide = 256, kWideTokens = 32, kWideRow = kWide * 2;
+constexpr int kWideTile = kWideTokens * kWideRow, kWideStage = 2 * kWideTile, kWideStages = 4;
+constexpr int kWideLds = kWideStages * kWideStage;
+constexpr int kWideLoads = kWideStage / (kGradWaves * 1024);  // of a wave and step
+
+struct WideFrags {
+  bf16x8_t y[8], x[8];
+};
+
+struct WideWork {
+  const char* rows;  // what this wave fetches: the tile's first column in the expert's first row of dy or x
+  int64_t ld;        // bytes
+  int n;             // tokens
+  int left;          // bytes from the tile's first column to the end of a row
+  int wave;
+  uint32_t from, to;  // of a lane's 16 bytes: in two rows of memory, and in a stage
+  uint32_t at[8];     // of a lane's fragments in a tile, for the first 128 columns
+  char* lds;
+
+  // Memory of a step: past the last token, and past the end of its row, loads give zeros.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t step_rows(int step) const {
+    const int t0 = min(step * kWideTokens, n), count = min(n - t0, kWideTokens);
+    const uint32_t bytes = count > 0 ? static_cast<uint32_t>((count - 1) * ld + left) : 0u;
+    return f8_buffer(reinterpret_cast<const uint8_t*>(rows + t0 * ld), __builtin_amdgcn_readfirstlane(bytes));
+  }
+  // Load q of a wave: tokens 2 p and 2 p + 1, p = 8 (wave % 2) + q; waves 0 and 1 of dy, 2 and 3 of x.
+  __device__ __forceinline__ u32x4_t fetch(__amdgpu_buffer_rsrc_t r, int q) const {
+    return buffer16(r, from, ((wave & 1) * kWideLoads + q) * 2 * static_cast<uint32_t>(ld));
+  }
+  // The 32-byte pieces of a row are permuted by its token (GradTile), here by 2 p modulo 8.
+  __device__ __forceinline__ void put(const u32x4_t& v, int q, int step) const {
+    char* p = lds + (step & (kWideStages - 1)) * kWideStage + q * 1024;
+    *reinterpret_cast<u32x4_t*>(p + (to ^ (((2 * q) & 7) * 32))) = v;
+  }
+  // Fragment f of 8: dy's for f < 8, else x's; half h has 16 tokens.
+  __device__ __forceinline__ void read(WideFrags& frags, int f, int h, int step) const {
+    typedef short i16x4_t __attribute__((ext_vector_type(4)));
+    struct Halves {
+      i16x4_t h[2];
+    };
+    const int side = f < 8 ? wave >> 1 : wave & 1;
+    const char* p = lds + (step & (kWideStages - 1)) * kWideStage + (f < 8 ? 0 : kWideTile) + side * 256 +
+                    h * 16 * kWideRow + at[f & 7];
+    bf16x8_t& v = f < 8 ? frags.y[f] : frags.x[f - 8];
+    Halves b = __builtin_bit_cast(Halves, v);
+    b.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(p));
+    v = __builtin_bit_cast(bf16x8_t, b);
+  }
+};
+
+// One step: products of this one's fragments; between them the next one's are read, the one after that, fetched two
+// steps ago, is written, and the one two further on is fetched.
+__device__ __forceinline__ void wide_step(const WideWork& w, int step, const WideFrags& now, WideFrags& next,
+                                          u32x4_t (&fetched)[kWideLoads], f32x4_t (&acc)[8][8]) {
+  const auto rows = w.step_rows(step + 4);
+  // the next step's tiles are written, by all waves
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // rows of the result are x's columns, so that a lane has four of them next to each other
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.x[j], now.y[i], acc[i][j], 0, 0, 0);
+      const int m = i * 8 + j;
+      if (m < 32) {
+        w.read(next, m / 2, m % 2, step + 1);
+      } else if (m < 32 + 2 * kWideLoads) {
+        const int q = (m - 32) / 2;
+        if (m % 2 == 0) w.put(fetched[q], q, step + 2);
+        else fetched[q] = w.fetch(rows, q);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+__global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a) {
+  extern __shared__ __align__(16) char lds_stages[];
+  const int lane = threadIdx.x & 63;
+  const int tiles_k = (a.K + kWide - 1) / kWide;
+  const int id = xcd_run(blockIdx.x, gridDim.x);
+  const int n0 = id / tiles_k * kWide, k0 = id % tiles_k * kWide;
+  const GradRows r = grad_rows(a, kWideTokens);
+  const int64_t first = r.first, last = r.last;
+  WideWork w;
+  w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool of_x = w.wave >= 2;
+  w.ld = (of_x ? a.ldx : a.ldy) * 2;
+  w.rows = static_cast<const char*>(of_x ? a.x : a.dy) + first * w.ld + (of_x ? k0 : n0) * 2;
+  w.n = static_cast<int>(last - first);
+  w.left = (of_x ? a.K - k0 : a.N - n0) * 2;
+  w.lds = lds_stages;
+  w.from = (lane >> 5) * static_cast<uint32_t>(w.ld) + (lane & 31) * 16;
+  w.to = (of_x ? kWideTile : 0) + (w.wave & 1) * kWideLoads * 1024 + (lane >> 5) * kWideRow +
+         (((lane & 31) * 16) ^ ((lane >> 5) * 32));
+  const int token = 4 * (lane >> 4) + ((lane & 15) >> 2);
+#pragma unroll
+  for (int f = 0; f < 8; ++f) w.at[f] = token * kWideRow + (f ^ (token & 7)) * 32 + 8 * (lane & 3);
+
+  f32x4_t acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int steps = (w.n + kWideTokens - 1) / kWideTokens;
+  WideFrags fa, fb;
+  u32x4_t ra[kWideLoads], rb[kWideLoads];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const auto rows = w.step_rows(s);
+#pragma unroll
+    for (int q = 0; q < kWideLoads; ++q) {
+      u32x4_t& v = s & 1 ? rb[q] : ra[q];
+      if (s >= 2) w.put(v, q, s - 2);
+      v = w.fetch(rows, q);
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+  for (int f = 0; f < 16; ++f)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) w.read(fa, f, h, 0);
+  for (int s = 0; s < steps; s += 2) {  // a step past the end adds zeros
+    wide_step(w, s, fa, fb, ra, acc);
+    wide_step(w, s + 1, fb, fa, rb, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int n = n0 + (w.wave >> 1) * 128 + 16 * i + (lane & 15);
+    if (n >= a.N) continue;
+    float* row = r.out + static_cast<int64_t>(n) * a.K;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = k0 + (w.wave & 1) * 128 + 16 * j + 4 * (lane >> 4);
+      if (k < a.K) store_piece<EF32>(row, k, a.K, __builtin_bit_cast(u32x4_t, acc[i][j]));
+    }
+  }
+}
+
+// dW from its parts, in their order.
+__global__ __launch_bounds__(256) void wgrad_sum_kernel(WgradArgs a) {
+  const int64_t n = static_cast<int64_t>(a.experts) * a.N * a.K;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  if (i + 4 > n) {
+    for (int64_t j = i; j < n; ++j) {
+      float s = 0.f;
+      for (int p = 0; p < a.parts; ++p) s += a.part[p * n + j];
+      a.dw[j] = s;
+    }
+    return;
+  }
+  f32x4_t s{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p) s += __builtin_bit_cast(f32x4_t, load16(a.part + p * n + i));
+  store16(a.dw + i, __builtin_bit_cast(u32x4_t, s));
+}
+
+bool whole_pieces(const void* p, int64_t ld, int width) {  // no 16 bytes cross the end of a row; 32 rows stay in 31 bits
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && width % 8 == 0 && ld <= 1 << 24;
+}
+
 }  // namespace
 
+// Parts of each expert's rows: as many as leave a workgroup for every CU, of 256
+// rows at the least on average; a part costs writing and reading dW once more.
+int wgrad_parts(int64_t T, int N, int K, int experts) {
+  const int64_t tiles = static_cast<int64_t>((N + kWide - 1) / kWide) * ((K + kWide - 1) / kWide) * experts;
+  const int64_t by_cus = 256 / tiles, by_rows = T / (256 * static_cast<int64_t>(experts));
+  const int64_t n = by_cus < by_rows ? by_cus : by_rows;
+  return static_cast<int>(n < 1 ? 1 : n > 16 ? 16 : n);
+}
+
 hipError_t launch_wgrad(const WgradArgs& a, int dtype, hipStream_t s) {
-  const dim3 grid(((a.N + 127) / 128) * ((a.K + 127) / 128), a.experts);
-  return dtype == 1 ? launch(wgrad_kernel<EBf16>, grid, kGradWaves * kWave, 0, s, a)
-                    : launch(wgrad_kernel<EF32>, grid, kGradWaves * kWave, 0, s, a);
+  hipError_t e;
+  if (dtype == 1 && whole_pieces(a.dy, a.ldy, a.N) && whole_pieces(a.x, a.ldx, a.K)) {
+    const dim3 grid(((a.N + kWide - 1) / kWide) * ((a.K + kWide - 1) / kWide), a.experts, a.parts);
+    e = launch_lds<&wgrad_wide_kernel, kWideLds>(grid, kGradWaves * kWave, kWideLds, s, a);
+  } else {
+    const dim3 grid(((a.N + 127) / 128) * ((a.K + 127) / 128), a.experts, a.parts);
+    e = dtype == 1 ? launch(wgrad_kernel<EBf16>, grid, kGradWaves * kWave, 0, s, a)
+                   : launch(wgrad_kernel<EF32>, grid, kGradWaves * kWave, 0, s, a);
+  }
+  if (e != hipSuccess || a.parts == 1) return e;
+  const int64_t n = static_cast<int64_t>(a.experts) * a.N * a.K;
+  return launch(wgrad_sum_kernel, dim3(static_cast<unsigned>((n + 1023) / 1024)), 256, 0, s, a);
 }
 
 }  // namespace twell

@@ -329,6 +329,17 @@ Fp8Ws fp8_ws(const twell_fp8_desc* d, int64_t T) {
   return w;
 }
 
+// Of the gradients: dx's product, and before it dw's parts in the same place.
+size_t fp8_bwd_ws(const twell_fp8_desc* d, int64_t T) {
+  const twell_fp8_desc t = transposed(d);
+  const int parts = twell::wgrad_parts(T, d->rows, d->cols, d->experts);
+  const size_t dx = fp8_ws(&t, T).total;
+  const size_t dw = parts == 1 ? 0
+                               : static_cast<size_t>(parts) * static_cast<size_t>(d->experts) *
+                                     static_cast<size_t>(d->rows) * static_cast<size_t>(d->cols) * 4;
+  return dx > dw ? dx : align256(dw);
+}
+
 // y = Q(x) W^T, arguments checked.
 twell_status fp8_product(const twell_fp8_desc* d, const twell_wplanes& p, int64_t T, const int32_t* offsets,
                          int32_t dtype, const void* x, int64_t ldx, void* y, int64_t ldy, void* ws, hipStream_t s) {
@@ -1032,9 +1043,8 @@ twell_status twell_fp8_linear_sizes(const twell_fp8_desc* d, int64_t T, size_t* 
   TWELL_TRY(check_fp8(d));
   if (T < 0 || !ws_fwd || !ws_bwd) return TWELL_EINVAL;
   if (T > kMaxSide) return TWELL_EUNSUPPORTED;
-  const twell_fp8_desc t = transposed(d);
   *ws_fwd = fp8_ws(d, T).total;
-  *ws_bwd = fp8_ws(&t, T).total;
+  *ws_bwd = fp8_bwd_ws(d, T);
   return TWELL_OK;
 }
 
@@ -1067,8 +1077,8 @@ twell_status twell_fp8_linear_bwd(const twell_fp8_desc* d, twell_wplanes w_t, in
     if (dx) {
       TWELL_TRY(check_elems(dx, dtype));
       TWELL_TRY(check_fp8_planes(w_t));
-      if (!ws || !aligned16(ws) || ws_bytes < fp8_ws(&t, T).total) return TWELL_EINVAL;
     }
+    if (!ws || !aligned16(ws) || ws_bytes < fp8_bwd_ws(d, T)) return TWELL_EINVAL;
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dw) {
@@ -1083,6 +1093,8 @@ twell_status twell_fp8_linear_bwd(const twell_fp8_desc* d, twell_wplanes w_t, in
     a.N = d->rows;
     a.K = d->cols;
     a.experts = d->experts;
+    a.parts = twell::wgrad_parts(T, d->rows, d->cols, d->experts);
+    a.part = static_cast<float*>(ws);
     TWELL_TRY(from_hip(twell::launch_wgrad(a, dtype, s)));
   }
   if (!dx || T == 0) return TWELL_OK;

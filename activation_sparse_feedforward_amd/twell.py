@@ -1011,13 +1011,14 @@ def twell_fp8_linear_bwd(desc: Fp8Desc, planes_t: Optional[Weights], x, dy, dx, 
     if x is None and dw is not None:
         raise TypeError("x: expected a torch.Tensor")
     px, ldx = (None, d) if x is None else _rows(x, "x", T, d, dy.dtype, dev)
-    po, ldo, need, pws, planes = None, d, 0, None, CPlanes(None, None)
+    need = _fp8_ws(desc, T)[1]
+    pws = _fit(ws, "ws", need, torch.uint8, dev)
+    po, ldo, planes = None, d, CPlanes(None, None)
     if dx is not None:
         if planes_t is None:
             raise TypeError("planes_t: expected Weights")
         po, ldo = _rows(dx, "dx", T, d, dy.dtype, dev)
-        need = _fp8_ws(desc, T)[1]
-        pws, planes = _fit(ws, "ws", need, torch.uint8, dev), _fp8_planes(desc.transposed, planes_t, "planes_t", dev)
+        planes = _fp8_planes(desc.transposed, planes_t, "planes_t", dev)
     pw = None
     if dw is not None:
         _shaped(dw, "dw", (desc.experts, desc.rows, d))

@@ -490,7 +490,7 @@ twell_status twell_fp8_linear_fwd(const twell_fp8_desc* d, twell_wplanes w, int6
  *   dw_e  = sum_t dy[t] x[t]^T      over expert e's rows
  * dw [experts][rows x cols] fp32, from x and dy themselves with fp32 sums, is
  * overwritten (zeros for an expert without rows).  dx [T x cols] like y above.
- * Either may be NULL; without dw x may be NULL, without dx w_t's pointers and ws. */
+ * Either may be NULL; without dw x may be NULL, without dx w_t's pointers. */
 twell_status twell_fp8_linear_bwd(const twell_fp8_desc* d, twell_wplanes w_t, int64_t T, const int32_t* offsets,
                                   int32_t dtype, const void* x, int64_t ldx, const void* dy, int64_t lddy, void* dx,
                                   int64_t lddx, float* dw, void* ws, size_t ws_bytes, void* stream);
