@@ -139,17 +139,18 @@ __global__ __launch_bounds__(kPackWaves* kWave) void f8_rows_kernel(F8RowsArgs a
   if (p.expert < 0 || p.tile16 >= a.most_tiles) return;
   const int r = lane & 15;
   const S* row = static_cast<const S*>(a.x) + (p.row0 + (r < p.rows ? r : 0)) * a.ldx;
+  F8Inputs<E> in[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) in[j].load(row, (quad * 4 + j) * 128, lane, a.K);  // past the row: zeros
   uint32_t word = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int b = quad * 4 + j;
     if (b >= a.blocks) break;
-    F8Inputs<E> in;
-    in.load(row, b * 128, lane, a.K);
-    const uint32_t byte = f8_scale_byte(max_over_row(in.most()));
+    const uint32_t byte = f8_scale_byte(max_over_row(in[j].most()));
     word |= byte << (8 * j);
     u32x4_t c[2];
-    in.codes(f8_scale(byte), c);
+    in[j].codes(f8_scale(byte), c);
     uint8_t* to = a.codes + (p.tile16 * a.blocks + b) * kF8Bytes + lane * 16;
     *reinterpret_cast<u32x4_t*>(to) = c[0];
     *reinterpret_cast<u32x4_t*>(to + 1024) = c[1];

@@ -59,12 +59,12 @@ __device__ __forceinline__ GradRows grad_rows(const WgradArgs& a, int unit) {
 
 constexpr int kGradWaves = 4;  // 2 x 2
 
-// One operand's tile of kTokens x kCols in LDS.
-template <class E>
+// One operand's tile of kTokens x COLS in LDS.
+template <class E, int COLS>
 struct GradTile;
 template <>
-struct GradTile<EBf16> {
-  static constexpr int kTokens = 32, kCols = 128, kRow = kCols * 2;
+struct GradTile<EBf16, 128> {
+  static constexpr int kTokens = 32, kRow = 128 * 2;
   static constexpr int kBytes = kTokens * kRow;
   // 32-byte pieces of a row are permuted by its token: a read takes 4 tokens a
   // lane group, and those of two groups then lie in different banks
@@ -95,9 +95,9 @@ struct GradTile<EBf16> {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, acc, 0, 0, 0);
   }
 };
-template <>
-struct GradTile<EF32> {
-  static constexpr int kTokens = 32, kCols = 128, kRow = (kCols + 16) * 4;  // 4 tokens in 4 x 16 banks
+template <int COLS>
+struct GradTile<EF32, COLS> {
+  static constexpr int kTokens = 32, kRow = (COLS + 16) * 4;  // 4 tokens in 4 x 16 banks
   static constexpr int kBytes = kTokens * kRow;
   static __device__ __forceinline__ int at(int token, int col) { return token * kRow + col * 4; }
   struct Frag {
@@ -112,21 +112,23 @@ struct GradTile<EF32> {
   }
 };
 
-// A 128 x 128 tile of dW per workgroup, 64 x 64 a wave.
-template <class E>
+// fp32, and bf16 rows of less than 16 bytes: a tile of 32 F x 32 F of dW per
+// workgroup, 16 F x 16 F a wave.
+template <class E, int F>
 __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
   using S = typename E::storage;
-  using Tl = GradTile<E>;
+  constexpr int kCols = 32 * F;
+  using Tl = GradTile<E, kCols>;
   __shared__ __align__(16) char lds[2][2 * Tl::kBytes];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int tiles_k = (a.K + 127) / 128;
+  const int tiles_k = (a.K + kCols - 1) / kCols;
   const int id = xcd_run(blockIdx.x, gridDim.x);
-  const int n0 = id / tiles_k * 128, k0 = id % tiles_k * 128;
+  const int n0 = id / tiles_k * kCols, k0 = id % tiles_k * kCols;
   const GradRows r = grad_rows(a, Tl::kTokens);
   const int64_t first = r.first, last = r.last;
   const S* dy = static_cast<const S*>(a.dy);
   const S* x = static_cast<const S*>(a.x);
-  constexpr int kN = Piece<E>::kN, kPieces = Tl::kCols / kN;  // of a row
+  constexpr int kN = Piece<E>::kN, kPieces = kCols / kN;  // of a row
   constexpr int kEach = Tl::kTokens * kPieces / (kGradWaves * kWave);
   u32x4_t v[2][kEach];
   auto fetch = [&](int64_t t0) {
@@ -151,12 +153,12 @@ __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
       *reinterpret_cast<u32x4_t*>(stage + Tl::kBytes + at) = v[1][i];
     }
   };
-  f32x4_t acc[4][4];
+  f32x4_t acc[F][F];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int cn = (wave >> 1) * 64, ck = (wave & 1) * 64;
+    for (int j = 0; j < F; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int cn = (wave >> 1) * 16 * F, ck = (wave & 1) * 16 * F;
   fetch(first);
   int turn = 0;
   for (int64_t t0 = first; t0 < last; t0 += Tl::kTokens, turn ^= 1) {
@@ -166,26 +168,26 @@ __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
     if (t0 + Tl::kTokens < last) fetch(t0 + Tl::kTokens);
 #pragma unroll
     for (int s = 0; s < Tl::kSteps; ++s) {
-      typename Tl::Frag fx[4];
+      typename Tl::Frag fx[F];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) Tl::read(fx[j], stage + Tl::kBytes, ck + 16 * j, s, lane);
+      for (int j = 0; j < F; ++j) Tl::read(fx[j], stage + Tl::kBytes, ck + 16 * j, s, lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < F; ++i) {
         typename Tl::Frag fy;
         Tl::read(fy, stage, cn + 16 * i, s, lane);
         // rows of the result are x's columns, so that a lane has four of them next to each other
 #pragma unroll
-        for (int j = 0; j < 4; ++j) Tl::mfma(acc[i][j], fx[j], fy);
+        for (int j = 0; j < F; ++j) Tl::mfma(acc[i][j], fx[j], fy);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < F; ++i) {
     const int n = n0 + cn + 16 * i + (lane & 15);
     if (n >= a.N) continue;
     float* row = r.out + static_cast<int64_t>(n) * a.K;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < F; ++j) {
       const int k = k0 + ck + 16 * j + 4 * (lane >> 4);
       if (k < a.K) store_piece<EF32>(row, k, a.K, __builtin_bit_cast(u32x4_t, acc[i][j]));
     }
@@ -193,7 +195,7 @@ __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
 }
 
 // ------------------------------------------------------------------ 256 x 256 tiles, bf16
-// For rows that begin at 16 bytes.  Steps of 32 tokens x 256 columns of dy and of x;
+// Steps of 32 tokens x 256 columns of dy and of x;
 // a wave fetches a quarter of a step to registers four steps ahead, writes it to
 // LDS two steps ahead, and reads its fragments one step ahead.  128 x 128 a wave,
 // one wave a SIMD: a fragment feeds eight matrix instructions, so that LDS carries
@@ -209,13 +211,17 @@ struct WideFrags {
   bf16x8_t y[8], x[8];
 };
 
+// WHOLE: 16 bytes of a row never cross its end, and 32 rows fit 31 bits.  Else
+// they may reach into the row behind, whose values land in columns that are not
+// stored; the last row, which has none behind it, is a step of its own.
+template <bool WHOLE>
 struct WideWork {
-  const char* rows;  // what this wave fetches: the tile's first column in the expert's first row of dy or x
+  const char* rows;  // what this wave fetches: the expert's first row of dy or x (WHOLE: from the tile's first column on)
   int64_t ld;        // bytes
   int n;             // tokens
-  int left;          // bytes from the tile's first column to the end of a row
+  int left;          // WHOLE: bytes from the tile's first column to the end of a row
   int wave;
-  uint32_t from, to;  // of a lane's 16 bytes: in two rows of memory, and in a stage
+  uint32_t from, to;  // of a lane's 16 bytes: in a row (WHOLE: in two rows) of memory, and in a stage
   uint32_t at[8];     // of a lane's fragments in a tile, for the first 128 columns
   char* lds;
 
@@ -225,12 +231,22 @@ struct WideWork {
     const uint32_t bytes = count > 0 ? static_cast<uint32_t>((count - 1) * ld + left) : 0u;
     return f8_buffer(reinterpret_cast<const uint8_t*>(rows + t0 * ld), __builtin_amdgcn_readfirstlane(bytes));
   }
-  // Load q of a wave: tokens 2 p and 2 p + 1, p = 8 (wave % 2) + q; waves 0 and 1 of dy, 2 and 3 of x.
-  __device__ __forceinline__ u32x4_t fetch(__amdgpu_buffer_rsrc_t r, int q) const {
-    return buffer16(r, from, ((wave & 1) * kWideLoads + q) * 2 * static_cast<uint32_t>(ld));
+  // Token of a lane's load q of a wave: 2 p and 2 p + 1, p = 8 (wave % 2) + q; waves 0 and 1 of dy, 2 and 3 of x.
+  __device__ __forceinline__ int token(int q, int step) const {
+    return step * kWideTokens + ((wave & 1) * kWideLoads + q) * 2 + ((threadIdx.x >> 5) & 1);
+  }
+  __device__ __forceinline__ u32x4_t fetch(__amdgpu_buffer_rsrc_t r, int q, int step) const {
+    if constexpr (WHOLE) return buffer16(r, from, ((wave & 1) * kWideLoads + q) * 2 * static_cast<uint32_t>(ld));
+    else return load16(rows + min(token(q, step), n - 1) * ld + from);
   }
   // The 32-byte pieces of a row are permuted by its token (GradTile), here by 2 p modulo 8.
-  __device__ __forceinline__ void put(const u32x4_t& v, int q, int step) const {
+  template <bool ALL = WHOLE>
+  __device__ __forceinline__ void put(u32x4_t v, int q, int step) const {
+    if constexpr (!ALL) {
+      const bool there = token(q, step) < n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = there ? v[i] : 0;
+    }
     char* p = lds + (step & (kWideStages - 1)) * kWideStage + q * 1024;
     *reinterpret_cast<u32x4_t*>(p + (to ^ (((2 * q) & 7) * 32))) = v;
   }
@@ -252,9 +268,11 @@ struct WideWork {
 
 // One step: products of this one's fragments; between them the next one's are read, the one after that, fetched two
 // steps ago, is written, and the one two further on is fetched.
-__device__ __forceinline__ void wide_step(const WideWork& w, int step, const WideFrags& now, WideFrags& next,
+template <bool WHOLE>
+__device__ __forceinline__ void wide_step(const WideWork<WHOLE>& w, int step, const WideFrags& now, WideFrags& next,
                                           u32x4_t (&fetched)[kWideLoads], f32x4_t (&acc)[8][8]) {
-  const auto rows = w.step_rows(step + 4);
+  __amdgpu_buffer_rsrc_t rows;
+  if constexpr (WHOLE) rows = w.step_rows(step + 4);
   // the next step's tiles are written, by all waves
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
@@ -270,12 +288,13 @@ __device__ __forceinline__ void wide_step(const WideWork& w, int step, const Wid
       } else if (m < 32 + 2 * kWideLoads) {
         const int q = (m - 32) / 2;
         if (m % 2 == 0) w.put(fetched[q], q, step + 2);
-        else fetched[q] = w.fetch(rows, q);
+        else fetched[q] = w.fetch(rows, q, step + 4);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
 }
 
+template <bool WHOLE>
 __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a) {
   extern __shared__ __align__(16) char lds_stages[];
   const int lane = threadIdx.x & 63;
@@ -284,15 +303,22 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a) {
   const int n0 = id / tiles_k * kWide, k0 = id % tiles_k * kWide;
   const GradRows r = grad_rows(a, kWideTokens);
   const int64_t first = r.first, last = r.last;
-  WideWork w;
+  WideWork<WHOLE> w;
   w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool of_x = w.wave >= 2;
   w.ld = (of_x ? a.ldx : a.ldy) * 2;
-  w.rows = static_cast<const char*>(of_x ? a.x : a.dy) + first * w.ld + (of_x ? k0 : n0) * 2;
+  w.rows = static_cast<const char*>(of_x ? a.x : a.dy) + first * w.ld;
   w.n = static_cast<int>(last - first);
-  w.left = (of_x ? a.K - k0 : a.N - n0) * 2;
+  const int width = of_x ? a.K : a.N, c0 = of_x ? k0 : n0, c = c0 + (lane & 31) * 8;
+  if constexpr (WHOLE) {
+    w.rows += c0 * 2;
+    w.left = (width - c0) * 2;
+    w.from = (lane >> 5) * static_cast<uint32_t>(w.ld) + (lane & 31) * 16;
+  } else {
+    w.n = max(w.n - 1, 0);
+    w.from = (c < width ? c : 0) * 2;
+  }
   w.lds = lds_stages;
-  w.from = (lane >> 5) * static_cast<uint32_t>(w.ld) + (lane & 31) * 16;
   w.to = (of_x ? kWideTile : 0) + (w.wave & 1) * kWideLoads * 1024 + (lane >> 5) * kWideRow +
          (((lane & 31) * 16) ^ ((lane >> 5) * 32));
   const int token = 4 * (lane >> 4) + ((lane & 15) >> 2);
@@ -305,26 +331,47 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int steps = (w.n + kWideTokens - 1) / kWideTokens;
-  WideFrags fa, fb;
-  u32x4_t ra[kWideLoads], rb[kWideLoads];
+  if (steps > 0) {
+    WideFrags fa, fb;
+    u32x4_t ra[kWideLoads], rb[kWideLoads];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const auto rows = w.step_rows(s);
+    for (int s = 0; s < 4; ++s) {
+      __amdgpu_buffer_rsrc_t rows;
+      if constexpr (WHOLE) rows = w.step_rows(s);
 #pragma unroll
-    for (int q = 0; q < kWideLoads; ++q) {
-      u32x4_t& v = s & 1 ? rb[q] : ra[q];
-      if (s >= 2) w.put(v, q, s - 2);
-      v = w.fetch(rows, q);
+      for (int q = 0; q < kWideLoads; ++q) {
+        u32x4_t& v = s & 1 ? rb[q] : ra[q];
+        if (s >= 2) w.put(v, q, s - 2);
+        v = w.fetch(rows, q, s);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (int f = 0; f < 16; ++f)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w.read(fa, f, h, 0);
+    for (int s = 0; s < steps; s += 2) {  // a step past the end adds zeros
+      wide_step(w, s, fa, fb, ra, acc);
+      wide_step(w, s + 1, fb, fa, rb, acc);
     }
   }
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if (!WHOLE && last > first) {  // the last token, alone in a step
+    const uint16_t* row = reinterpret_cast<const uint16_t*>(w.rows + w.n * w.ld);
+    __syncthreads();
 #pragma unroll
-  for (int f = 0; f < 16; ++f)
+    for (int q = 0; q < kWideLoads; ++q) {
+      u32x4_t v{0, 0, 0, 0};
+      if (w.token(q, 0) == 0) v = load_piece<EBf16>(row, c, width);
+      w.template put<true>(v, q, 0);
+    }
+    __syncthreads();
+    WideFrags f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) w.read(fa, f, h, 0);
-  for (int s = 0; s < steps; s += 2) {  // a step past the end adds zeros
-    wide_step(w, s, fa, fb, ra, acc);
-    wide_step(w, s + 1, fb, fa, rb, acc);
+    for (int i = 0; i < 32; ++i) w.read(f, i / 2, i % 2, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.x[j], f.y[i], acc[i][j], 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -358,6 +405,12 @@ __global__ __launch_bounds__(256) void wgrad_sum_kernel(WgradArgs a) {
   store16(a.dw + i, __builtin_bit_cast(u32x4_t, s));
 }
 
+template <class E, int F>
+hipError_t go_tiles(const WgradArgs& a, hipStream_t s) {
+  const dim3 grid(((a.N + 32 * F - 1) / (32 * F)) * ((a.K + 32 * F - 1) / (32 * F)), a.experts, a.parts);
+  return launch(wgrad_kernel<E, F>, grid, kGradWaves * kWave, 0, s, a);
+}
+
 bool whole_pieces(const void* p, int64_t ld, int width) {  // no 16 bytes cross the end of a row; 32 rows stay in 31 bits
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && width % 8 == 0 && ld <= 1 << 24;
 }
@@ -375,13 +428,19 @@ int wgrad_parts(int64_t T, int N, int K, int experts) {
 
 hipError_t launch_wgrad(const WgradArgs& a, int dtype, hipStream_t s) {
   hipError_t e;
-  if (dtype == 1 && whole_pieces(a.dy, a.ldy, a.N) && whole_pieces(a.x, a.ldx, a.K)) {
+  if (dtype == 1 && a.N >= 8 && a.K >= 8) {
     const dim3 grid(((a.N + kWide - 1) / kWide) * ((a.K + kWide - 1) / kWide), a.experts, a.parts);
-    e = launch_lds<&wgrad_wide_kernel, kWideLds>(grid, kGradWaves * kWave, kWideLds, s, a);
+    if (whole_pieces(a.dy, a.ldy, a.N) && whole_pieces(a.x, a.ldx, a.K))
+      e = launch_lds<&wgrad_wide_kernel<true>, kWideLds>(grid, kGradWaves * kWave, kWideLds, s, a);
+    else
+      e = launch_lds<&wgrad_wide_kernel<false>, kWideLds>(grid, kGradWaves * kWave, kWideLds, s, a);
+  } else if (dtype == 1) {
+    e = go_tiles<EBf16, 4>(a, s);
   } else {
-    const dim3 grid(((a.N + 127) / 128) * ((a.K + 127) / 128), a.experts, a.parts);
-    e = dtype == 1 ? launch(wgrad_kernel<EBf16>, grid, kGradWaves * kWave, 0, s, a)
-                   : launch(wgrad_kernel<EF32>, grid, kGradWaves * kWave, 0, s, a);
+    // fp32 is bound by its matrix instructions: small tiles while there are few workgroups
+    // (777 rows of 5 experts of 1001 x 707: 30 us with 128 x 128, 20 with 64 x 64)
+    const int64_t tiles = static_cast<int64_t>((a.N + 127) / 128) * ((a.K + 127) / 128) * a.experts * a.parts;
+    e = tiles < 1024 ? go_tiles<EF32, 2>(a, s) : go_tiles<EF32, 4>(a, s);
   }
   if (e != hipSuccess || a.parts == 1) return e;
   const int64_t n = static_cast<int64_t>(a.experts) * a.N * a.K;
