@@ -282,19 +282,12 @@ struct F8RowsArgs {
 };
 // y [T x N] = rows times their expert's weights.
 struct F8GemmArgs {
-  const uint8_t *w_codes, *w_scales, *x_codes, *x_scales;
-  void* y;
-  const int32_t* offsets;
-  int64_t T, ldy, most_tiles;
-  int32_t N, tiles, blocks, quads, experts;
-};
-// The same from the rows themselves, where each expert has few.
-struct F8FewArgs {
   const uint8_t *w_codes, *w_scales;
+  const uint8_t *x_codes, *x_scales;  // as F8RowsArgs leaves them
   const void* x;
   void* y;
   const int32_t* offsets;
-  int64_t T, ldx, ldy;
+  int64_t T, ldx, ldy, most_tiles;
   int32_t N, K, tiles, blocks, quads, experts;
 };
 // dw [experts][N x K] = dy^T x over each expert's rows.
@@ -335,8 +328,7 @@ hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t s);
 hipError_t launch_f8_pack(const F8PackArgs& a, int dtype, hipStream_t s);
 hipError_t launch_f8_unpack(const F8PackArgs& a, int dtype, hipStream_t s);
 hipError_t launch_f8_rows(const F8RowsArgs& a, int dtype, hipStream_t s);
-hipError_t launch_f8_gemm(const F8GemmArgs& a, int dtype, hipStream_t s);
-hipError_t launch_f8_few(const F8FewArgs& a, int dtype, hipStream_t s);
+hipError_t launch_f8_product(const F8GemmArgs& a, const F8RowsArgs& rows, int dtype, hipStream_t s);
 hipError_t launch_wgrad(const WgradArgs& a, int dtype, hipStream_t s);
 hipError_t launch_tokens_sort(TokensSortArgs a, hipStream_t s);
 hipError_t launch_tokens_gather(const TokensArgs& a, int dtype, hipStream_t s);

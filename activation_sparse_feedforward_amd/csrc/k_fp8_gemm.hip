@@ -319,97 +319,135 @@ __global__ __launch_bounds__(256) void f8_gemm_exact_kernel(F8GemmArgs a) {
 // ------------------------------------------------------------------ few rows
 // With few rows for each expert what counts is reading the weights once, at
 // memory's rate, and one trip to memory where they are few too: weights go from
-// memory to the matrix core's registers, without LDS.  A workgroup has 16 rows
-// and NT x 16 weight rows; its waves take turns at the blocks of inputs and add
-// their sums through LDS, in the order of the waves.  A wave fetches U blocks of
-// weights, and the rows' inputs, before it uses the first.  Each wave rounds the
-// inputs that it needs itself: one launch, and the same codes every time.
-constexpr int kFewWaves = 8;
+// memory to the matrix core's registers, without LDS.  A workgroup has 16 MT rows
+// and 16 NT weight rows; its waves take turns at the blocks of inputs and add
+// their sums through LDS, in the order of the waves.  A wave fetches two blocks
+// of weights, and the rows' inputs, before it uses the first.
+// CODES: rows come as codes; else each wave rounds the inputs that it needs
+// itself, which saves a launch and costs each workgroup the rounding again.
+constexpr int kFewAhead = 2;
 
-template <class E, int NT, int U>
-__global__ __launch_bounds__(kFewWaves* kWave) void f8_few_kernel(F8FewArgs a) {
+template <class E, int MT, int NT, bool CODES, int WAVES = 8>
+__global__ __launch_bounds__(WAVES* kWave) void f8_few_kernel(F8GemmArgs a) {
   using S = typename E::storage;
   extern __shared__ __align__(16) float lds_sums[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
-  const F8Place p = f8_locate(a.offsets, a.experts, a.T, 16, blockIdx.y);
-  if (p.expert < 0) return;
+  const F8Place p = f8_locate(a.offsets, a.experts, a.T, 16 * MT, blockIdx.y);
+  if (p.expert < 0 || (CODES && p.tile16 + min(p.tiles16, MT) > a.most_tiles)) return;
   const int tile0 = blockIdx.x * NT, r = lane & 15;
-  const S* row = static_cast<const S*>(a.x) + (p.row0 + (r < p.rows ? r : 0)) * a.ldx;
+  const S* row[MT];
+  const uint8_t *xcodes[MT], *xscales[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if constexpr (CODES) {
+      const int64_t t = p.tile16 + min(m, p.tiles16 - 1);
+      xcodes[m] = a.x_codes + t * a.blocks * kF8Bytes + lane * 16;
+      xscales[m] = a.x_scales + t * a.quads * kF8Scales + r * 4;
+    } else {
+      row[m] = static_cast<const S*>(a.x) + (p.row0 + (16 * m + r < p.rows ? 16 * m + r : 0)) * a.ldx;
+    }
+  }
   const uint8_t *codes[NT], *scales[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     // a tile past the matrix is the last one again; its results are not stored
     const int64_t t = static_cast<int64_t>(p.expert) * a.tiles + min(tile0 + i, a.tiles - 1);
-    codes[i] = a.w_codes + t * a.blocks * kF8Bytes;
+    codes[i] = a.w_codes + t * a.blocks * kF8Bytes + lane * 16;
     scales[i] = a.w_scales + t * a.quads * kF8Scales + r * 4;
   }
-  f32x4_t acc[NT];
+  f32x4_t acc[MT][NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int b0 = wave; b0 < a.blocks; b0 += waves * U) {
-    F8Frag w[U][NT];
-    uint32_t sw[U][NT];
-    F8Inputs<E> in[U];
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int b0 = wave; b0 < a.blocks; b0 += waves * kFewAhead) {
+    F8Frag w[kFewAhead][NT], xc[kFewAhead][MT];
+    uint32_t sw[kFewAhead][NT], sx[kFewAhead][MT];
+    F8Inputs<E> in[kFewAhead][MT];
+#pragma unroll
+    for (int u = 0; u < kFewAhead; ++u) {
       const int b = b0 + u * waves;
       if (b < a.blocks) {
+        const int64_t at = static_cast<int64_t>(b) * kF8Bytes;
+        const int scale = (b >> 2) * kF8Scales + (b & 3);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          w[u][i].read(codes[i] + static_cast<int64_t>(b) * kF8Bytes + lane * 16);
-          sw[u][i] = scales[i][(b >> 2) * kF8Scales + (b & 3)];
+          w[u][i].read(codes[i] + at);
+          sw[u][i] = scales[i][scale];
         }
-        in[u].load(row, b * kF8Block, lane, a.K);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (CODES) {
+            xc[u][m].read(xcodes[m] + at);
+            sx[u][m] = xscales[m][scale];
+          } else {
+            in[u][m].load(row[m], b * kF8Block, lane, a.K);
+          }
+        }
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kFewAhead; ++u) {
       if (b0 + u * waves >= a.blocks) break;
-      const uint32_t sx = f8_scale_byte(max_over_row(in[u].most()));
-      F8Frag x;
-      in[u].codes(f8_scale(sx), x.v);
+      Bf16Frag wb[NT];
       if constexpr (E::kBytes == 4) {
-        Bf16Frag xb;
-        xb.from(x, sx);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          Bf16Frag wb;
-          wb.from(w[u][i], sw[u][i]);
-          bf16_mfma(acc[i], wb, xb);
+        for (int i = 0; i < NT; ++i) wb[i].from(w[u][i], sw[u][i]);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if constexpr (!CODES) {
+          sx[u][m] = f8_scale_byte(max_over_row(in[u][m].most()));
+          in[u][m].codes(f8_scale(sx[u][m]), xc[u][m].v);
         }
-      } else {
+        if constexpr (E::kBytes == 4) {
+          Bf16Frag xb;
+          xb.from(xc[u][m], sx[u][m]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) f8_mfma(acc[i], w[u][i], sw[u][i], x, sx);
+          for (int i = 0; i < NT; ++i) bf16_mfma(acc[m][i], wb[i], xb);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) f8_mfma(acc[m][i], w[u][i], sw[u][i], xc[u][m], sx[u][m]);
+        }
       }
     }
   }
+  constexpr int kSums = MT * NT;
   if (waves > 1) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-      *reinterpret_cast<f32x4_t*>(lds_sums + ((wave * NT + i) * kWave + lane) * 4) = acc[i];
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        *reinterpret_cast<f32x4_t*>(lds_sums + ((wave * kSums + m * NT + i) * kWave + lane) * 4) = acc[m][i];
     __syncthreads();
   }
-  for (int i = wave; i < NT; i += waves) {
-    f32x4_t sum = acc[0];
-    if (waves > 1) {
-      sum = *reinterpret_cast<const f32x4_t*>(lds_sums + (i * kWave + lane) * 4);
-      for (int v = 1; v < waves; ++v) sum += *reinterpret_cast<const f32x4_t*>(lds_sums + ((v * NT + i) * kWave + lane) * 4);
-    } else {
 #pragma unroll
-      for (int j = 1; j < NT; ++j) sum = i == j ? acc[j] : sum;
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int at = m * NT + i;
+      if (at % waves != wave) continue;
+      f32x4_t sum = acc[m][i];
+      if (waves > 1) {
+        sum = *reinterpret_cast<const f32x4_t*>(lds_sums + (at * kWave + lane) * 4);
+        for (int v = 1; v < waves; ++v)
+          sum += *reinterpret_cast<const f32x4_t*>(lds_sums + ((v * kSums + at) * kWave + lane) * 4);
+      }
+      const int n = (tile0 + i) * 16 + 4 * (lane >> 4);
+      if (16 * m + r < p.rows && n < a.N) store_acc<E>(a, p.row0 + 16 * m + r, n, sum);
     }
-    const int n = (tile0 + i) * 16 + 4 * (lane >> 4);
-    if (r < p.rows && n < a.N) store_acc<E>(a, p.row0 + r, n, sum);
-  }
 }
 
-template <class E, int NT, int U>
-hipError_t go_few(const F8FewArgs& a, hipStream_t s) {
-  int waves = kFewWaves;
+template <class E, int MT, int NT, bool CODES, int WAVES = 8>
+hipError_t go_few(const F8GemmArgs& a, hipStream_t s) {
+  int waves = WAVES;
   while (waves > 1 && waves > a.blocks) waves >>= 1;
-  const dim3 grid((a.tiles + NT - 1) / NT, static_cast<unsigned>(a.offsets ? a.T / 16 + a.experts : (a.T + 15) / 16));
-  return launch(f8_few_kernel<E, NT, U>, grid, waves * kWave, waves * NT * kWave * 16, s, a);
+  constexpr int kUnit = 16 * MT;
+  const int64_t mt = a.offsets ? a.T / kUnit + a.experts : (a.T + kUnit - 1) / kUnit;
+  const dim3 grid((a.tiles + NT - 1) / NT, static_cast<unsigned>(mt));
+  constexpr size_t kPerWave = MT * NT * kWave * 16;
+  return launch_lds<&f8_few_kernel<E, MT, NT, CODES, WAVES>, WAVES * kPerWave>(grid, waves * kWave, waves * kPerWave, s, a);
 }
 
 template <int kW, int kX>
@@ -431,15 +469,53 @@ hipError_t go_gemm(const F8GemmArgs& a, hipStream_t s) {
 // of each 8 (1.35e-5 of its norm for Gaussian data); a code's own rounding is 2^-4,
 // the result's 2^-8.  fp32 results have the same codes multiplied as bf16 values,
 // exactly, with fp32 sums, at half the rate or less.
-hipError_t launch_f8_gemm(const F8GemmArgs& a, int dtype, hipStream_t s) {
-  if (dtype != 1)
+//
+// Which kernel: by estimates of the times in us, whose constants were fitted to
+// 300 measured calls (1 to 8192 rows of 512 x 700 to 11008 x 4096, 1 to 64
+// experts); the kernel taken is the fastest there or within a tenth of it, some
+// cases of up to 17 us aside.  Replayed, of 8192 x 2048 in bf16:
+//   rows                          1     16    32    64    128   256   512   1024
+//   rounding on the way, 16 x 32  6.3   6.8   9.5   15.4  26.9  49
+//                        32 x 32              8.7   15.1  27.3
+//   codes,               32 x 32  9.5   10.6  10.7  12.3  16.1  23.8  39
+//                        64 x 64              13.0  13.4  13.8  20.5  34    60
+//   codes through LDS,   64 x 256 17.9  19.1  19.6  20.7  20.6  21.1  22.9  30.6
+//                       128 x 256 19.9  21.0  21.5  22.4  24.6  24.8  25.9  29.6
+hipError_t launch_f8_product(const F8GemmArgs& a, const F8RowsArgs& rows, int dtype, hipStream_t s) {
+  const bool bf16 = dtype == 1;
+  auto row_tiles = [&](int64_t unit) { return a.offsets ? a.T / unit + a.experts : (a.T + unit - 1) / unit; };
+  const int64_t pairs = (a.tiles + 1) / 2, quads = (a.tiles + 3) / 4, blocks = a.blocks;
+  // long fp32 rows take longer to round in every workgroup than their codes' launch
+  const bool on_the_way = bf16 || a.T == 1 || blocks <= 32;
+  if (on_the_way && a.T <= 16 * static_cast<int64_t>(a.experts)) {
+    if (row_tiles(16) * pairs < 256)  // few workgroups: half as large, and twice the waves to share the inputs
+      return bf16 ? go_few<EBf16, 1, 1, false, 16>(a, s) : go_few<EF32, 1, 1, false, 16>(a, s);
+    return bf16 ? go_few<EBf16, 1, 2, false>(a, s) : go_few<EF32, 1, 2, false>(a, s);
+  }
+  if (on_the_way && row_tiles(16) * pairs * blocks <= (bf16 ? 8192 : 4096)) {
+    if (row_tiles(16) * pairs <= 256) return bf16 ? go_few<EBf16, 1, 2, false>(a, s) : go_few<EF32, 1, 2, false>(a, s);
+    return bf16 ? go_few<EBf16, 2, 2, false>(a, s) : go_few<EF32, 2, 2, false>(a, s);
+  }
+  const hipError_t e = launch_f8_rows(rows, dtype, s);
+  if (e != hipSuccess) return e;
+  // an expert's last tile is half full on average
+  const double tiles64 = a.offsets ? a.T / 64.0 + 0.5 * a.experts : static_cast<double>(row_tiles(64));
+  const double few = (bf16 ? 1.4e-3 : 2.4e-3) * tiles64 * quads * blocks;
+  if (bf16) {
+    const double rounds = tiles64 * ((a.tiles + 15) / 16) / 512;
+    if (0.75 * blocks * (rounds > 1 ? rounds : 1) <= few) {
+      // tiles of 128 rows that an expert fills half cost as much as full ones
+      const double tiles128 = a.offsets ? a.T / 128.0 + 0.5 * a.experts : static_cast<double>(row_tiles(128));
+      const bool large = tiles128 * ((a.tiles + 15) / 16) > (a.offsets ? 256 : 159);
+      return large ? go_gemm<8>(a, s) : go_gemm<4>(a, s);
+    }
+    return row_tiles(64) * quads >= 256 ? go_few<EBf16, 4, 4, true>(a, s) : go_few<EBf16, 2, 2, true>(a, s);
+  }
+  const double rounds = 0.5 * tiles64 * ((a.tiles + 7) / 8) / 512;
+  if (1.35 * blocks * (rounds > 1 ? rounds : 1) <= few)
     return launch_lds<&f8_gemm_exact_kernel, 2 * kExactStage>(tile_grid<kExactTiles, kExactTiles>(a), 256,
                                                               2 * kExactStage, s, a);
-  return go_gemm<8>(a, s);
-}
-
-hipError_t launch_f8_few(const F8FewArgs& a, int dtype, hipStream_t s) {
-  return dtype == 1 ? go_few<EBf16, 2, 2>(a, s) : go_few<EF32, 2, 2>(a, s);
+  return row_tiles(64) * pairs >= 256 ? go_few<EF32, 4, 2, true>(a, s) : go_few<EF32, 2, 2, true>(a, s);
 }
 
 }  // namespace twell

@@ -345,24 +345,6 @@ twell_status fp8_product(const twell_fp8_desc* d, const twell_wplanes& p, int64_
                          int32_t dtype, const void* x, int64_t ldx, void* y, int64_t ldy, void* ws, hipStream_t s) {
   const Fp8Ws w = fp8_ws(d, T);
   const int32_t blocks = blocks_of(d->cols);
-  if (T <= 16 * static_cast<int64_t>(d->experts)) {
-    twell::F8FewArgs f{};
-    f.w_codes = static_cast<const uint8_t*>(p.codes);
-    f.w_scales = static_cast<const uint8_t*>(p.scales);
-    f.x = x;
-    f.y = y;
-    f.offsets = offsets;
-    f.T = T;
-    f.ldx = ldx;
-    f.ldy = ldy;
-    f.N = d->rows;
-    f.K = d->cols;
-    f.tiles = tiles_of(d->rows);
-    f.blocks = blocks;
-    f.quads = quads_of(blocks);
-    f.experts = d->experts;
-    return from_hip(twell::launch_f8_few(f, dtype, s));
-  }
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   twell::F8RowsArgs r{};
   r.x = x;
@@ -376,12 +358,14 @@ twell_status fp8_product(const twell_fp8_desc* d, const twell_wplanes& p, int64_
   r.blocks = blocks;
   r.quads = quads_of(blocks);
   r.experts = d->experts;
-  TWELL_TRY(from_hip(twell::launch_f8_rows(r, dtype, s)));
   twell::F8GemmArgs g{};
   g.w_codes = static_cast<const uint8_t*>(p.codes);
   g.w_scales = static_cast<const uint8_t*>(p.scales);
   g.x_codes = r.codes;
   g.x_scales = r.scales;
+  g.x = x;
+  g.ldx = ldx;
+  g.K = d->cols;
   g.y = y;
   g.offsets = offsets;
   g.T = T;
@@ -392,7 +376,7 @@ twell_status fp8_product(const twell_fp8_desc* d, const twell_wplanes& p, int64_
   g.blocks = blocks;
   g.quads = r.quads;
   g.experts = d->experts;
-  return from_hip(twell::launch_f8_gemm(g, dtype, s));
+  return from_hip(twell::launch_f8_product(g, r, dtype, s));
 }
 
 }  // namespace
