@@ -244,7 +244,6 @@ struct TokensArgs {
 
 // Layer norm.
 constexpr int kNormMostWidth = 16384;
-constexpr int kNormMostBlocks = 1024;
 struct NormArgs {
   const void* x;
   const void* w;  // or null: ones
@@ -260,7 +259,7 @@ struct NormArgs {
   int32_t d, blocks;
   float eps;
 };
-int norm_blocks(int64_t T);
+int norm_blocks(int64_t T, int d, int dtype);
 
 // Weights in e4m3 (fp8.hpp): E matrices of N rows x K inputs, and transposed.
 struct F8PackArgs {

@@ -114,67 +114,101 @@ __global__ __launch_bounds__((W == 1 ? 4 : W) * kWave) void norm_fwd_kernel(Norm
 
 // A workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its share of dw
 // and db in registers, which it writes to part[blockIdx.x][2][d] at the end:
-// sums over tokens then take a fixed order.
+// sums over tokens then take a fixed order.  The next row is on its way while one
+// is summed and written.
 template <class E, class EW, int W, int U>
 __global__ __launch_bounds__(W* kWave) void norm_bwd_kernel(NormArgs a) {
   using S = typename E::storage;
   using P = Piece<E>;
   constexpr int kN = P::kN;
+  constexpr bool kWeights = U * kN <= 12;  // kept in registers; else read again for each row, from the caches
+  constexpr bool kValues = W * U < 48;     // likewise h and dy w, else worked out twice from the row's pieces
   __shared__ float lds[2][2 * W];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int c0 = (wave * U * kWave + lane) * kN;
   constexpr int kStep = kWave * kN;
-  float w[U][kN], dw[U][kN], db[U][kN];
+  float w[kWeights ? U : 1][kN], dw[U][kN], db[U][kN];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    load_weights<E, EW>(a.w, c0 + u * kStep, a.d, 1.f, w[u]);
+    if constexpr (kWeights) load_weights<E, EW>(a.w, c0 + u * kStep, a.d, 1.f, w[u]);
 #pragma unroll
     for (int j = 0; j < kN; ++j) dw[u][j] = db[u][j] = 0.f;
   }
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  int turn = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+  struct Row {
+    u32x4_t x[U], g[U];
+    float mean, rstd;
+  };
+  Row row;
+  auto fetch = [&](Row& r, int64_t t) {
+    if (t >= a.T) return;
     const S* x = static_cast<const S*>(a.x) + t * a.ldx;
     const S* dy = static_cast<const S*>(a.dy) + t * a.ldy;
-    const float mean = a.stats_in[2 * t], rstd = a.stats_in[2 * t + 1];
-    float h[U][kN], g[U][kN];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      r.x[u] = load_piece<E>(x, c0 + u * kStep, a.d);
+      r.g[u] = load_piece<E>(dy, c0 + u * kStep, a.d);
+    }
+    r.mean = a.stats_in[2 * t];
+    r.rstd = a.stats_in[2 * t + 1];
+  };
+  // h and dy of piece u of a row
+  auto values = [&](const Row& r, int u, float* h, float* g) {
+    P::unpack(r.x[u], h);
+    P::unpack(r.g[u], g);
+    if constexpr (!kWeights) load_weights<E, EW>(a.w, c0 + u * kStep, a.d, 1.f, w[0]);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) h[j] = c0 + u * kStep + j < a.d ? (h[j] - r.mean) * r.rstd : 0.f;
+  };
+  fetch(row, blockIdx.x);
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    constexpr int kHeld = kValues ? U : 1;
+    float h[kHeld][kN], g[kHeld][kN];
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * kStep;
-      P::unpack(load_piece<E>(x, c, a.d), h[u]);
-      P::unpack(load_piece<E>(dy, c, a.d), g[u]);
+      const int q = kValues ? u : 0;
+      values(row, u, h[q], g[q]);
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
-        h[u][j] = c + j < a.d ? (h[u][j] - mean) * rstd : 0.f;
-        dw[u][j] = fmaf(g[u][j], h[u][j], dw[u][j]);
-        db[u][j] += g[u][j];
-        g[u][j] *= w[u][j];
-        s[0] += g[u][j];
-        s[1] = fmaf(g[u][j], h[u][j], s[1]);
+        dw[u][j] = fmaf(g[q][j], h[q][j], dw[u][j]);
+        db[u][j] += g[q][j];
+        g[q][j] *= w[kWeights ? u : 0][j];
+        s[0] += g[q][j];
+        s[1] = fmaf(g[q][j], h[q][j], s[1]);
       }
     }
+    const float r = row.rstd;
+    const Row same = row;
+    fetch(row, t + gridDim.x);
     across_waves<W>(s, lds[turn]);  // two turns: a wave may be one row ahead of another
     S* dx = static_cast<S*>(a.dx) + t * a.lddx;
     const float m0 = s[0] * inv_d, m1 = s[1] * inv_d;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      const int q = kValues ? u : 0;
+      if constexpr (!kValues) {
+        values(same, u, h[0], g[0]);
 #pragma unroll
-      for (int j = 0; j < kN; ++j) g[u][j] = rstd * (g[u][j] - m0 - h[u][j] * m1);
-      store_piece<E>(dx, c0 + u * kStep, a.d, P::pack(g[u]));
+        for (int j = 0; j < kN; ++j) g[0][j] *= w[kWeights ? u : 0][j];
+      }
+#pragma unroll
+      for (int j = 0; j < kN; ++j) g[q][j] = r * (g[q][j] - m0 - h[q][j] * m1);
+      store_piece<E>(dx, c0 + u * kStep, a.d, P::pack(g[q]));
     }
   }
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.d;
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int u = 0; u < U; ++u) {
+    const int c = c0 + u * kStep;
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int c = c0 + u * kStep + j;
-      if (c < a.d) {
-        part[c] = dw[u][j];
-        part[a.d + c] = db[u][j];
-      }
+    for (int i = 0; i < kN; i += 4) {
+      if (c + i >= a.d) continue;
+      store_piece<EF32>(part, c + i, a.d, Piece<EF32>::pack(dw[u] + i));
+      store_piece<EF32>(part + a.d, c + i, a.d, Piece<EF32>::pack(db[u] + i));
     }
+  }
 }
 
 // dw and db: column sums of part, parts in a fixed order.
@@ -219,12 +253,19 @@ template <class E, class EW>
 hipError_t go_rows_bwd(const NormArgs& a, hipStream_t s) {
   constexpr int kOne = kWave * Piece<E>::kN;
   const dim3 grid(a.blocks);
+  if (a.d <= kOne) return launch(norm_bwd_kernel<E, EW, 1, 1>, grid, 1 * kWave, 0, s, a);
+  if (a.d <= 2 * kOne) return launch(norm_bwd_kernel<E, EW, 2, 1>, grid, 2 * kWave, 0, s, a);
   if (a.d <= 4 * kOne) return launch(norm_bwd_kernel<E, EW, 4, 1>, grid, 4 * kWave, 0, s, a);
-  if (a.d <= 8 * kOne) return launch(norm_bwd_kernel<E, EW, 4, 2>, grid, 4 * kWave, 0, s, a);
+  if (a.d <= 8 * kOne) return launch(norm_bwd_kernel<E, EW, 8, 1>, grid, 8 * kWave, 0, s, a);
   if (a.d <= 16 * kOne) return launch(norm_bwd_kernel<E, EW, 16, 1>, grid, 16 * kWave, 0, s, a);
-  if constexpr (32 * kOne < kNormMostWidth)
-    if (a.d > 32 * kOne) return launch(norm_bwd_kernel<E, EW, 16, 4>, grid, 16 * kWave, 0, s, a);
-  return launch(norm_bwd_kernel<E, EW, 16, 2>, grid, 16 * kWave, 0, s, a);
+  if constexpr (E::kBytes == 2) {  // 16 waves have too few registers for two pieces of bf16
+    if (a.d <= 24 * kOne) return launch(norm_bwd_kernel<E, EW, 8, 3>, grid, 8 * kWave, 0, s, a);
+    return launch(norm_bwd_kernel<E, EW, 8, 4>, grid, 8 * kWave, 0, s, a);
+  } else {
+    if (a.d <= 32 * kOne) return launch(norm_bwd_kernel<E, EW, 16, 2>, grid, 16 * kWave, 0, s, a);
+    if (a.d <= 48 * kOne) return launch(norm_bwd_kernel<E, EW, 16, 3>, grid, 16 * kWave, 0, s, a);
+    return launch(norm_bwd_kernel<E, EW, 16, 4>, grid, 16 * kWave, 0, s, a);
+  }
 }
 template <class E, class EW>
 hipError_t go_bwd(const NormArgs& a, hipStream_t s) {
@@ -235,7 +276,15 @@ hipError_t go_bwd(const NormArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int norm_blocks(int64_t T) { return static_cast<int>(T < kNormMostBlocks ? T : kNormMostBlocks); }
+// Workgroups of the backward kernel.  Each writes 2 d sums, which norm_sum_kernel
+// reads: more of them cost more there, fewer have fewer loads under way.  (16384
+// rows of 2048 in bf16, 4 waves a row: 48 us with 256, 37.4 with 512, 38.6 with 1024;
+// of 4096, 8 waves: 79 with 256, 81 with 512; 2000 rows of 2048: 12.9, 13.9, 18.2.)
+int norm_blocks(int64_t T, int d, int dtype) {
+  const int waves = (d + (dtype == 1 ? 511 : 255)) / (dtype == 1 ? 512 : 256);  // of a row, with one piece a lane
+  const int64_t most = waves == 1 ? 2048 : waves <= 4 ? 1024 : 256, wanted = waves <= 4 ? (T + 3) / 4 : (T + 1) / 2;
+  return static_cast<int>(wanted < most ? wanted : most);
+}
 
 hipError_t launch_norm_fwd(const NormArgs& a, int dtype, int w_dtype, hipStream_t s) {
   if (dtype == 1) return w_dtype == 1 ? go_fwd<EBf16, EBf16>(a, s) : go_fwd<EBf16, EF32>(a, s);

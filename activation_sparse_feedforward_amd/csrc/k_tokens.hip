@@ -19,7 +19,7 @@ namespace {
 // rounds of the wave + in lower lanes of the round.
 constexpr int kSortWaves = 16;
 constexpr int kSortMostBlocks = 256;
-constexpr int kSortRun = 4096;  // pairs a workgroup has at the least, where there are several
+constexpr int kSortRun = 16384;  // pairs a workgroup has at the least, where there are several
 
 __device__ __forceinline__ void wave_handoff() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

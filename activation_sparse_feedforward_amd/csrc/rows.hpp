@@ -51,17 +51,36 @@ struct Piece<EF32> {
   }
 };
 
+// v's bytes moved down by `bytes` (1 .. 15), zeros from above.
+__device__ __forceinline__ u32x4_t shifted_down(const u32x4_t& v, int bytes) {
+  uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32, hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
+  const int s = 8 * (bytes & 7);
+  if (bytes & 8) {
+    lo = hi;
+    hi = 0;
+  }
+  lo = lo >> s | hi << 1 << (63 - s);
+  hi >>= s;
+  return u32x4_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                 static_cast<uint32_t>(hi >> 32)};
+}
+
 // Elements [c, c + kN) of a row of n elements; what is past its end reads as
-// zero and is not written.  c is a multiple of kN.
+// zero and is not written.  c is a multiple of kN.  The last piece of a row is read
+// as its last 16 bytes and moved down: one load (element by element it was eight,
+// one after another; layer norm's gradients of 16384 rows of 4099 in bf16 took 226 us).
 template <class E>
 __device__ __forceinline__ u32x4_t load_piece(const typename E::storage* row, int c, int n) {
-  if (c + Piece<E>::kN <= n) return load16(row + c);
+  constexpr int kN = Piece<E>::kN;
+  if (c + kN <= n) return load16(row + c);
   u32x4_t v{0, 0, 0, 0};
+  if (c >= n) return v;
+  if (n >= kN) return shifted_down(load16(row + n - kN), (c + kN - n) * E::kBytes);
 #pragma unroll
-  for (int i = 0; i < Piece<E>::kN; ++i) {
-    if (c + i >= n) continue;
-    if constexpr (E::kBytes == 2) v[i / 2] |= static_cast<uint32_t>(row[c + i]) << (16 * (i % 2));
-    else v[i] = __float_as_uint(row[c + i]);
+  for (int i = 0; i < kN; ++i) {  // a row of less than 16 bytes
+    if (i >= n) continue;
+    if constexpr (E::kBytes == 2) v[i / 2] |= static_cast<uint32_t>(row[i]) << (16 * (i % 2));
+    else v[i] = __float_as_uint(row[i]);
   }
   return v;
 }

@@ -259,7 +259,7 @@ twell_status check_norm(const twell_norm_desc* d) {
 }
 // Each workgroup's sums of dw and db.
 size_t norm_ws(const twell_norm_desc* d) {
-  return align256(static_cast<size_t>(twell::norm_blocks(d->T)) * 2 * d->d_model * 4);
+  return align256(static_cast<size_t>(twell::norm_blocks(d->T, d->d_model, d->dtype)) * 2 * d->d_model * 4);
 }
 twell::NormArgs norm_args(const twell_norm_desc* d) {
   twell::NormArgs a{};
@@ -268,7 +268,7 @@ twell::NormArgs norm_args(const twell_norm_desc* d) {
   a.ldy = d->ldy;
   a.lddx = d->lddx;
   a.d = d->d_model;
-  a.blocks = twell::norm_blocks(d->T);
+  a.blocks = twell::norm_blocks(d->T, d->d_model, d->dtype);
   a.eps = d->eps;
   return a;
 }
