@@ -19,7 +19,9 @@ namespace {
 // rounds of the wave + in lower lanes of the round.
 constexpr int kSortWaves = 16;
 constexpr int kSortMostBlocks = 256;
-constexpr int kSortRun = 16384;  // pairs a workgroup has at the least, where there are several
+constexpr int kSortAlone = 4096;  // pairs that one workgroup sorts alone, in one launch (6.0 us replayed; 16000: 15.4)
+constexpr int kSortRun = 2048;    // else pairs of a workgroup, at the least (131072 of 64 experts in us: 11.3 with 1024,
+                                  // 9.8, 10.4 with 4096; 16000: 7.0, 7.6, 7.8)
 
 __device__ __forceinline__ void wave_handoff() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -306,8 +308,9 @@ hipError_t go_combine_bwd(const TokensArgs& a, hipStream_t s) {
 }  // namespace
 
 int tokens_sort_blocks(int64_t pairs) {
+  if (pairs <= kSortAlone) return 1;
   const int64_t n = (pairs + kSortRun - 1) / kSortRun;
-  return static_cast<int>(n < 1 ? 1 : n < kSortMostBlocks ? n : kSortMostBlocks);
+  return static_cast<int>(n < kSortMostBlocks ? n : kSortMostBlocks);
 }
 
 hipError_t launch_tokens_sort(TokensSortArgs a, hipStream_t s) {

@@ -714,6 +714,10 @@ class TokensDesc(_Keeping):
     def pairs(self) -> int:
         return self.T * self.top_k
 
+    @functools.cached_property
+    def _choices(self) -> tuple:
+        return (self.T, self.top_k)
+
     def _strided(self, ld_tokens: int, ld_rows: int):
         return ctypes.byref(CTokensDesc(
             **_c_ints(64, T=self.T, ld_tokens=ld_tokens, ld_rows=ld_rows),
@@ -766,6 +770,10 @@ class NormDesc(_Keeping):
         d = self.d_model
         return self._strided(TWELL_FP32, d, d, d), self._strided(TWELL_BF16, d, d, d)
 
+    @functools.cached_property
+    def _row(self) -> tuple:
+        return (self.d_model,)
+
     def _at(self, w_dtype: int, ldx: int, ldy: int, lddx: int):
         return (self._refs[w_dtype] if ldx == ldy == lddx == self.d_model else self._strided(w_dtype, ldx, ldy, lddx))
 
@@ -792,15 +800,18 @@ def alloc_norm_ws(desc: NormDesc, device="cuda") -> torch.Tensor:
 
 def _exactly(t, name: str, shape: tuple, dtype: torch.dtype, dev: int) -> int:
     """Pointer of a contiguous tensor of just this shape and dtype on GPU dev."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.get_device() == dev and t.dtype is dtype
+            and t.is_contiguous()):
+        return t.data_ptr()
     if isinstance(t, torch.Tensor) and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    return _fit(t, name, 0, dtype, dev)
+    return _fit(t, name, 0, dtype, dev)  # says what is wrong
 
 
 def twell_tokens_sort(desc: TokensDesc, ids, order: TokensOrder, ws, stream=None):
     """The order of pairs by expert: ids int32 [T, top_k] to order.offsets and order.pair_row (see include/twell.h)."""
     dev = _device(ids, "ids")
-    shape = (desc.T, desc.top_k)
+    shape = desc._choices
     st = library().twell_tokens_sort(
         desc._ref, _exactly(ids, "ids", shape, torch.int32, dev),
         _exactly(order.offsets, "order.offsets", (desc.experts + 1,), torch.int32, dev),
@@ -816,7 +827,7 @@ def twell_tokens_gather(desc: TokensDesc, x, order: TokensOrder, rows, stream=No
     px, ldx = _rows(x, "x", desc.T, d, dt, dev)
     pr, ldr = _rows(rows, "rows", desc.pairs, d, dt, dev)
     st = library().twell_tokens_gather(
-        desc._at(ldx, ldr), px, _exactly(order.pair_row, "order.pair_row", (desc.T, desc.top_k), torch.int32, dev), pr,
+        desc._at(ldx, ldr), px, _exactly(order.pair_row, "order.pair_row", desc._choices, torch.int32, dev), pr,
         _stream_on(dev, stream))
     if st:
         _check("twell_tokens_gather", st)
@@ -825,7 +836,7 @@ def twell_tokens_gather(desc: TokensDesc, x, order: TokensOrder, rows, stream=No
 def twell_tokens_combine(desc: TokensDesc, rows, order: TokensOrder, weights, y, stream=None):
     """y[t] = sum of weights[t, i] rows[pair_row[t, i]]; weights fp32 [T, top_k], or None for ones."""
     dev, dt, d = _device(rows, "rows"), desc.torch_dtype, desc.d_model
-    shape = (desc.T, desc.top_k)
+    shape = desc._choices
     pr, ldr = _rows(rows, "rows", desc.pairs, d, dt, dev)
     py, ldy = _rows(y, "y", desc.T, d, dt, dev)
     st = library().twell_tokens_combine(
@@ -840,7 +851,7 @@ def twell_tokens_combine_bwd(desc: TokensDesc, rows, order: TokensOrder, weights
     """Gradients of twell_tokens_combine with weights: drows [T * top_k, d_model] and dweights fp32 [T, top_k], either
     of them None if it is not wanted (rows may be None without dweights)."""
     dev, dt, d = _device(dy, "dy"), desc.torch_dtype, desc.d_model
-    shape = (desc.T, desc.top_k)
+    shape = desc._choices
     pg, ldg = _rows(dy, "dy", desc.T, d, dt, dev)
     if rows is None and dweights is not None:
         raise TypeError("rows: expected a torch.Tensor")
@@ -856,9 +867,13 @@ def twell_tokens_combine_bwd(desc: TokensDesc, rows, order: TokensOrder, weights
 
 
 def _norm_weights(desc: NormDesc, w, b, dev: int) -> tuple:
-    code = TWELL_FP32 if w is None and b is None else _any_dtype(b if w is None else w, "b" if w is None else "w")
-    dtype = torch.bfloat16 if code == TWELL_BF16 else torch.float32
-    return (code, *(None if t is None else _exactly(t, n, (desc.d_model,), dtype, dev) for t, n in ((w, "w"), (b, "b"))))
+    """Their dtype's code, and pointers or None."""
+    some = b if w is None else w
+    if some is None:
+        return TWELL_FP32, None, None
+    code, shape, dtype = _any_dtype(some, "b" if w is None else "w"), desc._row, some.dtype
+    return (code, None if w is None else _exactly(w, "w", shape, dtype, dev),
+            None if b is None else _exactly(b, "b", shape, dtype, dev))
 
 
 def twell_layernorm_fwd(desc: NormDesc, x, w, b, y, stats=None, stream=None):
@@ -899,6 +914,10 @@ class Fp8Desc(_Keeping):
     cols: int
 
     @functools.cached_property
+    def _ws(self) -> dict:
+        return {}  # workspace bytes by rows
+
+    @functools.cached_property
     def transposed(self) -> "Fp8Desc":
         return Fp8Desc(self.experts, self.cols, self.rows)
 
@@ -914,13 +933,18 @@ class Fp8Desc(_Keeping):
         return int(out.codes), int(out.scales)
 
 
-@functools.lru_cache(maxsize=1024)
 def _fp8_ws(desc: Fp8Desc, T: int) -> tuple:
-    fwd, bwd = ctypes.c_size_t(), ctypes.c_size_t()
-    _c_ints(64, T=T)
-    _check("twell_fp8_linear_sizes",
-           library().twell_fp8_linear_sizes(desc._ref, T, ctypes.byref(fwd), ctypes.byref(bwd)))
-    return int(fwd.value), int(bwd.value)
+    """Bytes of the workspaces (forward, backward) for T rows."""
+    kept = desc._ws.get(T)
+    if kept is None:
+        fwd, bwd = ctypes.c_size_t(), ctypes.c_size_t()
+        _c_ints(64, T=T)
+        _check("twell_fp8_linear_sizes",
+               library().twell_fp8_linear_sizes(desc._ref, T, ctypes.byref(fwd), ctypes.byref(bwd)))
+        if len(desc._ws) >= 1024:
+            desc._ws.clear()
+        kept = desc._ws[T] = int(fwd.value), int(bwd.value)
+    return kept
 
 
 def fp8_ws_bytes(desc: Fp8Desc, T: int) -> int:
@@ -940,8 +964,12 @@ def alloc_fp8_ws(desc: Fp8Desc, T: int, device="cuda") -> torch.Tensor:
 
 def _fp8_planes(desc: Fp8Desc, w: Weights, name: str, dev: int) -> CPlanes:
     codes, scales = desc.plane_bytes
-    return CPlanes(_fit(w.codes, name + ".codes", codes, torch.uint8, dev),
-                   _fit(w.scales, name + ".scales", scales, torch.uint8, dev))
+    c, s = w.codes, w.scales
+    if (isinstance(c, torch.Tensor) and c.get_device() == dev and c.dtype is _CODE_DTYPE and c.nbytes >= codes
+            and c.is_contiguous() and isinstance(s, torch.Tensor) and s.get_device() == dev
+            and s.dtype is _CODE_DTYPE and s.nbytes >= scales and s.is_contiguous()):  # _fit of both, no calls
+        return CPlanes(c.data_ptr(), s.data_ptr())
+    return CPlanes(_fit(c, name + ".codes", codes, _CODE_DTYPE, dev), _fit(s, name + ".scales", scales, _CODE_DTYPE, dev))
 
 
 def _offsets(desc: Fp8Desc, offsets, dev: int):
@@ -991,13 +1019,16 @@ def twell_fp8_linear_fwd(desc: Fp8Desc, planes: Weights, x, y, ws, offsets=None,
     """y [T, rows] = x [T, cols], rounded to 8 bits on the way, times the matrix, or each row's expert's: rows
     offsets[e] .. offsets[e + 1] - 1 are expert e's (see include/twell.h).  x and y may have strided rows."""
     code = _any_dtype(x, "x")
-    T, dev = _two_axes(x, "x", desc.cols), _device(x, "x")
-    px, ldx = _rows(x, "x", T, desc.cols, x.dtype, dev)
-    py, ldy = _rows(y, "y", T, desc.rows, x.dtype, dev)
+    T, dtype, dev = _two_axes(x, "x", desc.cols), x.dtype, x.get_device()
+    if dev < 0:
+        _device(x, "x")
+    px, ldx = _rows(x, "x", T, desc.cols, dtype, dev)
+    py, ldy = _rows(y, "y", T, desc.rows, dtype, dev)
     need = _fp8_ws(desc, T)[0]
-    st = library().twell_fp8_linear_fwd(desc._ref, _fp8_planes(desc, planes, "planes", dev), T,
-                                        _offsets(desc, offsets, dev), code, px, ldx, py, ldy,
-                                        _fit(ws, "ws", need, torch.uint8, dev), need, _stream_on(dev, stream))
+    st = library().twell_fp8_linear_fwd(
+        desc._ref, _fp8_planes(desc, planes, "planes", dev), T,
+        None if offsets is None and desc.experts == 1 else _offsets(desc, offsets, dev), code, px, ldx, py, ldy,
+        _fit(ws, "ws", need, torch.uint8, dev), need, _stream_on(dev, stream))
     if st:
         _check("twell_fp8_linear_fwd", st)
 
