@@ -182,6 +182,10 @@ __device__ __forceinline__ u32x4_t buffer16(__amdgpu_buffer_rsrc_t base, uint32_
   return __builtin_amdgcn_raw_buffer_load_b128(base, lane_offset, offset, 0);
 }
 
+__device__ __forceinline__ uint32_t buffer4(__amdgpu_buffer_rsrc_t base, uint32_t lane_offset, uint32_t offset) {
+  return __builtin_amdgcn_raw_buffer_load_b32(base, lane_offset, offset, 0);
+}
+
 // Workgroup id to tile: ids go round-robin to the 8 XCDs, each of which gets a
 // run of tiles here, so that workgroups that share operands share an L2.
 __device__ __forceinline__ int xcd_run(int id, int n) {

@@ -134,7 +134,7 @@ struct F8Gemm {
   const F8GemmArgs& a;
   F8Work<16, FX> work;
   int lane, wave;
-  __amdgpu_buffer_rsrc_t w_rows, x_rows;
+  __amdgpu_buffer_rsrc_t w_rows, x_rows, w_words, x_words;
   uint32_t w_from[4], x_from[kLoads];  // at block 0
   uint8_t* lds;
   f32x4_t acc[4][FX];
@@ -146,11 +146,21 @@ struct F8Gemm {
   __device__ __forceinline__ void fetch_w(F8Frag& w, int i, int half, int kb) {
     w.v[half] = buffer16(w_rows, lane * 16, w_from[i] + kb * kF8Bytes + half * 1024);
   }
+  struct Words {
+    uint32_t w, x[FX];  // scales of four blocks: 128 rows of weights, which a wave's lie in, share theirs
+  };
+  __device__ __forceinline__ void fetch_words(Words& s, int q) {
+    s.w = buffer4(w_words, (lane & 15) * 4, q * kF8Scales);
+#pragma unroll
+    for (int j = 0; j < FX; ++j)
+      s.x[j] = buffer4(x_words, (lane & 15) * 4, static_cast<uint32_t>(work.x_tile(j)) * a.quads * kF8Scales + q * kF8Scales);
+  }
   // One block, with everything else that has to happen meanwhile dealt out between
   // the matrix instructions (sched_barrier pins the order: with one wave a SIMD
-  // anything issued in clumps leaves the matrix core idle).
-  __device__ __forceinline__ void block(int kb, const F8Frag (&w)[4], F8Frag (&w_next)[4], uint32_t sw,
-                                        const uint32_t (&sx)[FX]) {
+  // anything issued in clumps leaves the matrix core idle).  FIRST: of four; it
+  // fetches the next four's scales, ahead of what the next block waits for.
+  template <bool FIRST>
+  __device__ __forceinline__ void block(int kb, const F8Frag (&w)[4], F8Frag (&w_next)[4], const Words& s, Words& s_next) {
     // of what this wave has fetched only the last block's rows may still be under way, so the next block's are
     // there; and all waves are done with the block before this one, whose place is filled now
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
@@ -160,11 +170,15 @@ struct F8Gemm {
     // past the end: the last block again, not used (a branch here would move matrix instructions)
     const int kw = min(kb + 1, a.blocks - 1), kx = min(kb + 3, a.blocks - 1);
     uint8_t* fill = lds + ((kb + 3) & 3) * kStage;
+    if constexpr (FIRST) {
+      fetch_words(s_next, min((kb >> 2) + 1, a.quads - 1));
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int j = 0; j < FX; ++j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f8_mfma(acc[i][j], w[i], sw, x[j % 4], sx[j]);
+        f8_mfma(acc[i][j], w[i], s.w, x[j % 4], s.x[j]);
         if (i == 0) x[(j + 3) % 4].read(j + 3 < FX ? here + (j + 3) * kF8Bytes : next + (j + 3 - FX) * kF8Bytes);
         else if (j * 3 + i - 1 < 8) fetch_w(w_next[(j * 3 + i - 1) / 2], (j * 3 + i - 1) / 2, (j * 3 + i - 1) % 2, kw);
         else if (j * 3 + i - 9 < kLoads) fetch_x(j * 3 + i - 9, kx, fill);
@@ -187,17 +201,11 @@ struct F8Gemm {
       const int half = wave * kLoads + q;
       x_from[q] = static_cast<uint32_t>(work.x_tile(half >> 1)) * blocks * kF8Bytes + (half & 1) * 1024;
     }
-    // 128 rows of weights, which a wave's lie in, share their scales
-    const uint8_t* ws = work.w_scales + static_cast<int64_t>(work.w_tile(4 * wave)) * quads * kF8Scales;
-    const uint8_t* xs = work.x_scales + (lane & 15) * 4;
-    auto w_word = [&](int q) { return *reinterpret_cast<const uint32_t*>(ws + q * kF8Scales); };
-    auto x_word = [&](int j, int q) {
-      return *reinterpret_cast<const uint32_t*>(xs + (static_cast<int64_t>(work.x_tile(j)) * quads + q) * kF8Scales);
-    };
+    w_words = f8_buffer(work.w_scales + static_cast<int64_t>(work.w_tile(4 * wave)) * quads * kF8Scales);
+    x_words = f8_buffer(work.x_scales);
     F8Frag wa[4], wb[4];
-    uint32_t sw_next = w_word(0), sx_next[FX];
-#pragma unroll
-    for (int j = 0; j < FX; ++j) sx_next[j] = x_word(j, 0);
+    Words words, words_next;
+    fetch_words(words_next, 0);
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) fetch_x(q, 0, lds);
 #pragma unroll
@@ -213,24 +221,22 @@ struct F8Gemm {
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
     for (int j = 0; j < 3; ++j) x[j].read(lds + lane * 16 + j * kF8Bytes);
-    // four blocks at a time, whose scales share words; the next four's are fetched before them
+    // four blocks at a time, whose scales share words
     for (int kb0 = 0; kb0 < blocks; kb0 += 4) {
-      uint32_t sw = sw_next, sx[FX];
-#pragma unroll
-      for (int j = 0; j < FX; ++j) sx[j] = sx_next[j];
-      const int q = min((kb0 >> 2) + 1, quads - 1), end = min(kb0 + 4, blocks);
-      sw_next = w_word(q);
-#pragma unroll
-      for (int j = 0; j < FX; ++j) sx_next[j] = x_word(j, q);
+      words = words_next;
+      block<true>(kb0, wa, wb, words, words_next);
+      const int end = min(kb0 + 4, blocks);
 #pragma nounroll
-      for (int kb = kb0; kb < end; ++kb) {
-        block(kb, wa, wb, sw, sx);
-        sw >>= 8;
+      for (int kb = kb0 + 1; kb < end; ++kb) {
+        words.w >>= 8;
 #pragma unroll
-        for (int j = 0; j < FX; ++j) sx[j] >>= 8;
+        for (int j = 0; j < FX; ++j) words.x[j] >>= 8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) wa[i] = wb[i];
+        block<false>(kb, wa, wb, words, words_next);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wa[i] = wb[i];
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load is still on its way to LDS when the workgroup ends
     work.template store<EBf16>(a, 4 * wave, 0, acc);
