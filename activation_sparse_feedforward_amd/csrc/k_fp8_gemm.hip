@@ -333,7 +333,7 @@ __global__ __launch_bounds__(256) void f8_gemm_exact_kernel(F8GemmArgs a) {
 // itself, which saves a launch and costs each workgroup the rounding again.
 constexpr int kFewAhead = 2;
 
-template <class E, int MT, int NT, bool CODES, int WAVES = 8>
+template <class E, int MT, int NT, bool CODES, int WAVES>
 __global__ __launch_bounds__(WAVES* kWave) void f8_few_kernel(F8GemmArgs a) {
   using S = typename E::storage;
   extern __shared__ __align__(16) float lds_sums[];
@@ -445,7 +445,7 @@ __global__ __launch_bounds__(WAVES* kWave) void f8_few_kernel(F8GemmArgs a) {
     }
 }
 
-template <class E, int MT, int NT, bool CODES, int WAVES = 8>
+template <class E, int MT, int NT, bool CODES, int WAVES>
 hipError_t go_few(const F8GemmArgs& a, hipStream_t s) {
   int waves = WAVES;
   while (waves > 1 && waves > a.blocks) waves >>= 1;
@@ -476,52 +476,68 @@ hipError_t go_gemm(const F8GemmArgs& a, hipStream_t s) {
 // the result's 2^-8.  fp32 results have the same codes multiplied as bf16 values,
 // exactly, with fp32 sums, at half the rate or less.
 //
-// Which kernel: by estimates of the times in us, whose constants were fitted to
-// 300 measured calls (1 to 8192 rows of 512 x 700 to 11008 x 4096, 1 to 64
-// experts); the kernel taken is the fastest there or within a tenth of it, some
-// cases of up to 17 us aside.  Replayed, of 8192 x 2048 in bf16:
-//   rows                          1     16    32    64    128   256   512   1024
-//   rounding on the way, 16 x 32  6.3   6.8   9.5   15.4  26.9  49
-//                        32 x 32              8.7   15.1  27.3
-//   codes,               32 x 32  9.5   10.6  10.7  12.3  16.1  23.8  39
-//                        64 x 64              13.0  13.4  13.8  20.5  34    60
-//   codes through LDS,   64 x 256 17.9  19.1  19.6  20.7  20.6  21.1  22.9  30.6
-//                       128 x 256 19.9  21.0  21.5  22.4  24.6  24.8  25.9  29.6
+// Which kernel: by the sizes, fitted to 230 calls, each timed with every kernel (1 to
+// 32768 rows of 768 x 1024 to 11008 x 4096, 1 to 128 experts, both types): the one
+// taken is 2 % behind the fastest on average, up to a fifth in three cases.
+// Replayed, us, bf16:
+//                               8192 x 2048               64 experts of 1024 x 2048
+//   rows                        1    32   64   256  1024  64    256   1024  4096  8192
+//   rounding on the way
+//     16 x 32, 8 waves          6.5  9.6  16.0 51.5 185   21.2  31.6  45.5  120   221
+//     16 x 64, 8 waves          6.5  7.6  12.6 43.0 165   21.6  32.4  42.9  106   192
+//     16 x 32, 4 waves          7.1  9.5  14.7 44.2 160   18.9  26.7  38.8  95.9  175
+//     16 x 64, 4 waves          7.6  8.8  10.5 34.9 130   20.0  27.7  35.5  81.2  145
+//   codes from a launch of their own
+//     32 x 32, 4 waves          9.9  11.0 12.4 22.4 61.0  23.7  31.8  37.7  58.8  89.9
+//     64 x 64, 4 waves          12.8 14.0 14.2 18.2 44.3  28.9  37.5  40.1  52.2  74.0
+//     64 x 256, through LDS     17.6 18.9 20.2 20.6 29.4  30.9  36.4  39.9  46.5  67.6
+//     128 x 256, through LDS    19.2 20.7 21.8 24.1 28.9  30.1  39.1  42.8  52.6  59.4
+// With many workgroups, small ones with few waves follow each other without a gap
+// (the waves of one wait for each other at its end); with few, more waves a
+// workgroup keep more of the weights on their way.
+template <class E>
+hipError_t go_few_rows(const F8GemmArgs& a, int64_t groups, hipStream_t s) {
+  if (groups < 256) return go_few<E, 1, 1, false, 16>(a, s);
+  if (groups == 256) return go_few<E, 1, 2, false, 8>(a, s);
+  if (groups <= 512) return go_few<E, 1, 4, false, 8>(a, s);  // one round, of half as many
+  if constexpr (E::kBytes == 2) {  // 16 x 32 suits tiles of few rows; fp32's widening costs less in 16 x 64 everywhere
+    if (a.T <= 16 * static_cast<int64_t>(a.experts) && groups <= 2048) return go_few<E, 1, 2, false, 4>(a, s);
+  }
+  return go_few<E, 1, 4, false, 4>(a, s);
+}
+
 hipError_t launch_f8_product(const F8GemmArgs& a, const F8RowsArgs& rows, int dtype, hipStream_t s) {
   const bool bf16 = dtype == 1;
+  // tiles of rows: the most there can be, and about how many (an expert's last one is half full on average)
   auto row_tiles = [&](int64_t unit) { return a.offsets ? a.T / unit + a.experts : (a.T + unit - 1) / unit; };
+  auto row_work = [&](int unit) {
+    return a.offsets ? static_cast<double>(a.T) / unit + 0.5 * a.experts : static_cast<double>(row_tiles(unit));
+  };
   const int64_t pairs = (a.tiles + 1) / 2, quads = (a.tiles + 3) / 4, blocks = a.blocks;
-  // long fp32 rows take longer to round in every workgroup than their codes' launch
-  const bool on_the_way = bf16 || a.T == 1 || blocks <= 32;
-  if (on_the_way && a.T <= 16 * static_cast<int64_t>(a.experts)) {
-    if (row_tiles(16) * pairs < 256)  // few workgroups: half as large, and twice the waves to share the inputs
-      return bf16 ? go_few<EBf16, 1, 1, false, 16>(a, s) : go_few<EF32, 1, 1, false, 16>(a, s);
-    return bf16 ? go_few<EBf16, 1, 2, false>(a, s) : go_few<EF32, 1, 2, false>(a, s);
-  }
-  if (on_the_way && row_tiles(16) * pairs * blocks <= (bf16 ? 8192 : 4096)) {
-    if (row_tiles(16) * pairs <= 256) return bf16 ? go_few<EBf16, 1, 2, false>(a, s) : go_few<EF32, 1, 2, false>(a, s);
-    return bf16 ? go_few<EBf16, 2, 2, false>(a, s) : go_few<EF32, 2, 2, false>(a, s);
-  }
+  const int64_t groups = row_tiles(16) * pairs;
+  // rounding again in every workgroup costs fp32 more: long rows take longer than their codes' launch
+  if ((bf16 || a.T == 1 || blocks <= 32) &&
+      (a.T <= 16 * static_cast<int64_t>(a.experts) || groups * blocks <= (bf16 ? 16384 : 12288)))
+    return bf16 ? go_few_rows<EBf16>(a, groups, s) : go_few_rows<EF32>(a, groups, s);
   const hipError_t e = launch_f8_rows(rows, dtype, s);
   if (e != hipSuccess) return e;
-  // an expert's last tile is half full on average
-  const double tiles64 = a.offsets ? a.T / 64.0 + 0.5 * a.experts : static_cast<double>(row_tiles(64));
-  const double few = (bf16 ? 1.4e-3 : 2.4e-3) * tiles64 * quads * blocks;
-  if (bf16) {
-    const double rounds = tiles64 * ((a.tiles + 15) / 16) / 512;
-    if (0.75 * blocks * (rounds > 1 ? rounds : 1) <= few) {
-      // tiles of 128 rows that an expert fills half cost as much as full ones
-      const double tiles128 = a.offsets ? a.T / 128.0 + 0.5 * a.experts : static_cast<double>(row_tiles(128));
-      const bool large = tiles128 * ((a.tiles + 15) / 16) > (a.offsets ? 256 : 159);
-      return large ? go_gemm<8>(a, s) : go_gemm<4>(a, s);
-    }
-    return row_tiles(64) * quads >= 256 ? go_few<EBf16, 4, 4, true>(a, s) : go_few<EBf16, 2, 2, true>(a, s);
-  }
-  const double rounds = 0.5 * tiles64 * ((a.tiles + 7) / 8) / 512;
-  if (1.35 * blocks * (rounds > 1 ? rounds : 1) <= few)
+  // estimates in us; those of the tiles through LDS leave a part out that the others have as well
+  if (!bf16) {
+    const double few = 4.2e-4 * row_work(32) * pairs * blocks;
+    const double rounds = 0.5 * row_work(64) * ((a.tiles + 7) / 8) / 512;
+    if (1.35 * blocks * (rounds > 1 ? rounds : 1) > few) return go_few<EF32, 2, 2, true, 4>(a, s);
     return launch_lds<&f8_gemm_exact_kernel, 2 * kExactStage>(tile_grid<kExactTiles, kExactTiles>(a), 256,
                                                               2 * kExactStage, s, a);
-  return row_tiles(64) * pairs >= 256 ? go_few<EF32, 4, 2, true>(a, s) : go_few<EF32, 2, 2, true>(a, s);
+  }
+  const double few32 = 3.8e-4 * row_work(32) * pairs * blocks, few64 = 1.5e-3 * row_work(64) * quads * blocks;
+  const double strips = (a.tiles + 15) / 16, rounds = row_work(64) * strips / 512;
+  if (1.05 * blocks * (rounds > 1 ? rounds : 1) > (few32 < few64 ? few32 : few64)) {
+    // 64 x 64 tiles only where they are enough
+    return few64 < few32 && row_tiles(64) * quads >= 256 ? go_few<EBf16, 4, 4, true, 4>(a, s)
+                                                         : go_few<EBf16, 2, 2, true, 4>(a, s);
+  }
+  // tiles of 128 rows that an expert fills half cost as much as full ones
+  return row_work(128) * strips > (a.offsets ? 256 : 159) ? go_gemm<8>(a, s) : go_gemm<4>(a, s);
 }
 
 }  // namespace twell

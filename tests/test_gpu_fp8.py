@@ -191,6 +191,18 @@ def test_more_rows(T_, N, K, counts, dtype):
     _case(T_, N, K, dtype, counts, seed=T_)
 
 
+# one or more for each kernel that the launcher chooses among: rounding on the way with few to many workgroups,
+# codes in small and larger tiles, tiles through LDS of 64 and 128 rows (fp32: 128 x 128)
+@pytest.mark.parametrize("T_,N,K,counts", [(15, 8180, 130, None), (100, 2000, 300, None), (50, 620, 250, [1, 3] * 10 + [0] * 20),
+                                           (470, 250, 400, [2, 1, 0] * 150), (250, 500, 8200, None),
+                                           (1020, 1020, 2100, None), (3000, 1030, 650, None), (4200, 1030, 520, None),
+                                           (4000, 1100, 300, [1400, 0, 70, 2520])])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_each_kernel_of_the_products(T_, N, K, counts, dtype):
+    say(f"[gpu case] fp8 product T={T_} N={N} K={K} {dtype} of {len(counts or [0])} experts")
+    _case(T_, N, K, dtype, counts, seed=T_)
+
+
 def test_many_experts():
     say("[gpu case] fp8 1024 experts")
     r = np.random.default_rng(0)
