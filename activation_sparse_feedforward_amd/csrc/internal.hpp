@@ -239,7 +239,7 @@ struct TokensArgs {
   const float* weights;    // [T * k]; combine: null = 1
   float* dweights;         // [T * k] or null
   int64_t T, pairs, ld_tokens, ld_rows, ld_out;  // ld_out: of rows_out
-  int32_t d, k, pieces;    // pieces: of a row, one wave each (set by the launcher)
+  int32_t d, k, pieces;    // pieces: of a token, one wave each (set by the launcher)
 };
 
 // Layer norm.

@@ -385,7 +385,9 @@ twell_status twell_moe_fwd(const twell_moe_desc* d, const void* x, const void* w
  * their elements (int32 and fp32 arrays 4 bytes, workspaces 16).  Tensors of one
  * call must not overlap where not said otherwise.  Limits: 2^20 tokens, T x
  * d_model up to 2^33, 1024 experts, top_k up to 32, strides up to 2^40 elements
- * (TWELL_EUNSUPPORTED beyond).  T = 0 reads no tensor.  All are deterministic. */
+ * (TWELL_EUNSUPPORTED beyond).  T = 0 reads no tensor.  All are deterministic.  A
+ * workspace belongs to one call at a time: calls, or graphs that hold some, that may
+ * run at once need one each. */
 
 /* T tokens, top_k choices among `experts` each.  A pair p = t * top_k + i is
  * choice i of token t; there are up to T * top_k sorted rows.  Rows of

@@ -75,7 +75,7 @@ def test_gather_combine_and_gradients(d, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("T_,k,E,dropped", [(1, 1, 1, 0.0), (1, 8, 64, 0.0), (3, 32, 40, 0.1), (5, 9, 2, 0.0),
-                                            (130, 8, 16, 1.0), (129, 7, 300, 0.5)])
+                                            (130, 8, 16, 1.0), (129, 7, 300, 0.5), (2047, 3, 7, 0.2), (2048, 3, 7, 0.2)])
 def test_gather_combine_and_gradients_by_choices(T_, k, E, dropped, dtype):
     say(f"[gpu case] gather, combine, gradients T={T_} k={k} E={E} dropped={dropped} {dtype}")
     _through(T.TokensDesc(T_, 320, E, k, dtype), _ids(T_, k, E, T_, dropped), k)
