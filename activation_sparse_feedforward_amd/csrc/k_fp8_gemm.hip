@@ -124,7 +124,12 @@ struct F8Work {
 // whose codes go to LDS with direct loads, three blocks ahead, and from there to
 // registers three fragments ahead.  So a fragment from LDS feeds four matrix
 // instructions and LDS carries 2 KB for 131 k operations of each wave: with both
-// operands in LDS and 64 x 64 a wave it would be twice that, which bounds it.
+// operands in LDS and 64 x 64 a wave it would be twice that, which bounds it (16384
+// rows of 2048 through 8192 x 2048, with rounding the rows: 352 us so, 271 to 288 as
+// it is; 256 x 256 tiles with one workgroup a CU 367).  The product alone takes 240
+// to 260 us, 2.1 to 2.3 PFLOP/s, of 8192 inputs 840 to 877, 2.5 to 2.6; the matrix
+// cores are busy for two thirds of the time, at a clock of 1.5 to 1.8 GHz that their
+// power sets, and with all loads in an L2 it would be 7 % faster.
 template <int FX>
 struct F8Gemm {
   static constexpr int kStages = 4, kStage = FX * kF8Bytes, kLds = kStages * kStage;
@@ -253,7 +258,8 @@ __global__ __launch_bounds__(256, FX < 16 ? 2 : 1) void f8_gemm_kernel(F8GemmArg
 }
 
 // fp32 results: codes widened to bf16, four instructions a block.  2 x 2 waves of 64 x 64, both operands through
-// LDS in two stages.
+// LDS in two stages.  Widening is 128 conversions beside 64 matrix instructions of a wave and block: 8192 rows of 8
+// experts of 1024 x 2048 take 72 us with their rounding.
 constexpr int kExactTiles = 8;  // of 16 weight rows, and of 16 rows
 constexpr int kExactStage = 2 * kExactTiles * kF8Bytes;
 __global__ __launch_bounds__(256) void f8_gemm_exact_kernel(F8GemmArgs a) {
@@ -476,7 +482,7 @@ hipError_t go_gemm(const F8GemmArgs& a, hipStream_t s) {
 // the result's 2^-8.  fp32 results have the same codes multiplied as bf16 values,
 // exactly, with fp32 sums, at half the rate or less.
 //
-// Which kernel: by the sizes, fitted to 230 calls, each timed with every kernel (1 to
+// Which kernel: by the sizes, fitted to 218 calls, each timed with every kernel (1 to
 // 32768 rows of 768 x 1024 to 11008 x 4096, 1 to 128 experts, both types): the one
 // taken is 2 % behind the fastest on average, up to a fifth in three cases.
 // Replayed, us, bf16:

@@ -138,7 +138,9 @@ __global__ __launch_bounds__(kSortWaves* kWave) void tokens_place_kernel(TokensS
 // All three kernels are bound by the rows they read and write; nothing is
 // computed that takes as long.  A wave has a piece of one token: what a token
 // reads or writes once (x, y, dy) is then touched once, and its k rows are read
-// or written whole lines at a time, all their loads in flight together.
+// or written whole lines at a time, all their loads in flight together.  16384
+// tokens of 2048 in bf16, 8 choices each: gather 114 us, combine 118, its gradient
+// 231, which is 5.3, 5.1 and 4.9 TB/s, where a copy of 2 GiB reaches 4.9.
 
 // Row of a pair, or -1.  The bound keeps a list that was not made by the sort
 // from leading outside the rows.

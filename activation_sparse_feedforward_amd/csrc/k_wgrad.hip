@@ -113,7 +113,8 @@ struct GradTile<EF32, COLS> {
 };
 
 // fp32, and bf16 rows of less than 16 bytes: a tile of 32 F x 32 F of dW per
-// workgroup, 16 F x 16 F a wave.
+// workgroup, 16 F x 16 F a wave.  fp32 is bound by its matrix instructions, at a
+// sixteenth of bf16's rate: 777 rows of 5 experts of 1001 x 707 take 20 to 22 us.
 template <class E, int F>
 __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
   using S = typename E::storage;
@@ -201,7 +202,10 @@ __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
 // one wave a SIMD: a fragment feeds eight matrix instructions, so that LDS carries
 // 96 bytes a cycle (64 x 64 a wave take 192, which bounds the kernel above).
 // (Direct loads to LDS would save the registers, but the compiler waits for all of
-// them before every transposed read.)
+// them before every transposed read.)  16384 rows, 8192 x 2048: 414 to 440 us, 1.25 to
+// 1.33 PFLOP/s, where a library's bf16 product of 8192^3 reaches 1.38; 8191 wide, rows
+// not aligned, 569 us; 16 uneven experts of 1024 x 2048 97 us: two workgroups a CU one
+// after the other, each with a start and 256 KB to store that nothing overlaps.
 constexpr int kWide = 256, kWideTokens = 32, kWideRow = kWide * 2;
 constexpr int kWideTile = kWideTokens * kWideRow, kWideStage = 2 * kWideTile, kWideStages = 4;
 constexpr int kWideLds = kWideStages * kWideStage;
