@@ -391,3 +391,71 @@ def test_other_stream_and_replayed_graph(T_, counts):
         graph.replay()
         torch.cuda.synchronize()
         assert same()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T_,N,K,counts", [(600, 2000, 2600, None), (1020, 1020, 2100, None), (4200, 1030, 520, None),
+                                           (4000, 1100, 300, [1400, 0, 70, 2520]), (9000, 1100, 300, [3000, 5000, 999])])
+def test_kernels_of_many_rows_in_other_places(T_, N, K, counts, dtype):
+    """Rows of other strides, NaN and infinities, replays with other work between them, and offsets of another origin:
+    each kernel that reads codes of rows, against its own results for the same rows."""
+    say(f"[gpu case] fp8 T={T_} N={N} K={K} {dtype} in other places")
+    g = torch.Generator(device="cuda").manual_seed(T_)
+    E = 1 if counts is None else len(counts)
+    desc = T.Fp8Desc(E, N, K)
+    p, _ = _packed(desc, torch.randn(E, N, K, generator=g, device="cuda"), both=False)
+    x = torch.randn(T_, K, generator=g, device="cuda").to(DT[dtype])
+    off = None if counts is None else _offsets(counts, T_)
+    n = T_ if counts is None else sum(counts)
+    ws = guarded((T.fp8_ws_bytes(desc, T_),), torch.uint8)
+    y, again = (guarded((T_, N), DT[dtype]) for _ in range(2))
+    T.twell_fp8_linear_fwd(desc, p, x, y, ws, offsets=off)
+    check_guards(y, ws)
+    assert bool((y[n:].contiguous().view(torch.uint8) == 0xA5).all())
+
+    wide = [torch.zeros(T_, m + 7, device="cuda", dtype=DT[dtype]) for m in (K, N)]
+    xs, ys = (v[:, 3:-4] for v in wide)
+    xs.copy_(x)
+    T.twell_fp8_linear_fwd(desc, p, xs, ys, ws, offsets=off)
+    assert torch.equal(ys[:n], y[:n]) and not any(bool(v[:, :3].any() | v[:, -4:].any()) for v in wide)
+
+    bad = x.clone()
+    bad[1, K - 1], bad[n - 2, 0], bad[n // 2, K // 2] = float("nan"), float("inf"), float("-inf")
+    T.twell_fp8_linear_fwd(desc, p, bad, again, ws, offsets=off)
+    rows = torch.zeros(n, dtype=torch.bool, device="cuda")
+    rows[[1, n - 2, n // 2]] = True
+    assert torch.isnan(again[:n][rows]).all() and torch.equal(again[:n][~rows], y[:n][~rows])
+
+    graph = capture(lambda: T.twell_fp8_linear_fwd(desc, p, x, again, ws, offsets=off))
+    for _ in range(3):
+        again.fill_(3.0)
+        ws.fill_(0x3C)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again[:n], y[:n])
+
+    if counts is not None:
+        for o in ([T_] * E + [0], [0, T_, 5, T_, 9][:E + 1], [-9] + [2 ** 31 - 1] * E, list(range(7, 7 + E + 1))):
+            T.twell_fp8_linear_fwd(desc, p, x, again, ws, offsets=torch.tensor(o, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    check_guards(again, ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_most_rows(dtype):
+    """2^20 rows, the most there may be, of two widths."""
+    for N, K in ((8, 8), (40, 136)):
+        say(f"[gpu case] fp8 2^20 rows, {N} x {K} {dtype}")
+        desc = T.Fp8Desc(1, N, K)
+        p, t = _packed(desc, torch.randn(1, N, K, device="cuda"))
+        x, dy = (torch.randn(1 << 20, m, device="cuda").to(DT[dtype]) for m in (K, N))
+        ws, y, dx, dw = T.alloc_fp8_ws(desc, 1 << 20), torch.empty_like(dy), torch.empty_like(x), torch.empty(1, N, K, device="cuda")
+        T.twell_fp8_linear_fwd(desc, p, x, y, ws)
+        T.twell_fp8_linear_bwd(desc, t, x, dy, dx, dw, ws)
+        some = torch.cat([torch.arange(40), torch.arange((1 << 20) - 40, 1 << 20), torch.randint(1 << 20, (200,))]).cuda()
+        wv = h64(_values(desc, p))[0]
+        for got, of, m in ((y, x, wv.T), (dx, dy, wv)):
+            q = e4m3_rows(h64(of[some]))
+            check(got[some], q @ m, product_bound(q, m.T, q @ m, dtype), "rows")
+        ref, mag = dy.double().t() @ x.double(), dy.double().abs().t() @ x.double().abs()
+        check(dw[0], h64(ref), (2 ** 20 + 8) * U32 * h64(mag), "dw")
