@@ -77,7 +77,7 @@ __device__ __forceinline__ void store_acc(const Args& a, int64_t row, int n, con
 // lane group g gives its quarter of every tile for tile g whole, so that a lane has 16
 // outputs in a row, two stores, and four lanes a line of 128 bytes (16384 x 8192 of
 // 512 and 2048 inputs: 130 and 291 us with four stores of 8 bytes, 112 and 272 so).
-template <class Args>
+template <bool PAST, class Args>
 __device__ __forceinline__ void store_four_acc(const Args& a, int64_t row, int n, const f32x4_t (&acc)[4], bool live) {
   u32x4_t out[2];
 #pragma unroll
@@ -96,8 +96,13 @@ __device__ __forceinline__ void store_four_acc(const Args& a, int64_t row, int n
   }
   if (!live) return;  // lanes without a row took part above
   uint16_t* y = static_cast<uint16_t*>(a.y) + row * a.ldy + n + 16 * ((threadIdx.x & 63) >> 4);
-  store16(y, out[0]);
-  store16(y + 8, out[1]);
+  if constexpr (PAST) {
+    store16_past(y, out[0]);
+    store16_past(y + 8, out[1]);
+  } else {
+    store16(y, out[0]);
+    store16(y + 8, out[1]);
+  }
 }
 
 // ------------------------------------------------------------------ many rows
@@ -130,7 +135,7 @@ struct F8Work {
   // tiles past the matrix or the expert's rows are the last one again; their results are not stored
   __device__ __forceinline__ int w_tile(int i) const { return min(w0 + i, w_last); }
   __device__ __forceinline__ int x_tile(int i) const { return min(i, x_last); }
-  template <class E, int FW, int FX>
+  template <class E, bool PAST = false, int FW, int FX>
   __device__ __forceinline__ void store(const F8GemmArgs& a, int fw0, int fx0, const f32x4_t (&acc)[FW][FX]) const {
     const int lane = threadIdx.x & 63;
     if constexpr (E::kBytes == 2 && FW == 4) {
@@ -139,7 +144,7 @@ struct F8Work {
         for (int j = 0; j < FX; ++j) {
           const f32x4_t four[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
           const int r = (fx0 + j) * 16 + (lane & 15);
-          store_four_acc(a, p.row0 + r, (w0 + fw0) * 16, four, r < p.rows);
+          store_four_acc<PAST>(a, p.row0 + r, (w0 + fw0) * 16, four, r < p.rows);
         }
         return;
       }
@@ -163,12 +168,12 @@ struct F8Work {
 // registers three fragments ahead.  So a fragment from LDS feeds four matrix
 // instructions and LDS carries 2 KB for 131 k operations of each wave: with both
 // operands in LDS and 64 x 64 a wave it would be twice that, which bounds it (16384
-// rows of 2048 through 8192 x 2048, with rounding the rows: 352 us so, 271 to 288 as
-// it is; 256 x 256 tiles with one workgroup a CU 367).  The product alone takes 240
-// to 260 us, 2.1 to 2.3 PFLOP/s, of 8192 inputs 840 to 877, 2.5 to 2.6; the matrix
-// cores are busy for two thirds of the time, at a clock of 1.5 to 1.8 GHz that their
-// power sets, and with all loads in an L2 it would be 7 % faster.
-template <int FX>
+// rows of 2048 through 8192 x 2048, with rounding the rows: 352 us so, 249 to 258 as
+// it is; 256 x 256 tiles with one workgroup a CU 367).  The product alone takes some
+// 230 us, 2.4 PFLOP/s, of 8192 inputs 825, 2.7; the matrix cores are busy for two
+// thirds of the time, at a clock of 1.5 to 1.8 GHz that their power sets, and
+// with all loads in an L2 it would be 7 % faster.
+template <int FX, bool PAST>  // PAST: results past the caches
 struct F8Gemm {
   static constexpr int kStages = 4, kStage = FX * kF8Bytes, kLds = kStages * kStage;
   static constexpr int kLoads = FX / 2;  // direct loads of a wave and block, 1 KB each
@@ -282,14 +287,14 @@ struct F8Gemm {
       for (int i = 0; i < 4; ++i) wa[i] = wb[i];
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load is still on its way to LDS when the workgroup ends
-    work.template store<EBf16>(a, 4 * wave, 0, acc);
+    work.template store<EBf16, PAST>(a, 4 * wave, 0, acc);
   }
 };
 
-template <int FX>
-__global__ __launch_bounds__(256, FX < 16 ? 2 : 1) void f8_gemm_kernel(F8GemmArgs a) {
+template <int FX, bool PAST>
+__global__ __launch_bounds__(256, 2) void f8_gemm_kernel(F8GemmArgs a) {
   extern __shared__ __align__(16) uint8_t lds_tiles[];
-  F8Gemm<FX> g{a};
+  F8Gemm<FX, PAST> g{a};
   if (!g.work.init(a)) return;
   g.lds = lds_tiles;
   g.run();
@@ -506,9 +511,10 @@ dim3 tile_grid(const F8GemmArgs& a) {
   const int64_t mt = a.offsets ? a.T / (16 * kX) + a.experts : (a.T + 16 * kX - 1) / (16 * kX);
   return dim3(static_cast<unsigned>(nt * mt));
 }
-template <int FX>
+template <int FX, bool PAST>
 hipError_t go_gemm(const F8GemmArgs& a, hipStream_t s) {
-  return launch_lds<&f8_gemm_kernel<FX>, F8Gemm<FX>::kLds>(tile_grid<16, FX>(a), 256, F8Gemm<FX>::kLds, s, a);
+  using G = F8Gemm<FX, PAST>;
+  return launch_lds<&f8_gemm_kernel<FX, PAST>, G::kLds>(tile_grid<16, FX>(a), 256, G::kLds, s, a);
 }
 
 }  // namespace
@@ -581,7 +587,10 @@ hipError_t launch_f8_product(const F8GemmArgs& a, const F8RowsArgs& rows, int dt
                                                          : go_few<EBf16, 2, 2, true, 4>(a, s);
   }
   // tiles of 128 rows that an expert fills half cost as much as full ones
-  return row_work(128) * strips > (a.offsets ? 256 : 159) ? go_gemm<8>(a, s) : go_gemm<4>(a, s);
+  if (row_work(128) * strips <= (a.offsets ? 256 : 159)) return go_gemm<4, false>(a, s);
+  // Results of 64 MB and more, unless there is little to read for them, go past the caches, which keep the operands:
+  // 16384 x 8192 of 2048 and 8192 inputs 260 -> 248 and 903 -> 868 us, but of 512 inputs 107 -> 111.
+  return a.T * a.N >= int64_t(1) << 25 && blocks >= 8 ? go_gemm<8, true>(a, s) : go_gemm<8, false>(a, s);
 }
 
 }  // namespace twell

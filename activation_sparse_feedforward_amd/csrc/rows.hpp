@@ -11,6 +11,10 @@ typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ u32x4_t load16(const void* p) { return *static_cast<const u32x4_any_t*>(p); }
 __device__ __forceinline__ void store16(void* p, u32x4_t v) { *static_cast<u32x4_any_t*>(p) = v; }
+// The same past the caches.
+__device__ __forceinline__ void store16_past(void* p, u32x4_t v) {
+  __builtin_nontemporal_store(static_cast<u32x4_any_t>(v), static_cast<u32x4_any_t*>(p));
+}
 
 // Two fp32 values as bf16, rounded to nearest even; NaN stays NaN.
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {

@@ -395,7 +395,8 @@ def test_other_stream_and_replayed_graph(T_, counts):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("T_,N,K,counts", [(600, 2000, 2600, None), (1020, 1020, 2100, None), (4200, 1030, 520, None),
-                                           (4000, 1100, 300, [1400, 0, 70, 2520]), (9000, 1100, 300, [3000, 5000, 999])])
+                                           (4000, 1100, 300, [1400, 0, 70, 2520]), (9000, 1100, 300, [3000, 5000, 999]),
+                                           (16500, 2040, 1030, None)])
 def test_kernels_of_many_rows_in_other_places(T_, N, K, counts, dtype):
     """Rows of other strides, NaN and infinities, replays with other work between them, and offsets of another origin:
     each kernel that reads codes of rows, against its own results for the same rows."""
