@@ -542,6 +542,7 @@ hipError_t go_gemm(const F8GemmArgs& a, hipStream_t s) {
 //     64 x 64, 4 waves          12.8 14.0 14.2 18.2 44.3  28.9  37.5  40.1  52.2  74.0
 //     64 x 256, through LDS     17.6 18.9 20.2 20.6 29.4  30.9  36.4  39.9  46.5  67.6
 //     128 x 256, through LDS    19.2 20.7 21.8 24.1 28.9  30.1  39.1  42.8  52.6  59.4
+// (The last two before they stored whole lines, which takes 2 to 14 % off them.)
 // With many workgroups, small ones with few waves follow each other without a gap
 // (the waves of one wait for each other at its end); with few, more waves a
 // workgroup keep more of the weights on their way.
