@@ -238,7 +238,7 @@ struct TokensArgs {
   const int32_t* pair_row;  // [T * k]
   const float* weights;    // [T * k]; combine: null = 1
   float* dweights;         // [T * k] or null
-  int64_t T, pairs, ld_tokens, ld_rows, ld_out;  // ld_out: of rows_out
+  int64_t T, pairs, ld_tokens, ld_rows, ld_out;  // ld_rows: of rows; ld_out: of rows_out
   int32_t d, k, pieces;    // pieces: of a token, one wave each (set by the launcher)
 };
 

@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kRowWaves* kWave) void tokens_gather_kernel(TokensA
   for (int i = 0; i < a.k; ++i) {
     const int r = row_of(a, w.t * a.k + i);
     if (r < 0) continue;
-    S* to = static_cast<S*>(a.rows_out) + static_cast<int64_t>(r) * a.ld_rows;
+    S* to = static_cast<S*>(a.rows_out) + static_cast<int64_t>(r) * a.ld_out;
 #pragma unroll
     for (int u = 0; u < U; ++u) store_piece<E>(to, w.c + u * kStep, a.d, v[u]);
   }
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(kRowWaves* kWave) void tokens_combine_bwd_kernel(To
     if (r >= 0) {
       const float wt = a.weights[p];
       const S* row = static_cast<const S*>(a.rows) + static_cast<int64_t>(r) * a.ld_rows;
-      S* to = a.rows_out ? static_cast<S*>(a.rows_out) + static_cast<int64_t>(r) * a.ld_rows : nullptr;
+      S* to = a.rows_out ? static_cast<S*>(a.rows_out) + static_cast<int64_t>(r) * a.ld_out : nullptr;
       for (int c0 = lane * P::kN; c0 < (KEEP ? lane * P::kN + 1 : a.d); c0 += U * kStep) {
         u32x4_t v[U];
 #pragma unroll

@@ -163,6 +163,43 @@ def test_strided_and_unaligned_rows(dtype):
     assert torch.equal(drows[live:], before[3][live:, 3:3 + d])
 
 
+# (first column, elements beside the row) of rows and of drows; None: no rows
+@pytest.mark.parametrize("of_rows,of_drows", [((3, 9), (0, 0)), ((0, 0), (5, 11)), ((1, 2), (4, 40)), ((4, 40), (1, 2)),
+                                              (None, (0, 0)), (None, (2, 7))])
+@pytest.mark.parametrize("T_", [41, 2049])  # a wave a choice, a wave a token
+@pytest.mark.parametrize("d", [301, 2600])  # dy kept in registers and read again, in both types
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradients_into_rows_of_another_stride(dtype, d, T_, of_rows, of_drows):
+    say(f"[gpu case] combine's gradients {dtype} T={T_} d={d} rows {of_rows} drows {of_drows}")
+    k, E, dt = 2, 3, DT[dtype]
+    P = T_ * k
+    desc = T.TokensDesc(T_, d, E, k, dtype)
+    o = _sorted(desc, _ids(T_, k, E, d, 0.1))
+    live, pr = int(o.offsets[-1]), o.pair_row.view(-1).long()
+    g = torch.Generator(device="cuda").manual_seed(d + T_)
+    dy = torch.randn(T_, d, generator=g, device="cuda").to(dt)
+    w = torch.rand(T_, k, generator=g, device="cuda")
+    z = None
+    if of_rows:
+        z = torch.randn(P, d + of_rows[1], generator=g, device="cuda").to(dt)[:, of_rows[0]:of_rows[0] + d]
+    first, beside = of_drows
+    base, dweights = guarded((P, d + beside), dt), guarded((T_, k), torch.float32)
+    drows = base[:, first:first + d]
+    T.twell_tokens_combine_bwd(desc, z, o, w, dy, drows, dweights if of_rows else None)
+    torch.cuda.synchronize()
+    check_guards(base, dweights)
+    kept = base.clone()
+    kept.view(torch.uint8).fill_(0xA5)
+    kept[:live, first:first + d] = drows[:live]
+    assert torch.equal(base.view(torch.uint8), kept.view(torch.uint8)), "beside the rows or behind the last one"
+    there = pr >= 0
+    want = h64((dy.double()[:, None] * w.double()[..., None]).view(P, d)[there])
+    check(drows[pr[there]], want, (U32 + HALF[dtype]) * 1.01 * np.abs(want), "drows")
+    if of_rows:
+        terms = torch.where(there[:, None], z.double()[pr.clamp(min=0)], 0).view(T_, k, d) * dy.double()[:, None]
+        check(dweights, h64(terms.sum(-1)), h64((d / 64 + 24) * U32 * terms.abs().sum(-1)), "dweights")
+
+
 def test_rows_beyond_32_bits():
     """Rows 2^26 elements apart: the last ones begin beyond 2^31 elements and 4 GiB."""
     say("[gpu case] rows beyond 4 GiB")
