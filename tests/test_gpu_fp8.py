@@ -5,7 +5,8 @@ import torch
 
 from activation_sparse_feedforward_amd import twell as T
 from _helpers import check_guards, guarded, say
-from _many_token import DT, E4M3, U32, capture, check, e4m3_nearest, e4m3_rows, e4m3_weights, h64, product_bound
+from _many_token import (DT, E4M3, U32, capture, check, e4m3_nearest, e4m3_rows, e4m3_scale, e4m3_weights, h64,
+                         product_bound)
 
 pytestmark = pytest.mark.gpu
 
@@ -58,6 +59,46 @@ def test_weights_there_and_back(E, N, K, dtype):
     assert np.array_equal(h64(_values(desc, p, torch.bfloat16)), want)  # four bits of a bf16's eight
     alone, _ = _packed(desc, w.view(-1), both=False)
     assert torch.equal(alone.codes, p.codes)
+
+
+def _scale_bytes(v, codes_rows, blocks):
+    """Scale bytes of one matrix's planes, [tiles of 16 rows][4 blocks][16 rows][4], from its values [rows, cols]."""
+    tiles, quads = -(-codes_rows // 16), -(-blocks // 4)
+    out = np.zeros((tiles, quads, 16, 4), np.uint8)
+    for a in range(0, codes_rows, 128):
+        for b in range(blocks):
+            most = np.abs(v[a:a + 128, 128 * b:128 * b + 128]).max()
+            out[a // 16:a // 16 + 8, b // 4, :, b % 4] = 127 + int(np.log2(e4m3_scale(most)))
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E,N,K", SHAPES + [(2, 500, 640), (1, 512, 512)])
+def test_planes_are_written_whole(E, N, K, dtype):
+    """Every byte of codes and scales comes from the weights: 128 x 128 weights share a scale, in all of their rows,
+    and blocks that only fill up the last four have zeros."""
+    say(f"[gpu case] fp8 planes {E} x {N} x {K} {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    w = torch.randn(E, N, K, generator=g, device="cuda") * torch.exp(4 * torch.randn(E, 1, K, generator=g, device="cuda"))
+    w = w.to(DT[dtype])
+    desc = T.Fp8Desc(E, N, K)
+    p, t = _packed(desc, w)  # over bytes of 0xA5
+    q, u = _planes(desc), _planes(desc.transposed)
+    for plane in (*q, *u):
+        plane.fill_(0x3C)
+    T.twell_fp8_weights_pack(desc, w, q, u)
+    alone = _planes(desc)
+    T.twell_fp8_weights_pack(desc, w, alone)
+    torch.cuda.synchronize()
+    check_guards(*q, *u, *alone)
+    assert torch.equal(p.codes, q.codes) and torch.equal(t.codes, u.codes) and torch.equal(p.codes, alone.codes)
+    wh = h64(w)
+    want = np.stack([_scale_bytes(m, N, -(-K // 128)) for m in wh])
+    want_t = np.stack([_scale_bytes(m.T, K, -(-N // 128)) for m in wh])
+    for got in (p, q, alone):
+        assert np.array_equal(got.scales.cpu().numpy(), want.reshape(-1))
+    for got in (t, u):
+        assert np.array_equal(got.scales.cpu().numpy(), want_t.reshape(-1))
 
 
 def test_rounding_of_every_value_and_border():
@@ -460,3 +501,37 @@ def test_most_rows(dtype):
             check(got[some], q @ m, product_bound(q, m.T, q @ m, dtype), "rows")
         ref, mag = dy.double().t() @ x.double(), dy.double().abs().t() @ x.double().abs()
         check(dw[0], h64(ref), (2 ** 20 + 8) * U32 * h64(mag), "dw")
+
+
+@pytest.mark.parametrize("T_,N,K,counts", [(16500, 2040, 1030, None), (33000, 1030, 1152, None),
+                                           (17000, 2100, 1100, [9000, 0, 7, 7900])])
+def test_results_past_the_caches(T_, N, K, counts):
+    """bf16 results of 64 MB and more, of 8 blocks of inputs and more, against 64 bits: first and last rows, the ends of
+    tiles and of experts, others at random; whole groups of 64 outputs and the part of one behind them."""
+    say(f"[gpu case] fp8 T={T_} N={N} K={K} {counts} past the caches")
+    assert T_ * N >= 1 << 25 and K > 7 * 128 and N % 64
+    g = torch.Generator(device="cuda").manual_seed(T_)
+    E = 1 if counts is None else len(counts)
+    desc = T.Fp8Desc(E, N, K)
+    w = torch.randn(E, N, K, generator=g, device="cuda") * K ** -0.5
+    p, _ = _packed(desc, w, both=False)
+    x = torch.randn(T_, K, generator=g, device="cuda") * torch.exp(2 * torch.randn(T_, 1, generator=g, device="cuda"))
+    x = x.bfloat16()
+    off = None if counts is None else _offsets(counts, T_)
+    y, ws = guarded((T_, N), torch.bfloat16), guarded((T.fp8_ws_bytes(desc, T_),), torch.uint8)
+    T.twell_fp8_linear_fwd(desc, p, x, y, ws, offsets=off)
+    torch.cuda.synchronize()
+    check_guards(y, ws)
+    ends = np.concatenate([[0], np.cumsum(counts if counts else [T_])])
+    assert bool((y[ends[-1]:].contiguous().view(torch.uint8) == 0xA5).all())
+    r = np.random.default_rng(T_)
+    for e in range(E):
+        a, b = int(ends[e]), int(ends[e + 1])
+        if a == b:
+            continue
+        rows = np.concatenate([np.arange(a, a + 20), np.arange(a + 120, a + 136), np.arange(b - 140, b),
+                               r.integers(a, b, 64)])
+        rows = np.unique(rows[(rows >= a) & (rows < b)])
+        q, wv = e4m3_rows(h64(x[rows])), e4m3_weights(h64(w[e]))
+        ref = q @ wv.T
+        check(y[rows], ref, product_bound(q, wv, ref, "bf16"), f"y of expert {e}")
