@@ -8,6 +8,13 @@ namespace {
 
 constexpr int kPackWaves = 4;
 
+// The scale of block b of `blocks` to a row's four; the last block's workgroup fills what is left of them with zeros.
+__device__ __forceinline__ void put_scale(uint8_t* four, uint32_t byte, int b, int blocks) {
+  four[b % 4] = static_cast<uint8_t>(byte);
+  if (b + 1 == blocks)
+    for (int i = b % 4 + 1; i < 4; ++i) four[i] = 0;
+}
+
 // One workgroup per 128 x 128 weights, which share a scale, so that the codes of
 // the transposed matrix are the same numbers.  Reading and writing bound it; the
 // transposed codes go through LDS byte by byte, a tenth of that time.  16 fp32
@@ -61,13 +68,13 @@ __global__ __launch_bounds__(kPackWaves* kWave) void f8_pack_kernel(F8PackArgs a
   if (threadIdx.x < 128) {
     const int tile = rb * 8 + threadIdx.x / 16;
     if (tile < a.tiles)
-      a.scales[((e * a.tiles + tile) * a.quads + cb / 4) * kF8Scales + (threadIdx.x % 16) * 4 + cb % 4] =
-          static_cast<uint8_t>(byte);
+      put_scale(a.scales + ((e * a.tiles + tile) * a.quads + cb / 4) * kF8Scales + (threadIdx.x % 16) * 4, byte, cb,
+                a.blocks);
   } else if (a.codes_t) {
     const int i = threadIdx.x - 128, tile = cb * 8 + i / 16;
     if (tile < a.tiles_t)
-      a.scales_t[((e * a.tiles_t + tile) * a.quads_t + rb / 4) * kF8Scales + (i % 16) * 4 + rb % 4] =
-          static_cast<uint8_t>(byte);
+      put_scale(a.scales_t + ((e * a.tiles_t + tile) * a.quads_t + rb / 4) * kF8Scales + (i % 16) * 4, byte, rb,
+                a.blocks_t);
   }
   if (!a.codes_t) return;
   __syncthreads();
