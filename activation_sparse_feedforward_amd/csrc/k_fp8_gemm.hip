@@ -548,9 +548,11 @@ hipError_t go_gemm(const F8GemmArgs& a, hipStream_t s) {
 // workgroup keep more of the weights on their way.
 template <class E>
 hipError_t go_few_rows(const F8GemmArgs& a, int64_t groups, hipStream_t s) {
-  if (groups < 256) return go_few<E, 1, 1, false, 16>(a, s);
-  if (groups == 256) return go_few<E, 1, 2, false, 8>(a, s);
-  if (groups <= 512) return go_few<E, 1, 4, false, 8>(a, s);  // one round, of half as many
+  // At most 256 workgroups, one for each CU, of the narrowest tiles that allow it (16 rows of 2048 inputs, us in tiles of
+  // 16 x 16, 16 x 32, 16 x 64: 4096 outputs 5.8, 6.3, 7.2; 5120: 9.0, 6.4, 7.2; 8192: 9.3, 6.8, 7.5; 8224: 12.1, 8.7, 7.5)
+  if (groups <= 128) return go_few<E, 1, 1, false, 16>(a, s);
+  if (groups <= 256) return go_few<E, 1, 2, false, 8>(a, s);
+  if (groups <= 512) return go_few<E, 1, 4, false, 8>(a, s);
   if constexpr (E::kBytes == 2) {  // 16 x 32 suits tiles of few rows; fp32's widening costs less in 16 x 64 everywhere
     if (a.T <= 16 * static_cast<int64_t>(a.experts) && groups <= 2048) return go_few<E, 1, 2, false, 4>(a, s);
   }

@@ -244,6 +244,17 @@ def test_each_kernel_of_the_products(T_, N, K, counts, dtype):
     _case(T_, N, K, dtype, counts, seed=T_)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T_,N,K,counts", [(3, 4096, 300, None), (3, 4097, 300, None), (3, 8192, 300, None),
+                                           (3, 8193, 300, None), (3, 16384, 300, None), (3, 16385, 300, None),
+                                           (40, 1360, 1200, None), (40, 1370, 1200, None), (6, 510, 2100, [2, 0, 1, 3]),
+                                           (6, 1030, 2100, [2, 0, 1, 3])])
+def test_borders_between_kernels_of_few_rows(T_, N, K, counts, dtype):
+    """On both sides of 128, 256 and 512 tiles of 16 rows x 32 outputs."""
+    say(f"[gpu case] fp8 product T={T_} N={N} K={K} {dtype} at a border")
+    _case(T_, N, K, dtype, counts, seed=N)
+
+
 def test_many_experts():
     say("[gpu case] fp8 1024 experts")
     r = np.random.default_rng(0)
