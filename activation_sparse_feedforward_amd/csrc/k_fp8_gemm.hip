@@ -528,21 +528,21 @@ hipError_t go_gemm(const F8GemmArgs& a, hipStream_t s) {
 //
 // Which kernel: by the sizes, fitted to 218 calls, each timed with every kernel (1 to
 // 32768 rows of 768 x 1024 to 11008 x 4096, 1 to 128 experts, both types): the one
-// taken is 2 % behind the fastest on average, up to a fifth in three cases.
-// Replayed, us, bf16:
-//                               8192 x 2048               64 experts of 1024 x 2048
+// taken is 3 % behind the fastest on average, by more than 10 % in 13 of them and by
+// 21 % at the most.  Replayed, us, bf16:
+//                               8192 x 2048                64 experts of 1024 x 2048
 //   rows                        1    32   64   256  1024  64    256   1024  4096  8192
 //   rounding on the way
-//     16 x 32, 8 waves          6.5  9.6  16.0 51.5 185   21.2  31.6  45.5  120   221
-//     16 x 64, 8 waves          6.5  7.6  12.6 43.0 165   21.6  32.4  42.9  106   192
-//     16 x 32, 4 waves          7.1  9.5  14.7 44.2 160   18.9  26.7  38.8  95.9  175
-//     16 x 64, 4 waves          7.6  8.8  10.5 34.9 130   20.0  27.7  35.5  81.2  145
+//     16 x 16, 16 waves         8.0  16.1 28.5 105  411   35.5  51.6  87.6  256   484
+//     16 x 32, 8 waves          6.4  9.4  15.4 50.3 184   21.0  31.5  45.2  121   223
+//     16 x 64, 8 waves          6.5  7.6  12.7 43.2 164   21.6  32.3  42.9  105   192
+//     16 x 32, 4 waves          7.0  9.3  14.4 43.7 160   19.0  26.8  38.7  96.0  175
+//     16 x 64, 4 waves          7.5  8.8  10.5 35.1 131   20.0  28.0  35.6  81.3  145
 //   codes from a launch of their own
-//     32 x 32, 4 waves          9.9  11.0 12.4 22.4 61.0  23.7  31.8  37.7  58.8  89.9
-//     64 x 64, 4 waves          12.8 14.0 14.2 18.2 44.3  28.9  37.5  40.1  52.2  74.0
-//     64 x 256, through LDS     17.6 18.9 20.2 20.6 29.4  30.9  36.4  39.9  46.5  67.6
-//     128 x 256, through LDS    19.2 20.7 21.8 24.1 28.9  30.1  39.1  42.8  52.6  59.4
-// (The last two before they stored whole lines, which takes 2 to 14 % off them.)
+//     32 x 32, 4 waves          9.8  10.9 12.5 22.5 61.0  23.4  31.8  37.7  58.9  89.9
+//     64 x 64, 4 waves          12.8 13.9 14.3 18.2 44.3  28.6  37.9  40.3  52.6  74.0
+//     64 x 256, through LDS     17.3 18.7 19.4 19.9 28.3  30.8  36.5  39.4  45.9  66.3
+//     128 x 256, through LDS    19.1 20.3 20.8 22.4 28.1  30.2  39.2  42.2  49.9  56.9
 // With many workgroups, small ones with few waves follow each other without a gap
 // (the waves of one wait for each other at its end); with few, more waves a
 // workgroup keep more of the weights on their way.
@@ -589,8 +589,12 @@ hipError_t launch_f8_product(const F8GemmArgs& a, const F8RowsArgs& rows, int dt
     return few64 < few32 && row_tiles(64) * quads >= 256 ? go_few<EBf16, 4, 4, true, 4>(a, s)
                                                          : go_few<EBf16, 2, 2, true, 4>(a, s);
   }
-  // tiles of 128 rows that an expert fills half cost as much as full ones
-  if (row_work(128) * strips <= (a.offsets ? 256 : 159)) return go_gemm<4, false>(a, s);
+  // While there are few, tiles of 64 rows: up to half as many of 128 rows as CUs they halve each CU's work; past that
+  // some CUs have two, as much as one of 128 rows.  One matrix, us with 64 and 128 rows, by tiles of 128: 2048 inputs 128
+  // 22.8, 25.5; 144 24.8, 25.4; 160 25.6, 25.7; 192 26.7, 27.8; 224 29.2, 28.7; 272 41.1, 39.3; 4096 inputs 144 36.6,
+  // 37.9; 160 37.9, 37.5; 192 39.7, 38.0; 256 43.9, 42.6.  Of experts the last tiles cost as much as full ones: 16 of 2048
+  // outputs and inputs 128 31.5, 32.6; 192 35.8, 34.2; 256 38.5, 45.4; 320 56.3, 48.6; 64 of 1024: 256 46.3, 50.1.
+  if (row_work(128) * strips <= (a.offsets ? 256 : 160)) return go_gemm<4, false>(a, s);
   // Results of 64 MB and more, unless there is little to read for them, go past the caches, which keep the operands:
   // 16384 x 8192 of 2048 and 8192 inputs 260 -> 248 and 903 -> 868 us, but of 512 inputs 107 -> 111.
   return a.T * a.N >= int64_t(1) << 25 && blocks >= 8 ? go_gemm<8, true>(a, s) : go_gemm<8, false>(a, s);

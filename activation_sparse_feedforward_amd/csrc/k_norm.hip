@@ -280,8 +280,10 @@ hipError_t go_bwd(const NormArgs& a, hipStream_t s) {
 
 // Workgroups of the backward kernel.  Each writes 2 d sums, which norm_sum_kernel
 // reads: more of them cost more there, fewer have fewer loads under way.  (16384
-// rows of 2048 in bf16, 4 waves a row: 48 us with 256, 37.4 with 512, 38.6 with 1024;
-// of 4096, 8 waves: 79 with 256, 81 with 512; 2000 rows of 2048: 12.9, 13.9, 18.2.)
+// rows in bf16 with 256, 512, 1024 and 2048, us: 600 wide, 2 waves a row, 79, 46, 29.6,
+// 26; 1024 wide 44, 31, 25, 28.5; 1500 wide, 3 waves, 114, 65, 44, 49; 2048 wide, 4 waves,
+// 48.6, 37.1, 38.9, 46; of 4096, 8 waves: 79 with 256, 81 with 512.  2000 rows of 2048: 12.8
+// with 256, 14.8 with 512.)
 int norm_blocks(int64_t T, int d, int dtype) {
   const int waves = (d + (dtype == 1 ? 511 : 255)) / (dtype == 1 ? 512 : 256);  // of a row, with one piece a lane
   const int64_t most = waves == 1 ? 2048 : waves <= 4 ? 1024 : 256, wanted = waves <= 4 ? (T + 3) / 4 : (T + 1) / 2;

@@ -113,8 +113,12 @@ struct GradTile<EF32, COLS> {
 };
 
 // fp32, and bf16 rows of less than 16 bytes: a tile of 32 F x 32 F of dW per
-// workgroup, 16 F x 16 F a wave.  fp32 is bound by its matrix instructions, at a
-// sixteenth of bf16's rate: 777 rows of 5 experts of 1001 x 707 take 20 to 22 us.
+// workgroup, 16 F x 16 F a wave.  Many rows of fp32 are bound by its matrix
+// instructions, at a sixteenth of bf16's rate (16384 rows, 2048 x 2048: 1143 us, 120
+// TFLOP/s, where a library's product reaches 153; 8192 rows of 8 experts of 1024 x 2048:
+// 308 us, 111), few by their starts: 777 rows of 5 experts of 1001 x 707 take 20 to 22
+// us, 50 TFLOP/s, 1024 x 704 in whole tiles 20; an expert is some five steps, each
+// fetched one ahead, behind the offsets.
 template <class E, int F>
 __global__ __launch_bounds__(kGradWaves* kWave) void wgrad_kernel(WgradArgs a) {
   using S = typename E::storage;
