@@ -137,9 +137,9 @@ __global__ __launch_bounds__(kPackWaves* kWave) void f8_unpack_kernel(F8PackArgs
 }
 
 // Rows to codes: a wave has four blocks of 16 rows, whose scales make whole words.
-// Each load takes 64 bytes of 16 rows each, half lines in bf16: 16384 rows of 2048 in
-// bf16 take 31 us (3.3 TB/s, rows from memory to codes that stay in the caches, where a
-// copy reaches 4.9), of 1024 12 us.
+// 16384 rows of 2048 in bf16 take 31 us from memory (3.3 TB/s, where a copy reaches
+// 4.9: a load takes 64 bytes of each of 16 rows, half lines), 20 from the caches; of
+// 1024 12 us.
 template <class E>
 __global__ __launch_bounds__(kPackWaves* kWave) void f8_rows_kernel(F8RowsArgs a) {
   using S = typename E::storage;
