@@ -348,8 +348,8 @@ __global__ __launch_bounds__(256) void f8_gemm_exact_kernel(F8GemmArgs a) {
 #pragma unroll
       for (int j = 0; j < F; ++j) sx[j] >>= 8;
     }
-    // the reads of the stage that is filled next were used before this barrier
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    // this stage is there, and all waves' reads of the one that is filled next have come back
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (kb + 1 < a.blocks) fetch(kb + 1);
     Bf16Frag xb[F];
 #pragma unroll
